@@ -68,7 +68,9 @@ typedef enum {
   SQ_ERR_TIMEOUT = -4,     /* a bounded device-side wait gave up (see sq_sync_status) */
   SQ_ERR_WORKSPACE = -5,   /* ws NULL or smaller than sq_workspace_size() */
   SQ_ERR_UNSUPPORTED = -6, /* no sm_100a device, or the library was built without it */
-  SQ_ERR_BOUNDS = -7       /* a device-side bounds guard fired (libsq_debug.so only; see sq_sync_status) */
+  SQ_ERR_BOUNDS = -7       /* an index read from device memory (a slot, position, page or length of the paged
+                              cache calls) was out of range and its access was skipped, or a device-side bounds
+                              guard fired (libsq_debug.so only); reported by sq_sync_status */
 } sq_status;
 
 typedef enum { SQ_PER_TENSOR = 0, SQ_PER_CHANNEL = 1 } sq_gran;
@@ -81,8 +83,11 @@ typedef enum {
   SQ_OP_LLMINT8 = 3,           /* also llmint8_decomposed_linear_ex */
   SQ_OP_QUANT_ACT_PER_TENSOR = 4,
   SQ_OP_MEAN_STD_THRESHOLD = 5,
-  SQ_OP_ABS_PERCENTILE = 6
+  SQ_OP_ABS_PERCENTILE = 6,
+  SQ_OP_PAGED_ATTENTION = 7 /* sized by (batch, query heads, head dimension) */
 } sq_op;
+
+typedef enum { SQ_KV_BF16 = 0, SQ_KV_INT8 = 1 } sq_kv_type;
 
 /*
  * Per-input-channel absolute maximum of the activations (calibration statistic).
@@ -336,6 +341,139 @@ SQ_API sq_status sq_quant_act_per_token_asym(const void* X_bf16, int64_t M, int6
  */
 SQ_API sq_status sq_weight_row_sums(const int8_t* Wq, int64_t N, int64_t K, int32_t* rowsum, sq_stream_t stream);
 
+/* ============================================================================ 4-bit weights
+ * Weight-only quantization to 4 bits with one scale per group of consecutive input channels
+ * ([SQ] §2.4 and §6.1 name W4A16 beside W8A8 for the decoding of a few tokens, which only
+ * streams the weight): half the bytes of the int8 weight, activations stay bf16.
+ *
+ * A weight [N, K] with groups of `group` (32, 64 or 128) input channels is held as
+ *   Wp      the 4-bit codes 0..15, sq_int4_weight_bytes(N, K) bytes, in the tiled layout below;
+ *   w_scale bf16 [ceil(K / group), N];
+ *   w_zero  uint8 [ceil(K / group), N], zero points 0..15, or NULL (every zero point is 8),
+ * and stands for the values (code - zero) * scale. The last group is short when K is not a
+ * multiple of `group`. N must be a multiple of 8, K one of 16.
+ * Layout of Wp: tiles of 16 rows x 128 columns, 1024 bytes each, [ceil(N/16)][ceil(K/128)];
+ * positions past N or K hold code 8. Within a tile the code of row r, column c is in byte
+ *   (4 r + (c/2) % 4) * 16 + (c/32) * 4 + (c%2) * 2 + (c/16) % 2      (integer divisions)
+ * in the low nibble if (c/8) % 2 == 0 and the high nibble if it is 1: sixteen bytes of one
+ * thread are its operand fragments of eight 16x8x16 matrix instructions.
+ */
+
+/* Bytes of the packed codes of an [N, K] weight (0 if a size is not positive). */
+SQ_API size_t sq_int4_weight_bytes(int64_t N, int64_t K);
+
+/*
+ * Group quantization of a weight to 4 bits, smoothing included as in sq_smooth_quant_weight:
+ *   w'[n,k] = W[n,k] * s[k]                     (fp32; s == NULL means 1)
+ *   w_zero == NULL: a = max |w'| of the group,   e = bf16_rne(a / 7), z = 8
+ *   w_zero given  : lo = min(0, min w'), hi = max(0, max w') of the group,
+ *                   e = bf16_rne((hi - lo) / 15), z = clamp(rne(-lo * r), 0, 15)
+ *   r = min(1 / e, FLT_MAX) (0 if e == 0),  code = clamp(rne(w' * r) + z, 0, 15)
+ * (fp32, IEEE divisions, round half to even). The codes are taken against the rounded scale,
+ * so rounding it to bf16 costs no accuracy of its own beyond a grid 2^-9 wider or narrower.
+ * W: bf16 [N, K], ldw. s: fp32 [K] or NULL. Wp, w_scale, w_zero (or NULL): written whole.
+ */
+SQ_API sq_status sq_quant_weight_int4(const void* W_bf16, int64_t N, int64_t K, int64_t ldw, const float* s,
+                                      int64_t group, uint8_t* Wp, void* w_scale_bf16, uint8_t* w_zero,
+                                      sq_stream_t stream);
+
+/*
+ * The values a 4-bit weight stands for, out[n,k] = bf16_rne((code - zero) * scale): for
+ * products of many tokens, and to inspect a quantization. out: bf16 [N, K] dense.
+ */
+SQ_API sq_status sq_dequant_weight_int4(const uint8_t* Wp, const void* w_scale_bf16, const uint8_t* w_zero,
+                                        int64_t group, int64_t N, int64_t K, void* out_bf16, sq_stream_t stream);
+
+/*
+ * Linear layer of a few tokens with a 4-bit weight:
+ *   Y[m,n] = bf16_rne( sum_k X[m,k] * (code[n,k] - zero[g,n]) * scale[g,n] + bias[n] ),  g = k / group
+ * Products are exact in fp32, sums are fp32 (group by group, then over the groups, in an
+ * order that depends on the shapes only: the same inputs give the same bits).
+ * X: bf16 [M, K], ldx, 1 <= M <= 64 (more tokens: sq_dequant_weight_int4 or the int8 GEMM).
+ * For a weight quantized with smoothing factors s, X must already be divided by s (folded
+ * into what produces it, [SQ] §4.2). bias: bf16 [N] or NULL. Y: bf16 [M, N].
+ */
+SQ_API sq_status sq_int4_linear(const void* X_bf16, int64_t M, int64_t K, int64_t ldx, const uint8_t* Wp,
+                                const void* w_scale_bf16, const uint8_t* w_zero, int64_t group,
+                                const void* bias_bf16, void* Y_bf16, int64_t N, sq_stream_t stream);
+
+/* ============================================================================ paged key-value cache
+ * The keys and values of the sequences being decoded, in pages of page_size tokens, as bf16
+ * or as int8 codes with one fp32 scale per token and head ([SQ] §5.2 KV-cache INT8, per-token
+ * and per-head scales; symmetric absmax quantization as for activations). The descriptor is
+ * read during the call only; its tensors are device memory of the caller:
+ *   k, v: [num_pages, heads, page_size, head_dim], dense but for the page stride;
+ *   k_scale, v_scale: fp32 [num_pages, heads, page_size], dense but for the scale page stride
+ *   (SQ_KV_INT8; NULL for SQ_KV_BF16). k and v share one page stride, so do the scales.
+ * The slot of a token is page * page_size + its place in the page.
+ */
+typedef struct {
+  int32_t type;              /* sq_kv_type */
+  int32_t reserved;          /* 0 */
+  void* k;                   /* 16-byte aligned, as all of them */
+  void* v;
+  float* k_scale;
+  float* v_scale;
+  int64_t num_pages;         /* num_pages * page_size < 2^31 */
+  int64_t heads;             /* key heads, 1..1024 */
+  int64_t page_size;         /* tokens, a power of two in [1, 1024] */
+  int64_t head_dim;          /* 64, 96, 128 or 256 */
+  int64_t page_stride;       /* elements from a page of k (v) to the next, >= heads * page_size * head_dim,
+                                a multiple of 16 */
+  int64_t scale_page_stride; /* elements from a page of k_scale (v_scale) to the next, >= heads * page_size */
+} sq_kv_cache;
+
+/*
+ * Position rotation of the new tokens' queries and keys, and their keys and values appended to
+ * the cache, in one pass. For token t at p = positions[t], each head row x of q and k becomes
+ *   half-split (interleaved == 0): pairs (i, i + rot_dim/2);  interleaved: pairs (2i, 2i + 1)
+ *   y_a = x_a * cos[p,i] - x_b * sin[p,i],   y_b = x_b * cos[p,i] + x_a * sin[p,i]
+ * (fp32, every operation rounded, no contraction), i < rot_dim / 2; elements from rot_dim on
+ * stay. Queries are written to q_out, keys and values to slot slots[t] of the cache: as bf16
+ * (rounded once), or as int8 from the fp32 values of one head's row:
+ *   a = max |y|, scale = a / 127, code = clamp(rne(y * min(127 / a, FLT_MAX)), -128, 127)
+ * (IEEE divisions; a == 0 gives codes and scale 0).
+ * q: bf16 [T, H, head_dim], k, v: bf16 [T, heads, head_dim]: token strides ldq, ldk, ldv in
+ * elements (multiples of 8, at least a token's row), heads and elements dense. q and q_out may
+ * both be NULL (H = 0). q_out: bf16 [T, H, head_dim] dense; it may be q itself when ldq is
+ * H * head_dim, and must not overlap the inputs otherwise.
+ * cos, sin: fp32 [max_pos, rot_dim / 2] dense; rot_dim a multiple of 16 up to head_dim, or 0
+ * (no rotation; cos, sin and positions may then be NULL).
+ * positions, slots: int32 [T]. A negative slot marks a padding token: nothing is written for
+ * it, in q_out neither. A slot or position past the end writes nothing for its token and
+ * records SQ_ERR_BOUNDS (see sq_sync_status). The slots of one call must be distinct.
+ */
+SQ_API sq_status sq_rope_kv_append(const void* q_bf16, int64_t ldq, const void* k_bf16, int64_t ldk,
+                                   const void* v_bf16, int64_t ldv, int64_t T, int64_t H, const float* cos,
+                                   const float* sin, int64_t max_pos, int64_t rot_dim, int interleaved,
+                                   const int32_t* positions, const int32_t* slots, const sq_kv_cache* cache,
+                                   void* q_out_bf16, sq_stream_t stream);
+
+/*
+ * Attention of one new token per sequence over the paged cache. Sequence b has seq_lens[b]
+ * tokens (the new one included), token t in page block_table[b][t / page_size]; query head h
+ * reads key head h / (H / heads):
+ *   out[b,h] = sum_t p_t v_t,  p = softmax_t( scale * (q[b,h] . k_t) ),
+ *   over max(0, seq_lens[b] - window) <= t < seq_lens[b]   (window == 0: the whole sequence)
+ *   lse[b,h] = log sum_t exp( scale * (q[b,h] . k_t) )
+ * with fp32 scores, softmax statistics and sums, one rounding of out to bf16. A sequence of
+ * length 0 gives out 0 and lse -inf. Cache contents behind a sequence's last token (NaN
+ * included) are never used. The work is split over the sequences' lengths and joined in a
+ * fixed order: the same inputs give the same bits.
+ * q: bf16 [B, H, head_dim], sequence stride ldq (a multiple of 8). H a multiple of the cache's
+ * heads. block_table: int32 [B, max_pages], row stride ld_table. seq_lens: int32 [B].
+ * out: bf16 [B, H, head_dim] dense. lse: fp32 [B, H] or NULL. 1 <= B <= 65535.
+ * A page index out of range hides its tokens, a negative length counts as 0 and one past
+ * max_pages * page_size as that; each records SQ_ERR_BOUNDS (see sq_sync_status).
+ * ws: sq_workspace_size(SQ_OP_PAGED_ATTENTION, B, H, head_dim) bytes, 16-byte aligned,
+ * zero-filled before its first use; every completed call leaves its counters at zero again.
+ * Calls that share one ws must not overlap on the GPU.
+ */
+SQ_API sq_status sq_paged_attention(const void* q_bf16, int64_t ldq, int64_t B, int64_t H, const sq_kv_cache* cache,
+                                    const int32_t* block_table, int64_t ld_table, int64_t max_pages,
+                                    const int32_t* seq_lens, int64_t window, float scale, void* out_bf16, float* lse,
+                                    void* ws, size_t ws_bytes, sq_stream_t stream);
+
 /* Bytes of scratch an operation needs for the given shape (0 if none). Returns 0 for an
  * unknown op; never fails otherwise. */
 SQ_API size_t sq_workspace_size(int op, int64_t M, int64_t N, int64_t K);
@@ -346,7 +484,8 @@ SQ_API const char* sq_last_error(void);
 
 /* Synchronises `stream`, then reads and clears the current device's error word, which
  * kernels set when a bounded wait gives up (a device-side stall or lost arrival) instead
- * of spinning forever, and, in the debug build libsq_debug.so (same ABI, kernels compiled
+ * of spinning forever, when an index that a paged-cache call read from device memory was out
+ * of range (its access was skipped), and, in the debug build libsq_debug.so (same ABI, kernels compiled
  * with device-side bounds guards that skip and record an out-of-range access), when a guard
  * fires. Returns SQ_OK, SQ_ERR_TIMEOUT, SQ_ERR_BOUNDS or SQ_ERR_CUDA. */
 SQ_API sq_status sq_sync_status(sq_stream_t stream);

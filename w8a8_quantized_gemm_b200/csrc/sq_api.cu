@@ -84,6 +84,78 @@ sq_status check_vec(const char* fn, const char* what, const void* p, bool requir
   return SQ_OK;
 }
 
+sq_status check_int4(const char* fn, const void* Wp, const void* w_scale, const void* w_zero, int64_t group,
+                     int64_t N) {
+  sq_status st;
+  if (group != 32 && group != 64 && group != 128)
+    return fail(SQ_ERR_INVALID, "%s: group=%lld must be 32, 64 or 128", fn, static_cast<long long>(group));
+  if (N % 8 != 0) return fail(SQ_ERR_INVALID, "%s: N=%lld must be a multiple of 8", fn, static_cast<long long>(N));
+  if ((st = check_vec(fn, "Wp", Wp, true)) != SQ_OK) return st;
+  if ((st = check_vec(fn, "w_scale", w_scale, true)) != SQ_OK) return st;
+  return check_vec(fn, "w_zero", w_zero, false);
+}
+
+constexpr int64_t kMaxHeads = 1024;
+
+sq_status check_heads(const char* fn, const char* what, const void* p, int64_t rows, int64_t heads, int64_t D,
+                      int64_t ld) {
+  if (rows < 1 || rows > kMaxRows)
+    return fail(SQ_ERR_INVALID, "%s: %lld rows of %s out of [1, 2^31-1]", fn, static_cast<long long>(rows), what);
+  if (ld < heads * D) return fail(SQ_ERR_INVALID, "%s: stride %lld of %s below a row", fn, static_cast<long long>(ld), what);
+  if (ld % 8 != 0) return fail(SQ_ERR_ALIGN, "%s: stride of %s must be a multiple of 8", fn, what);
+  return check_vec(fn, what, p, true);
+}
+
+sq_status check_index(const char* fn, const char* what, const int32_t* p) {
+  if (p == nullptr) return fail(SQ_ERR_INVALID, "%s: %s is NULL", fn, what);
+  if (reinterpret_cast<uintptr_t>(p) & 3u) return fail(SQ_ERR_ALIGN, "%s: %s not 4-byte aligned", fn, what);
+  return SQ_OK;
+}
+
+sq_status check_cache(const char* fn, const sq_kv_cache* c, sq::KvView* out) {
+  if (c == nullptr) return fail(SQ_ERR_INVALID, "%s: cache is NULL", fn);
+  if ((c->type != SQ_KV_BF16 && c->type != SQ_KV_INT8) || c->reserved != 0)
+    return fail(SQ_ERR_INVALID, "%s: bad cache type", fn);
+  const bool int8 = c->type == SQ_KV_INT8;
+  sq_status st;
+  if ((st = check_vec(fn, "cache k", c->k, true)) != SQ_OK) return st;
+  if ((st = check_vec(fn, "cache v", c->v, true)) != SQ_OK) return st;
+  if ((st = check_vec(fn, "cache k_scale", c->k_scale, int8)) != SQ_OK) return st;
+  if ((st = check_vec(fn, "cache v_scale", c->v_scale, int8)) != SQ_OK) return st;
+  if (!int8 && (c->k_scale != nullptr || c->v_scale != nullptr))
+    return fail(SQ_ERR_INVALID, "%s: a bf16 cache has no scales", fn);
+  if (c->head_dim != 64 && c->head_dim != 96 && c->head_dim != 128 && c->head_dim != 256)
+    return fail(SQ_ERR_INVALID, "%s: head_dim=%lld must be 64, 96, 128 or 256", fn, static_cast<long long>(c->head_dim));
+  if (c->heads < 1 || c->heads > kMaxHeads)
+    return fail(SQ_ERR_INVALID, "%s: cache heads=%lld out of [1, %lld]", fn, static_cast<long long>(c->heads),
+                static_cast<long long>(kMaxHeads));
+  if (c->page_size < 1 || c->page_size > 1024 || (c->page_size & (c->page_size - 1)) != 0)
+    return fail(SQ_ERR_INVALID, "%s: page_size=%lld must be a power of two in [1, 1024]", fn,
+                static_cast<long long>(c->page_size));
+  if (c->num_pages < 1 || c->num_pages > kMaxRows / c->page_size)
+    return fail(SQ_ERR_INVALID, "%s: num_pages=%lld: num_pages * page_size must be in [1, 2^31-1]", fn,
+                static_cast<long long>(c->num_pages));
+  const int64_t row = c->heads * c->page_size;
+  if (c->page_stride < row * c->head_dim || c->page_stride > (int64_t(1) << 40))
+    return fail(SQ_ERR_INVALID, "%s: page_stride below a page", fn);
+  if (c->page_stride % 16 != 0) return fail(SQ_ERR_ALIGN, "%s: page_stride must be a multiple of 16", fn);
+  if (int8 && (c->scale_page_stride < row || c->scale_page_stride > (int64_t(1) << 40)))
+    return fail(SQ_ERR_INVALID, "%s: scale_page_stride below a page", fn);
+  out->k = c->k;
+  out->v = c->v;
+  out->k_scale = c->k_scale;
+  out->v_scale = c->v_scale;
+  out->num_pages = c->num_pages;
+  out->page_stride = c->page_stride;
+  out->scale_page_stride = int8 ? c->scale_page_stride : 0;
+  out->heads = static_cast<int>(c->heads);
+  out->head_dim = static_cast<int>(c->head_dim);
+  out->page_shift = 0;
+  while ((int64_t(1) << out->page_shift) < c->page_size) ++out->page_shift;
+  out->int8 = int8;
+  return SQ_OK;
+}
+
 constexpr size_t kAlign = 256;
 size_t up(size_t x) { return (x + kAlign - 1) & ~(kAlign - 1); }
 
@@ -492,6 +564,159 @@ sq_status sq_weight_row_sums(const int8_t* Wq, int64_t N, int64_t K, int32_t* ro
   return e == cudaSuccess ? SQ_OK : cuda_fail(e, fn);
 }
 
+size_t sq_int4_weight_bytes(int64_t N, int64_t K) { return N < 1 || K < 1 ? 0 : sq::int4_weight_bytes(N, K); }
+
+sq_status sq_quant_weight_int4(const void* W_bf16, int64_t N, int64_t K, int64_t ldw, const float* s, int64_t group,
+                               uint8_t* Wp, void* w_scale_bf16, uint8_t* w_zero, sq_stream_t stream) {
+  const char* fn = "sq_quant_weight_int4";
+  sq_status st = check_rows(fn, "W", W_bf16, N, K, ldw);
+  if (st != SQ_OK) return st;
+  if ((st = check_int4(fn, Wp, w_scale_bf16, w_zero, group, N)) != SQ_OK) return st;
+  if ((st = check_vec(fn, "s", s, false)) != SQ_OK) return st;
+  cudaError_t e = sq::launch_int4_quant(static_cast<const uint16_t*>(W_bf16), N, K, ldw, s, static_cast<int>(group),
+                                        Wp, static_cast<uint16_t*>(w_scale_bf16), w_zero,
+                                        reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? SQ_OK : cuda_fail(e, fn);
+}
+
+sq_status sq_dequant_weight_int4(const uint8_t* Wp, const void* w_scale_bf16, const uint8_t* w_zero, int64_t group,
+                                 int64_t N, int64_t K, void* out_bf16, sq_stream_t stream) {
+  const char* fn = "sq_dequant_weight_int4";
+  sq_status st = check_rows(fn, "out", out_bf16, N, K, K);
+  if (st != SQ_OK) return st;
+  if ((st = check_int4(fn, Wp, w_scale_bf16, w_zero, group, N)) != SQ_OK) return st;
+  cudaError_t e = sq::launch_int4_dequant(Wp, static_cast<const uint16_t*>(w_scale_bf16), w_zero,
+                                          static_cast<int>(group), N, K, static_cast<uint16_t*>(out_bf16),
+                                          reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? SQ_OK : cuda_fail(e, fn);
+}
+
+sq_status sq_int4_linear(const void* X_bf16, int64_t M, int64_t K, int64_t ldx, const uint8_t* Wp,
+                         const void* w_scale_bf16, const uint8_t* w_zero, int64_t group, const void* bias_bf16,
+                         void* Y_bf16, int64_t N, sq_stream_t stream) {
+  const char* fn = "sq_int4_linear";
+  sq_status st = check_rows(fn, "X", X_bf16, M, K, ldx);
+  if (st != SQ_OK) return st;
+  if (M > 64) return fail(SQ_ERR_INVALID, "%s: M=%lld above 64", fn, static_cast<long long>(M));
+  if (N < 1 || N > kMaxRows) return fail(SQ_ERR_INVALID, "%s: N=%lld out of [1, 2^31-1]", fn, static_cast<long long>(N));
+  if ((st = check_int4(fn, Wp, w_scale_bf16, w_zero, group, N)) != SQ_OK) return st;
+  if ((st = check_vec(fn, "bias", bias_bf16, false)) != SQ_OK) return st;
+  if ((st = check_vec(fn, "Y", Y_bf16, true)) != SQ_OK) return st;
+  sq::Int4LinearArgs a;
+  a.X = static_cast<const uint16_t*>(X_bf16);
+  a.M = M;
+  a.N = N;
+  a.K = K;
+  a.ldx = ldx;
+  a.Wp = Wp;
+  a.scale = static_cast<const uint16_t*>(w_scale_bf16);
+  a.zero = w_zero;
+  a.group = static_cast<int>(group);
+  a.bias = static_cast<const uint16_t*>(bias_bf16);
+  a.Y = static_cast<uint16_t*>(Y_bf16);
+  cudaError_t e = sq::launch_int4_linear(a, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? SQ_OK : cuda_fail(e, fn);
+}
+
+sq_status sq_rope_kv_append(const void* q_bf16, int64_t ldq, const void* k_bf16, int64_t ldk, const void* v_bf16,
+                            int64_t ldv, int64_t T, int64_t H, const float* cos, const float* sin, int64_t max_pos,
+                            int64_t rot_dim, int interleaved, const int32_t* positions, const int32_t* slots,
+                            const sq_kv_cache* cache, void* q_out_bf16, sq_stream_t stream) {
+  const char* fn = "sq_rope_kv_append";
+  sq::RopeAppendArgs a;
+  sq_status st = check_cache(fn, cache, &a.cache);
+  if (st != SQ_OK) return st;
+  const int64_t D = cache->head_dim;
+  if ((q_bf16 == nullptr) != (q_out_bf16 == nullptr) || (q_bf16 == nullptr) != (H == 0))
+    return fail(SQ_ERR_INVALID, "%s: q and q_out must both be given with H >= 1, or be NULL with H = 0", fn);
+  if (H < 0 || H > kMaxHeads) return fail(SQ_ERR_INVALID, "%s: H=%lld out of [0, %lld]", fn, static_cast<long long>(H),
+                                          static_cast<long long>(kMaxHeads));
+  if (H > 0 && (st = check_heads(fn, "q", q_bf16, T, H, D, ldq)) != SQ_OK) return st;
+  if ((st = check_heads(fn, "k", k_bf16, T, cache->heads, D, ldk)) != SQ_OK) return st;
+  if ((st = check_heads(fn, "v", v_bf16, T, cache->heads, D, ldv)) != SQ_OK) return st;
+  if ((st = check_vec(fn, "q_out", q_out_bf16, false)) != SQ_OK) return st;
+  if (H > 0 && q_out_bf16 == q_bf16 && ldq != H * D)
+    return fail(SQ_ERR_INVALID, "%s: q_out may be q only when q is dense", fn);
+  if (rot_dim < 0 || rot_dim > D || rot_dim % 16 != 0)
+    return fail(SQ_ERR_INVALID, "%s: rot_dim=%lld must be a multiple of 16 in [0, head_dim]", fn,
+                static_cast<long long>(rot_dim));
+  if (rot_dim > 0) {
+    if ((st = check_vec(fn, "cos", cos, true)) != SQ_OK) return st;
+    if ((st = check_vec(fn, "sin", sin, true)) != SQ_OK) return st;
+    if ((st = check_index(fn, "positions", positions)) != SQ_OK) return st;
+    if (max_pos < 1) return fail(SQ_ERR_INVALID, "%s: max_pos must be positive", fn);
+  }
+  if ((st = check_index(fn, "slots", slots)) != SQ_OK) return st;
+  a.q = static_cast<const uint16_t*>(q_bf16);
+  a.k = static_cast<const uint16_t*>(k_bf16);
+  a.v = static_cast<const uint16_t*>(v_bf16);
+  a.ldq = ldq;
+  a.ldk = ldk;
+  a.ldv = ldv;
+  a.T = T;
+  a.H = static_cast<int>(H);
+  a.cos_t = cos;
+  a.sin_t = sin;
+  a.max_pos = max_pos;
+  a.rot = static_cast<int>(rot_dim);
+  a.interleaved = interleaved != 0;
+  a.positions = positions;
+  a.slots = slots;
+  a.q_out = static_cast<uint16_t*>(q_out_bf16);
+  a.status = sq::device_status_word();
+  if (a.status == nullptr) return fail(SQ_ERR_CUDA, "%s: device status word not found", fn);
+  cudaError_t e = sq::launch_rope_kv_append(a, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? SQ_OK : cuda_fail(e, fn);
+}
+
+sq_status sq_paged_attention(const void* q_bf16, int64_t ldq, int64_t B, int64_t H, const sq_kv_cache* cache,
+                             const int32_t* block_table, int64_t ld_table, int64_t max_pages, const int32_t* seq_lens,
+                             int64_t window, float scale, void* out_bf16, float* lse, void* ws, size_t ws_bytes,
+                             sq_stream_t stream) {
+  const char* fn = "sq_paged_attention";
+  sq::PagedAttentionArgs a;
+  sq_status st = check_cache(fn, cache, &a.cache);
+  if (st != SQ_OK) return st;
+  const int64_t D = cache->head_dim;
+  if (B < 1 || B > 65535) return fail(SQ_ERR_INVALID, "%s: B=%lld out of [1, 65535]", fn, static_cast<long long>(B));
+  if (H < 1 || H > kMaxHeads || H % cache->heads != 0)
+    return fail(SQ_ERR_INVALID, "%s: H=%lld must be a multiple of the cache's heads up to %lld", fn,
+                static_cast<long long>(H), static_cast<long long>(kMaxHeads));
+  if ((st = check_heads(fn, "q", q_bf16, B, H, D, ldq)) != SQ_OK) return st;
+  if ((st = check_vec(fn, "out", out_bf16, true)) != SQ_OK) return st;
+  if (lse != nullptr && (reinterpret_cast<uintptr_t>(lse) & 3u)) return fail(SQ_ERR_ALIGN, "%s: lse not aligned", fn);
+  if ((st = check_index(fn, "block_table", block_table)) != SQ_OK) return st;
+  if ((st = check_index(fn, "seq_lens", seq_lens)) != SQ_OK) return st;
+  if (max_pages < 1 || max_pages > kMaxRows || ld_table < max_pages)
+    return fail(SQ_ERR_INVALID, "%s: max_pages=%lld, row stride %lld", fn, static_cast<long long>(max_pages),
+                static_cast<long long>(ld_table));
+  if (window < 0) return fail(SQ_ERR_INVALID, "%s: window must not be negative", fn);
+  if (!(scale == scale) || scale == INFINITY || scale == -INFINITY)
+    return fail(SQ_ERR_INVALID, "%s: scale must be finite", fn);
+  const size_t need = sq_workspace_size(SQ_OP_PAGED_ATTENTION, B, H, D);
+  if (need > 0 && (ws == nullptr || ws_bytes < need))
+    return fail(SQ_ERR_WORKSPACE, "%s: needs %zu workspace bytes, got %zu", fn, need,
+                ws == nullptr ? size_t(0) : ws_bytes);
+  if (need > 0 && !aligned16(ws)) return fail(SQ_ERR_ALIGN, "%s: ws not 16-byte aligned", fn);
+  a.q = static_cast<const uint16_t*>(q_bf16);
+  a.ldq = ldq;
+  a.B = B;
+  a.H = H;
+  a.table = block_table;
+  a.ld_table = ld_table;
+  a.max_pages = max_pages;
+  a.seq_lens = seq_lens;
+  a.window = window;
+  a.scale = scale;
+  a.out = static_cast<uint16_t*>(out_bf16);
+  a.lse = lse;
+  a.ws = ws;
+  a.status = sq::device_status_word();
+  if (a.status == nullptr) return fail(SQ_ERR_CUDA, "%s: device status word not found", fn);
+  cudaError_t e = sq::launch_paged_attention(a, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? SQ_OK : cuda_fail(e, fn);
+}
+
 size_t sq_workspace_size(int op, int64_t M, int64_t N, int64_t K) {
   switch (op) {
     case SQ_OP_SMOOTH_QUANT_WEIGHT:
@@ -506,6 +731,8 @@ size_t sq_workspace_size(int op, int64_t M, int64_t N, int64_t K) {
       return M < 1 ? 0 : sq::mean_std_workspace_bytes(M);
     case SQ_OP_ABS_PERCENTILE:
       return sq::abs_percentile_workspace_bytes();
+    case SQ_OP_PAGED_ATTENTION:
+      return (M < 1 || N < 1 || K < 1) ? 0 : sq::paged_attention_workspace_bytes(M, N, K);
     default:
       return 0;
   }
@@ -523,6 +750,9 @@ sq_status sq_sync_status(sq_stream_t stream) {
     const unsigned int zero = 0;
     e = cudaMemcpyToSymbol(sq::g_status_word, &zero, sizeof zero);
     if (e != cudaSuccess) return cuda_fail(e, "sq_sync_status: clear status word");
+    if (word & sq::kErrIndex)
+      return fail(SQ_ERR_BOUNDS,
+                  "a slot, position, page or length read from device memory was out of range (status bits 0x%x)", word);
     if (word & sq::kErrBounds)
       return fail(SQ_ERR_BOUNDS, "device bounds guard fired (status bits 0x%x)", word);
     return fail(SQ_ERR_TIMEOUT, "device wait timed out (status bits 0x%x: 1 producer, 2 mma, 4 epilogue, 8 teardown)",

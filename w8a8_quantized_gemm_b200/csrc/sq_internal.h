@@ -15,6 +15,7 @@ enum : unsigned int {
   kErrEpilogueWait = 4u,
   kErrTeardownWait = 8u,
   kErrBounds = 16u,  // a device-side bounds guard fired (builds with SQ_DEBUG_GUARDS only)
+  kErrIndex = 32u,   // a slot, position, page or length read from device memory was out of range
 };
 
 constexpr uint64_t kDefaultWaitLimitNs = 2000000000ull;  // 2 s per wait
@@ -186,5 +187,64 @@ cudaError_t launch_gemm(const GemmArgs& a, cudaStream_t stream, const char** why
 // ---- CUDA-core product for M <= 4 tokens (sq_gemv.cu): same arguments and results as the GEMM.
 bool gemv_applies(int64_t M, int64_t K, bool outliers);
 cudaError_t launch_gemv(const GemmArgs& a, cudaStream_t stream);
+
+// ---- 4-bit weights (sq_int4.cu); layouts as in sq.h, zero nullptr for symmetric codes
+size_t int4_weight_bytes(int64_t N, int64_t K);
+cudaError_t launch_int4_quant(const uint16_t* W, int64_t N, int64_t K, int64_t ldw, const float* s, int group,
+                              uint8_t* Wp, uint16_t* scale, uint8_t* zero, cudaStream_t stream);
+cudaError_t launch_int4_dequant(const uint8_t* Wp, const uint16_t* scale, const uint8_t* zero, int group, int64_t N,
+                                int64_t K, uint16_t* out, cudaStream_t stream);
+struct Int4LinearArgs {
+  const uint16_t* X = nullptr;     // [M, K], ldx
+  int64_t M = 0, N = 0, K = 0, ldx = 0;
+  const uint8_t* Wp = nullptr;
+  const uint16_t* scale = nullptr;
+  const uint8_t* zero = nullptr;
+  int group = 0;
+  const uint16_t* bias = nullptr;  // [N] or nullptr
+  uint16_t* Y = nullptr;           // [M, N]
+};
+cudaError_t launch_int4_linear(const Int4LinearArgs& a, cudaStream_t stream);
+
+// ---- paged key-value cache (sq_kv.cu)
+struct KvView {  // a checked sq_kv_cache, as the kernels take it
+  void* k = nullptr;
+  void* v = nullptr;
+  float* k_scale = nullptr;
+  float* v_scale = nullptr;
+  int64_t num_pages = 0, page_stride = 0, scale_page_stride = 0;
+  int heads = 0, head_dim = 0, page_shift = 0;
+  bool int8 = false;
+};
+struct RopeAppendArgs {
+  const uint16_t *q = nullptr, *k = nullptr, *v = nullptr;
+  int64_t ldq = 0, ldk = 0, ldv = 0, T = 0;
+  int H = 0;
+  const float *cos_t = nullptr, *sin_t = nullptr;
+  int64_t max_pos = 0;
+  int rot = 0;
+  bool interleaved = false;
+  const int32_t *positions = nullptr, *slots = nullptr;
+  KvView cache;
+  uint16_t* q_out = nullptr;
+  unsigned int* status = nullptr;
+};
+cudaError_t launch_rope_kv_append(const RopeAppendArgs& a, cudaStream_t stream);
+struct PagedAttentionArgs {
+  const uint16_t* q = nullptr;
+  int64_t ldq = 0, B = 0, H = 0;
+  KvView cache;
+  const int32_t* table = nullptr;
+  int64_t ld_table = 0, max_pages = 0;
+  const int32_t* seq_lens = nullptr;
+  int64_t window = 0;
+  float scale = 0.0f;
+  uint16_t* out = nullptr;
+  float* lse = nullptr;
+  void* ws = nullptr;
+  unsigned int* status = nullptr;
+};
+size_t paged_attention_workspace_bytes(int64_t B, int64_t H, int64_t D);
+cudaError_t launch_paged_attention(const PagedAttentionArgs& a, cudaStream_t stream);
 
 }  // namespace sq

@@ -1,0 +1,230 @@
+// Paged key-value cache: the append of new tokens with the position rotation on the way, and
+// the attention of one new token per sequence. "SmoothQuant量化实战" §5.2 (KV-cache INT8 with
+// per-token, per-head scales).
+#include "sq_internal.h"
+#include "sq_ptx.cuh"
+#include "sq_rows.cuh"
+
+#include <cuda_bf16.h>
+
+#include <algorithm>
+#include <cfloat>
+#include <cmath>
+
+namespace sq {
+namespace {
+
+__device__ __forceinline__ float bf16_to_f(uint16_t v) { return __uint_as_float(static_cast<uint32_t>(v) << 16); }
+__device__ __forceinline__ uint16_t f_to_bf16(float v) { return __bfloat16_as_ushort(__float2bfloat16_rn(v)); }
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 r = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+// ---------------------------------------------------------------- append
+constexpr int kAppendThreads = 256;
+
+// head_dim / 16 lanes own a head row (the group of `lanes`, a power of two, has idle ones for
+// head_dim 96): each holds 16 elements, which are 8 pairs when its part of the row is rotated,
+// whichever way pairs are formed, so the lane's 8 angles stay in registers while its group
+// walks over the token's heads. A CTA takes one token, or several when a token has fewer rows
+// than the CTA has groups.
+template <bool INT8, bool PAIRS>
+__global__ void __launch_bounds__(kAppendThreads)
+rope_kv_append_kernel(const uint16_t* q, int64_t ldq, const uint16_t* __restrict__ k, int64_t ldk,
+                      const uint16_t* __restrict__ v, int64_t ldv, int64_t T, int H, const float* __restrict__ cos_t,
+                      const float* __restrict__ sin_t, int64_t max_pos, int rot,
+                      const int32_t* __restrict__ positions, const int32_t* __restrict__ slots, KvView c,
+                      uint16_t* q_out, int lanes, int groups_per_token, unsigned int* status) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int D = c.head_dim, groups = kAppendThreads / lanes;
+  const int group = threadIdx.x / lanes, i = threadIdx.x % lanes;
+  const int64_t tok = static_cast<int64_t>(blockIdx.x) * (groups / groups_per_token) + group / groups_per_token;
+  if (tok >= T) return;
+  const unsigned quad = lanes == 32 ? 0xffffffffu : ((1u << lanes) - 1u) << (threadIdx.x & 31 & ~(lanes - 1));
+  const int slot = __ldg(slots + tok);
+  if (slot < 0) return;
+  const int64_t pos = rot > 0 ? __ldg(positions + tok) : 0;
+  const int page = slot >> c.page_shift, off = slot & ((1 << c.page_shift) - 1);
+  if (page >= c.num_pages || pos < 0 || (rot > 0 && pos >= max_pos)) {
+    if (i == 0 && group % groups_per_token == 0) atomicOr(status, kErrIndex);
+    return;
+  }
+  const bool on = 16 * i < D, turn = 16 * i < rot;
+  // places of the lane's two runs of 8 elements
+  const int p0 = turn && !PAIRS ? 8 * i : 16 * i, p1 = turn && !PAIRS ? rot / 2 + 8 * i : 16 * i + 8;
+  float cs[8], sn[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) cs[j] = 1.0f, sn[j] = 0.0f;
+  if (turn) {
+    const float4* cp = reinterpret_cast<const float4*>(cos_t + pos * (rot / 2) + 8 * i);
+    const float4* sp = reinterpret_cast<const float4*>(sin_t + pos * (rot / 2) + 8 * i);
+    const float4 c0 = __ldg(cp), c1 = __ldg(cp + 1), s0 = __ldg(sp), s1 = __ldg(sp + 1);
+    cs[0] = c0.x; cs[1] = c0.y; cs[2] = c0.z; cs[3] = c0.w; cs[4] = c1.x; cs[5] = c1.y; cs[6] = c1.z; cs[7] = c1.w;
+    sn[0] = s0.x; sn[1] = s0.y; sn[2] = s0.z; sn[3] = s0.w; sn[4] = s1.x; sn[5] = s1.y; sn[6] = s1.z; sn[7] = s1.w;
+  }
+  const int rows = H + 2 * c.heads;
+  for (int row = group % groups_per_token; row < rows; row += groups_per_token) {
+    const bool is_q = row < H, is_v = row >= H + c.heads;
+    const int head = is_q ? row : is_v ? row - H - c.heads : row - H;
+    const uint16_t* src = (is_q ? q + tok * ldq : is_v ? v + tok * ldv : k + tok * ldk) + static_cast<int64_t>(head) * D;
+    float x[16];
+    if (on) {
+      const uint4 r[2] = {*reinterpret_cast<const uint4*>(src + p0), *reinterpret_cast<const uint4*>(src + p1)};
+      rows::widen16(r, x);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 16; ++j) x[j] = 0.0f;
+    }
+    if (turn && !is_v) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        float& a = PAIRS ? x[2 * j] : x[j];
+        float& b = PAIRS ? x[2 * j + 1] : x[8 + j];
+        const float ya = __fsub_rn(__fmul_rn(a, cs[j]), __fmul_rn(b, sn[j]));
+        const float yb = __fadd_rn(__fmul_rn(b, cs[j]), __fmul_rn(a, sn[j]));
+        a = ya;
+        b = yb;
+      }
+    }
+    if (is_q || !INT8) {
+      uint16_t* dst = is_q ? q_out + (tok * H + head) * D
+                           : static_cast<uint16_t*>(is_v ? c.v : c.k) + page * c.page_stride +
+                                 (static_cast<int64_t>(head) << c.page_shift) * D + static_cast<int64_t>(off) * D;
+      if (on) {
+        *reinterpret_cast<uint4*>(dst + p0) = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]),
+                                                         pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+        *reinterpret_cast<uint4*>(dst + p1) = make_uint4(pack_bf16(x[8], x[9]), pack_bf16(x[10], x[11]),
+                                                         pack_bf16(x[12], x[13]), pack_bf16(x[14], x[15]));
+      }
+    } else {
+      float a = 0.0f;
+#pragma unroll
+      for (int j = 0; j < 16; ++j) a = fmaxf(a, fabsf(x[j]));
+      for (int o = lanes / 2; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(quad, a, o));
+      const float r = a > 0.0f ? fminf(__fdiv_rn(127.0f, a), FLT_MAX) : 0.0f;
+      const int64_t at = (static_cast<int64_t>(head) << c.page_shift) + off;
+      int8_t* dst = static_cast<int8_t*>(is_v ? c.v : c.k) + page * c.page_stride + at * D;
+      if (on) {
+        int e[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) e[j] = __float2int_rn(fminf(fmaxf(__fmul_rn(x[j], r), -128.0f), 127.0f));
+        *reinterpret_cast<uint2*>(dst + p0) =
+            make_uint2(rows::pack4(e[0], e[1], e[2], e[3]), rows::pack4(e[4], e[5], e[6], e[7]));
+        *reinterpret_cast<uint2*>(dst + p1) =
+            make_uint2(rows::pack4(e[8], e[9], e[10], e[11]), rows::pack4(e[12], e[13], e[14], e[15]));
+      }
+      if (i == 0) (is_v ? c.v_scale : c.k_scale)[page * c.scale_page_stride + at] = __fdiv_rn(a, 127.0f);
+    }
+  }
+}
+
+// ---------------------------------------------------------------- attention
+constexpr int kAttnWarps = 8;
+
+// One CTA per sequence and query head; each warp takes tokens in turn with its own running
+// maximum, sum and output (lane: elements lane + 32 j), joined at the end.
+template <bool INT8>
+__global__ void __launch_bounds__(kAttnWarps * 32)
+paged_attention_kernel(const uint16_t* __restrict__ q, int64_t ldq, int H, KvView c,
+                       const int32_t* __restrict__ table, int64_t ld_table, int64_t max_pages,
+                       const int32_t* __restrict__ seq_lens, int64_t window, float scale, uint16_t* __restrict__ out,
+                       float* __restrict__ lse, unsigned int* status) {
+  griddep_wait();
+  griddep_launch_dependents();
+  __shared__ float s_m[kAttnWarps], s_l[kAttnWarps], s_o[kAttnWarps][256];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, D = c.head_dim;
+  const int64_t b = blockIdx.y;
+  const int h = blockIdx.x, kvh = h / (H / c.heads);
+  const uint16_t* qr = q + b * ldq + static_cast<int64_t>(h) * D;
+  float qv[8], o[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) qv[j] = lane + 32 * j < D ? bf16_to_f(__ldg(qr + lane + 32 * j)) : 0.0f, o[j] = 0.0f;
+  int64_t len = __ldg(seq_lens + b);
+  const int64_t most = max_pages << c.page_shift;
+  if (len < 0 || len > most) {
+    if (threadIdx.x == 0 && h == 0) atomicOr(status, kErrIndex);
+    len = len < 0 ? 0 : most;
+  }
+  const int64_t first = window > 0 && len > window ? len - window : 0;
+  float m = -INFINITY, l = 0.0f;
+  for (int64_t t = first + warp; t < len; t += kAttnWarps) {
+    const int64_t page = __ldg(table + b * ld_table + (t >> c.page_shift));
+    if (page < 0 || page >= c.num_pages) {
+      if (lane == 0) atomicOr(status, kErrIndex);
+      continue;
+    }
+    const int64_t row = (static_cast<int64_t>(kvh) << c.page_shift) + (t & ((1 << c.page_shift) - 1));
+    const int64_t at = page * c.page_stride + row * D, sat = page * c.scale_page_stride + row;
+    float kx[8], vx[8], dot = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int d = lane + 32 * j;
+      kx[j] = vx[j] = 0.0f;
+      if (d < D) {
+        if (INT8) {
+          kx[j] = static_cast<const int8_t*>(c.k)[at + d] * c.k_scale[sat];
+          vx[j] = static_cast<const int8_t*>(c.v)[at + d] * c.v_scale[sat];
+        } else {
+          kx[j] = bf16_to_f(static_cast<const uint16_t*>(c.k)[at + d]);
+          vx[j] = bf16_to_f(static_cast<const uint16_t*>(c.v)[at + d]);
+        }
+      }
+      dot = fmaf(qv[j], kx[j], dot);
+    }
+#pragma unroll
+    for (int s = 16; s > 0; s >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, s);
+    const float x = dot * scale, mn = fmaxf(m, x), old = m == -INFINITY ? 0.0f : expf(m - mn), p = expf(x - mn);
+    l = l * old + p;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) o[j] = o[j] * old + p * vx[j];
+    m = mn;
+  }
+  if (lane == 0) s_m[warp] = m, s_l[warp] = l;
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    if (lane + 32 * j < D) s_o[warp][lane + 32 * j] = o[j];
+  __syncthreads();
+  float mt = -INFINITY, lt = 0.0f;
+  for (int w = 0; w < kAttnWarps; ++w) mt = fmaxf(mt, s_m[w]);
+  const int d = threadIdx.x;
+  float ot = 0.0f;
+  for (int w = 0; w < kAttnWarps; ++w) {
+    const float f = s_m[w] == -INFINITY ? 0.0f : expf(s_m[w] - mt);
+    lt += f * s_l[w];
+    if (d < D) ot += f * s_o[w][d];
+  }
+  if (d < D) out[(b * H + h) * D + d] = f_to_bf16(lt > 0.0f ? ot / lt : 0.0f);
+  if (d == 0 && lse != nullptr) lse[b * H + h] = lt > 0.0f ? mt + logf(lt) : -INFINITY;
+}
+
+}  // namespace
+
+cudaError_t launch_rope_kv_append(const RopeAppendArgs& a, cudaStream_t stream) {
+  int lanes = 4;
+  while (lanes * 16 < a.cache.head_dim) lanes *= 2;
+  const int groups = kAppendThreads / lanes, rows = a.H + 2 * a.cache.heads;
+  int per = 1;
+  while (per < rows && per < groups) per *= 2;
+  const int64_t tokens = groups / per;
+  auto kernel = a.cache.int8 ? (a.interleaved ? rope_kv_append_kernel<true, true> : rope_kv_append_kernel<true, false>)
+                             : (a.interleaved ? rope_kv_append_kernel<false, true> : rope_kv_append_kernel<false, false>);
+  return launch_kernel(kernel, dim3(static_cast<unsigned>((a.T + tokens - 1) / tokens)), dim3(kAppendThreads), 0, stream,
+                       true, a.q, a.ldq, a.k, a.ldk, a.v, a.ldv, a.T, a.H, a.cos_t, a.sin_t, a.max_pos, a.rot,
+                       a.positions, a.slots, a.cache, a.q_out, lanes, per, a.status);
+}
+
+size_t paged_attention_workspace_bytes(int64_t B, int64_t H, int64_t D) {
+  (void)B, (void)H, (void)D;
+  return 0;
+}
+
+cudaError_t launch_paged_attention(const PagedAttentionArgs& a, cudaStream_t stream) {
+  auto kernel = a.cache.int8 ? paged_attention_kernel<true> : paged_attention_kernel<false>;
+  return launch_kernel(kernel, dim3(static_cast<unsigned>(a.H), static_cast<unsigned>(a.B)), dim3(kAttnWarps * 32), 0,
+                       stream, true, a.q, a.ldq, static_cast<int>(a.H), a.cache, a.table, a.ld_table, a.max_pages,
+                       a.seq_lens, a.window, a.scale, a.out, a.lse, a.status);
+}
+
+}  // namespace sq

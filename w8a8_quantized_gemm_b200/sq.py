@@ -23,7 +23,9 @@ SQ_ERR_BOUNDS = -7
 SQ_PER_TENSOR, SQ_PER_CHANNEL = 0, 1
 SQ_OP_SMOOTH_QUANT_WEIGHT, SQ_OP_INT8_GEMM_DEQUANT, SQ_OP_LLMINT8 = 1, 2, 3
 SQ_OP_QUANT_ACT_PER_TENSOR, SQ_OP_MEAN_STD_THRESHOLD, SQ_OP_ABS_PERCENTILE = 4, 5, 6
+SQ_OP_PAGED_ATTENTION = 7
 SQ_NORM_LAYER, SQ_NORM_RMS = 0, 1
+SQ_KV_BF16, SQ_KV_INT8 = 0, 1
 
 if not os.path.exists(LIB_PATH):
     raise ImportError(f"{LIB_PATH} is missing: build it with `python -m w8a8_quantized_gemm_b200.build`")
@@ -48,6 +50,13 @@ _SIGS = {
     "sq_act_abs_percentile": ([_p, _i64, _i64, _i64, C.c_double, _p, _p, _sz, _p], _i32),
     "sq_quant_act_per_token_asym": ([_p, _i64, _i64, _i64, _p, _p, _p, _p, _p], _i32),
     "sq_weight_row_sums": ([_p, _i64, _i64, _p, _p], _i32),
+    "sq_int4_weight_bytes": ([_i64, _i64], _sz),
+    "sq_quant_weight_int4": ([_p, _i64, _i64, _i64, _p, _i64, _p, _p, _p, _p], _i32),
+    "sq_dequant_weight_int4": ([_p, _p, _p, _i64, _i64, _i64, _p, _p], _i32),
+    "sq_int4_linear": ([_p, _i64, _i64, _i64, _p, _p, _p, _i64, _p, _p, _i64, _p], _i32),
+    "sq_rope_kv_append": ([_p, _i64, _p, _i64, _p, _i64, _i64, _i64, _p, _p, _i64, _i64, _i32, _p, _p, _p, _p, _p],
+                          _i32),
+    "sq_paged_attention": ([_p, _i64, _i64, _i64, _p, _p, _i64, _i64, _p, _i64, _f32, _p, _p, _p, _sz, _p], _i32),
     "sq_workspace_size": ([_i32, _i64, _i64, _i64], _sz),
     "sq_last_error": ([], C.c_char_p),
     "sq_sync_status": ([_p], _i32),
@@ -296,6 +305,198 @@ def sq_weight_row_sums(Wq, rowsum, stream=None):
     _check(_lib.sq_weight_row_sums(_ptr(Wq, torch.int8, "Wq"), N, K, _ptr(rowsum, torch.int32, "rowsum"),
                                    _stream(stream)))
     return rowsum
+
+
+# ---------------------------------------------------------------- 4-bit weights
+def _here(*tensors):
+    """The device index of the given tensors (None entries skipped), which must be CUDA tensors
+    on the current device: the library launches there."""
+    torch = _torch()
+    dev = None
+    for t in tensors:
+        if t is None:
+            continue
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            raise TypeError("tensors must be CUDA tensors")
+        dev = torch.cuda.current_device() if dev is None else dev
+        if t.get_device() != dev:
+            raise ValueError(f"tensor on {t.device}, but the current device is cuda:{dev}")
+    return dev
+
+
+def _dense(t, dtype, shape, name):
+    """Data pointer of a contiguous tensor of exactly this type and shape (None passes)."""
+    if t is None:
+        return None
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def sq_int4_weight_bytes(N: int, K: int) -> int:
+    return int(_lib.sq_int4_weight_bytes(int(N), int(K)))
+
+
+def _int4(Wp, w_scale, w_zero, group, N, K):
+    torch = _torch()
+    groups = -(-K // group) if group > 0 else 0
+    return (_dense(Wp, torch.uint8, (sq_int4_weight_bytes(N, K),), "Wp"),
+            _dense(w_scale, torch.bfloat16, (groups, N), "w_scale"),
+            _dense(w_zero, torch.uint8, (groups, N), "w_zero"))
+
+
+def sq_quant_weight_int4(W, s, group: int, Wp, w_scale, w_zero=None, stream=None):
+    """4-bit codes and group scales of W [N, K] (times s); with w_zero, zero points too."""
+    torch = _torch()
+    N, K = W.shape
+    _here(W, s, Wp, w_scale, w_zero)
+    p, e, z = _int4(Wp, w_scale, w_zero, group, N, K)
+    _check(_lib.sq_quant_weight_int4(_ptr(W, torch.bfloat16, "W", True), N, K, W.stride(0),
+                                     _dense(s, torch.float32, (K,), "s"), int(group), p, e, z, _stream(stream)))
+    return Wp, w_scale, w_zero
+
+
+def sq_dequant_weight_int4(Wp, w_scale, w_zero, group: int, out, stream=None):
+    """The bf16 values [N, K] (the shape of `out`) that a 4-bit weight stands for."""
+    torch = _torch()
+    N, K = out.shape
+    _here(Wp, w_scale, w_zero, out)
+    p, e, z = _int4(Wp, w_scale, w_zero, group, N, K)
+    _check(_lib.sq_dequant_weight_int4(p, e, z, int(group), N, K, _dense(out, torch.bfloat16, (N, K), "out"),
+                                       _stream(stream)))
+    return out
+
+
+def sq_int4_linear(X, Wp, w_scale, w_zero, group: int, bias, Y, stream=None):
+    """Y [M, N] = X [M, K] times the 4-bit weight, plus bias; M <= 64."""
+    torch = _torch()
+    M, K = X.shape
+    N = Y.shape[-1]
+    _here(X, Wp, w_scale, w_zero, bias, Y)
+    p, e, z = _int4(Wp, w_scale, w_zero, group, N, K)
+    _check(_lib.sq_int4_linear(_ptr(X, torch.bfloat16, "X", True), M, K, X.stride(0), p, e, z, int(group),
+                               _dense(bias, torch.bfloat16, (N,), "bias"), _dense(Y, torch.bfloat16, (M, N), "Y"), N,
+                               _stream(stream)))
+    return Y
+
+
+# ---------------------------------------------------------------- paged key-value cache
+class _KvCacheStruct(C.Structure):
+    _fields_ = [("type", C.c_int32), ("reserved", C.c_int32), ("k", _p), ("v", _p), ("k_scale", _p), ("v_scale", _p),
+                ("num_pages", _i64), ("heads", _i64), ("page_size", _i64), ("head_dim", _i64), ("page_stride", _i64),
+                ("scale_page_stride", _i64)]
+
+
+class KvCache:
+    """Descriptor of a paged cache (sq_kv_cache) over the caller's tensors: k, v
+    [num_pages, heads, page_size, head_dim] bf16, or int8 with fp32 scales k_scale, v_scale
+    [num_pages, heads, page_size]; dense but for the page stride. Made once, passed to every
+    call; it holds the tensors."""
+
+    def __init__(self, k, v, k_scale=None, v_scale=None):
+        torch = _torch()
+        int8 = k.dtype == torch.int8
+        if k.dim() != 4 or (not int8 and k.dtype != torch.bfloat16) or v.dtype != k.dtype:
+            raise TypeError("k and v must be 4-D, both bfloat16 or both int8")
+        if int8 != (k_scale is not None) or int8 != (v_scale is not None):
+            raise ValueError("int8 caches have k_scale and v_scale, bf16 caches none")
+        pages, heads, page_size, dim = k.shape
+        for t, shape, dense in ((k, k.shape, (page_size * dim, dim, 1)), (v, k.shape, (page_size * dim, dim, 1)),
+                                (k_scale, k.shape[:3], (page_size, 1)), (v_scale, k.shape[:3], (page_size, 1))):
+            if t is None:
+                continue
+            if t.shape != shape or any(s != d for s, d, n in zip(t.stride()[1:], dense, t.shape[1:]) if n > 1):
+                raise ValueError("cache tensors must have one shape and be dense within a page")
+            if dense[-2:] == (page_size, 1) and len(dense) == 2 and t.dtype != torch.float32:
+                raise TypeError("cache scales must be float32")
+        if not k.is_cuda or any(t is not None and t.device != k.device for t in (v, k_scale, v_scale)):
+            raise ValueError("cache tensors must be on one CUDA device")
+
+        def stride(a, b):
+            if pages == 1:
+                return a.numel()
+            if a.stride(0) != b.stride(0):
+                raise ValueError("k and v (and their scales) must share one page stride")
+            return a.stride(0)
+
+        self.tensors = (k, v, k_scale, v_scale)
+        self.device = k.get_device()
+        self.heads, self.head_dim = heads, dim
+        self.struct = _KvCacheStruct(
+            SQ_KV_INT8 if int8 else SQ_KV_BF16, 0, k.data_ptr(), v.data_ptr(),
+            k_scale.data_ptr() if int8 else None, v_scale.data_ptr() if int8 else None, pages, heads, page_size, dim,
+            stride(k, v), stride(k_scale, v_scale) if int8 else 0)
+        self.ref = C.byref(self.struct)
+
+
+def _heads(t, heads, dim, name):
+    """(data pointer, token stride) of a bf16 [T, heads, dim] tensor dense within a token."""
+    torch = _torch()
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim or t.stride(2) != 1 or \
+            (heads > 1 and t.stride(1) != dim):
+        raise ValueError(f"{name} must be [tokens, {heads}, {dim}], dense within a token")
+    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else heads * dim
+
+
+def sq_rope_kv_append(q, k, v, cos, sin, positions, slots, cache: KvCache, q_out, interleaved: bool = False,
+                      stream=None):
+    """Rotate q and k by position, write q_out, append k and v to the cache's slots. q and q_out
+    may be None; cos, sin [max_pos, rot_dim / 2] and positions may be None (no rotation)."""
+    torch = _torch()
+    if _here(q, k, v, cos, sin, positions, slots, q_out) != cache.device:
+        raise ValueError(f"cache on cuda:{cache.device}, which is not the current device")
+    T, Hkv, D = k.shape
+    if Hkv != cache.heads or D != cache.head_dim or v.shape != k.shape:
+        raise ValueError(f"k and v must be [tokens, {cache.heads}, {cache.head_dim}]")
+    kp, ldk = _heads(k, Hkv, D, "k")
+    vp, ldv = _heads(v, Hkv, D, "v")
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out must be given together")
+    H, qp, ldq = 0, None, 0
+    if q is not None:
+        H = q.shape[1]
+        qp, ldq = _heads(q, H, D, "q")
+        if q.shape[0] != T:
+            raise ValueError("q and k must have the same number of tokens")
+    max_pos, half = (0, 0) if cos is None else cos.shape
+    if (cos is None) != (sin is None) or (cos is None) != (positions is None):
+        raise ValueError("cos, sin and positions must be given together")
+    _check(_lib.sq_rope_kv_append(
+        qp, ldq, kp, ldk, vp, ldv, T, H, _dense(cos, torch.float32, (max_pos, half), "cos"),
+        _dense(sin, torch.float32, (max_pos, half), "sin"), max_pos, 2 * half, int(bool(interleaved)),
+        _dense(positions, torch.int32, (T,), "positions"), _dense(slots, torch.int32, (T,), "slots"), cache.ref,
+        _dense(q_out, torch.bfloat16, (T, H, D), "q_out"), _stream(stream)))
+    return q_out
+
+
+def sq_paged_attention(q, cache: KvCache, block_table, seq_lens, scale: float, out, lse=None, window: int = 0, ws=None,
+                       stream=None):
+    """out [B, H, D]: attention of one token per sequence over the cache; lse [B, H] fp32 too."""
+    torch = _torch()
+    if _here(q, block_table, seq_lens, out, lse, ws) != cache.device:
+        raise ValueError(f"cache on cuda:{cache.device}, which is not the current device")
+    B, H, D = q.shape
+    if D != cache.head_dim:
+        raise ValueError(f"q must have head dimension {cache.head_dim}")
+    qp, ldq = _heads(q, H, D, "q")
+    if block_table.dim() != 2 or block_table.shape[0] != B or (block_table.shape[1] > 1 and block_table.stride(1) != 1):
+        raise ValueError(f"block_table must be [{B}, max_pages] with unit column stride")
+    if block_table.dtype != torch.int32:
+        raise TypeError("block_table must be torch.int32")
+    max_pages = block_table.shape[1]
+    wsp, wsb = _ws(ws)
+    _check(_lib.sq_paged_attention(
+        qp, ldq, B, H, cache.ref, block_table.data_ptr(), block_table.stride(0) if B > 1 else max_pages, max_pages,
+        _dense(seq_lens, torch.int32, (B,), "seq_lens"), int(window), float(scale),
+        _dense(out, torch.bfloat16, (B, H, D), "out"), _dense(lse, torch.float32, (B, H), "lse"), wsp, wsb,
+        _stream(stream)))
+    return out
 
 
 def sq_workspace_size(op: int, M: int, N: int, K: int) -> int:
