@@ -206,7 +206,7 @@ struct Int4LinearArgs {
 };
 cudaError_t launch_int4_linear(const Int4LinearArgs& a, cudaStream_t stream);
 
-// ---- paged key-value cache (sq_kv.cu)
+// ---- paged key-value cache (append in sq_kv.cu, attention in sq_attention.cu)
 struct KvView {  // a checked sq_kv_cache, as the kernels take it
   void* k = nullptr;
   void* v = nullptr;

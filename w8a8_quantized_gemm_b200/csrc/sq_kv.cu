@@ -1,6 +1,5 @@
-// Paged key-value cache: the append of new tokens with the position rotation on the way, and
-// the attention of one new token per sequence. "SmoothQuant量化实战" §5.2 (KV-cache INT8 with
-// per-token, per-head scales).
+// Paged key-value cache: the append of new tokens, with the position rotation on the way.
+// "SmoothQuant量化实战" §5.2 (KV-cache INT8 with per-token, per-head scales).
 #include "sq_internal.h"
 #include "sq_ptx.cuh"
 #include "sq_rows.cuh"
@@ -9,13 +8,10 @@
 
 #include <algorithm>
 #include <cfloat>
-#include <cmath>
 
 namespace sq {
 namespace {
 
-__device__ __forceinline__ float bf16_to_f(uint16_t v) { return __uint_as_float(static_cast<uint32_t>(v) << 16); }
-__device__ __forceinline__ uint16_t f_to_bf16(float v) { return __bfloat16_as_ushort(__float2bfloat16_rn(v)); }
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 r = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&r);
@@ -120,85 +116,6 @@ rope_kv_append_kernel(const uint16_t* q, int64_t ldq, const uint16_t* __restrict
   }
 }
 
-// ---------------------------------------------------------------- attention
-constexpr int kAttnWarps = 8;
-
-// One CTA per sequence and query head; each warp takes tokens in turn with its own running
-// maximum, sum and output (lane: elements lane + 32 j), joined at the end.
-template <bool INT8>
-__global__ void __launch_bounds__(kAttnWarps * 32)
-paged_attention_kernel(const uint16_t* __restrict__ q, int64_t ldq, int H, KvView c,
-                       const int32_t* __restrict__ table, int64_t ld_table, int64_t max_pages,
-                       const int32_t* __restrict__ seq_lens, int64_t window, float scale, uint16_t* __restrict__ out,
-                       float* __restrict__ lse, unsigned int* status) {
-  griddep_wait();
-  griddep_launch_dependents();
-  __shared__ float s_m[kAttnWarps], s_l[kAttnWarps], s_o[kAttnWarps][256];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, D = c.head_dim;
-  const int64_t b = blockIdx.y;
-  const int h = blockIdx.x, kvh = h / (H / c.heads);
-  const uint16_t* qr = q + b * ldq + static_cast<int64_t>(h) * D;
-  float qv[8], o[8];
-#pragma unroll
-  for (int j = 0; j < 8; ++j) qv[j] = lane + 32 * j < D ? bf16_to_f(__ldg(qr + lane + 32 * j)) : 0.0f, o[j] = 0.0f;
-  int64_t len = __ldg(seq_lens + b);
-  const int64_t most = max_pages << c.page_shift;
-  if (len < 0 || len > most) {
-    if (threadIdx.x == 0 && h == 0) atomicOr(status, kErrIndex);
-    len = len < 0 ? 0 : most;
-  }
-  const int64_t first = window > 0 && len > window ? len - window : 0;
-  float m = -INFINITY, l = 0.0f;
-  for (int64_t t = first + warp; t < len; t += kAttnWarps) {
-    const int64_t page = __ldg(table + b * ld_table + (t >> c.page_shift));
-    if (page < 0 || page >= c.num_pages) {
-      if (lane == 0) atomicOr(status, kErrIndex);
-      continue;
-    }
-    const int64_t row = (static_cast<int64_t>(kvh) << c.page_shift) + (t & ((1 << c.page_shift) - 1));
-    const int64_t at = page * c.page_stride + row * D, sat = page * c.scale_page_stride + row;
-    float kx[8], vx[8], dot = 0.0f;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int d = lane + 32 * j;
-      kx[j] = vx[j] = 0.0f;
-      if (d < D) {
-        if (INT8) {
-          kx[j] = static_cast<const int8_t*>(c.k)[at + d] * c.k_scale[sat];
-          vx[j] = static_cast<const int8_t*>(c.v)[at + d] * c.v_scale[sat];
-        } else {
-          kx[j] = bf16_to_f(static_cast<const uint16_t*>(c.k)[at + d]);
-          vx[j] = bf16_to_f(static_cast<const uint16_t*>(c.v)[at + d]);
-        }
-      }
-      dot = fmaf(qv[j], kx[j], dot);
-    }
-#pragma unroll
-    for (int s = 16; s > 0; s >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, s);
-    const float x = dot * scale, mn = fmaxf(m, x), old = m == -INFINITY ? 0.0f : expf(m - mn), p = expf(x - mn);
-    l = l * old + p;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) o[j] = o[j] * old + p * vx[j];
-    m = mn;
-  }
-  if (lane == 0) s_m[warp] = m, s_l[warp] = l;
-#pragma unroll
-  for (int j = 0; j < 8; ++j)
-    if (lane + 32 * j < D) s_o[warp][lane + 32 * j] = o[j];
-  __syncthreads();
-  float mt = -INFINITY, lt = 0.0f;
-  for (int w = 0; w < kAttnWarps; ++w) mt = fmaxf(mt, s_m[w]);
-  const int d = threadIdx.x;
-  float ot = 0.0f;
-  for (int w = 0; w < kAttnWarps; ++w) {
-    const float f = s_m[w] == -INFINITY ? 0.0f : expf(s_m[w] - mt);
-    lt += f * s_l[w];
-    if (d < D) ot += f * s_o[w][d];
-  }
-  if (d < D) out[(b * H + h) * D + d] = f_to_bf16(lt > 0.0f ? ot / lt : 0.0f);
-  if (d == 0 && lse != nullptr) lse[b * H + h] = lt > 0.0f ? mt + logf(lt) : -INFINITY;
-}
-
 }  // namespace
 
 cudaError_t launch_rope_kv_append(const RopeAppendArgs& a, cudaStream_t stream) {
@@ -213,18 +130,6 @@ cudaError_t launch_rope_kv_append(const RopeAppendArgs& a, cudaStream_t stream) 
   return launch_kernel(kernel, dim3(static_cast<unsigned>((a.T + tokens - 1) / tokens)), dim3(kAppendThreads), 0, stream,
                        true, a.q, a.ldq, a.k, a.ldk, a.v, a.ldv, a.T, a.H, a.cos_t, a.sin_t, a.max_pos, a.rot,
                        a.positions, a.slots, a.cache, a.q_out, lanes, per, a.status);
-}
-
-size_t paged_attention_workspace_bytes(int64_t B, int64_t H, int64_t D) {
-  (void)B, (void)H, (void)D;
-  return 0;
-}
-
-cudaError_t launch_paged_attention(const PagedAttentionArgs& a, cudaStream_t stream) {
-  auto kernel = a.cache.int8 ? paged_attention_kernel<true> : paged_attention_kernel<false>;
-  return launch_kernel(kernel, dim3(static_cast<unsigned>(a.H), static_cast<unsigned>(a.B)), dim3(kAttnWarps * 32), 0,
-                       stream, true, a.q, a.ldq, static_cast<int>(a.H), a.cache, a.table, a.ld_table, a.max_pages,
-                       a.seq_lens, a.window, a.scale, a.out, a.lse, a.status);
 }
 
 }  // namespace sq
