@@ -32,8 +32,6 @@
 namespace sq {
 namespace {
 
-constexpr int kTile = 16;  // tokens
-
 struct AttnParams {
   const uint16_t* q;
   int64_t ldq;
@@ -53,9 +51,11 @@ struct AttnParams {
   int blocks;  // units of a key head: group / (8 NT), rounded up
 };
 
-template <int D_, bool INT8_, int NT_, int WARPS_, int STAGES_>
+// D: head dimension; NT: query heads of a unit / 8; MT: tokens of a tile / 16.
+template <int D_, bool INT8_, int NT_, int MT_, int WARPS_, int STAGES_>
 struct Shape {
-  static constexpr int D = D_, NT = NT_, WARPS = WARPS_, STAGES = STAGES_;
+  static constexpr int D = D_, NT = NT_, MT = MT_, WARPS = WARPS_, STAGES = STAGES_;
+  static constexpr int kTile = 16 * MT;
   static constexpr bool INT8 = INT8_;
   static constexpr int kRowBytes = D * (INT8 ? 1 : 2);
   static constexpr int kRow = kRowBytes + 16;  // an odd number of 16-byte units: no bank conflicts
@@ -66,7 +66,7 @@ struct Shape {
   static constexpr int kPart = kHeads * (D + 2);  // floats: output, maximum, sum
   static constexpr size_t kSmem = WARPS * (static_cast<size_t>(kRing) + kPart * 4);
   static_assert(kRing >= kPart * 4, "a warp's last partial state is kept in its ring");
-  static_assert(kSmem <= 232448 - 1024, "shared memory of an SM");
+  static_assert(kSmem <= 232448 - 4096, "shared memory of an SM");
 };
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool valid) {
@@ -126,34 +126,45 @@ struct Range {
   int64_t lo, len;
   int first, last;
 };
+template <typename S>
 __device__ __forceinline__ Range range_of(const AttnParams& p, int b) {
   Range r;
   r.len = __ldg(p.seq_lens + b);
   r.len = min(max(r.len, int64_t(0)), p.max_pages << p.c.page_shift);
   r.lo = p.window > 0 && r.len > p.window ? r.len - p.window : 0;
-  r.first = static_cast<int>(r.lo / kTile);
-  r.last = r.len > 0 ? static_cast<int>((r.len + kTile - 1) / kTile) : r.first;
+  r.first = static_cast<int>(r.lo / S::kTile);
+  r.last = r.len > 0 ? static_cast<int>((r.len + S::kTile - 1) / S::kTile) : r.first;
   return r;
 }
 
 // A place on the line of tiles.
+template <typename S>
 struct Cursor {
   Range r;
-  int b, unit, tile;
-  int64_t unit_pos;  // place of the unit's first tile
-  __device__ __forceinline__ void next(const AttnParams& p, int units) {
+  int b, kvh, hb, tile;  // sequence, key head, block of its query heads
+  int64_t unit_pos;      // place of the unit's first tile
+  __device__ __forceinline__ void next(const AttnParams& p) {
     if (++tile < r.last) return;
     unit_pos += r.last - r.first;
-    if (++unit == units) {
-      unit = 0;
-      do {
-        if (++b >= p.B) return;
-        r = range_of(p, b);
-      } while (r.first == r.last);
+    if (++hb == p.blocks) {
+      hb = 0;
+      if (++kvh == p.c.heads) {
+        kvh = 0;
+        do {
+          if (++b >= p.B) return;
+          r = range_of<S>(p, b);
+        } while (r.first == r.last);
+      }
     }
     tile = r.first;
   }
 };
+
+// a / b of counts, which nearly always fit 32 bits (a 64-bit division costs ten times as much).
+__device__ __forceinline__ int64_t divide(int64_t a, int64_t b) {
+  if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return a / b;
+}
 
 // Sum over the warp of a 64-bit count.
 __device__ __forceinline__ int64_t warp_sum(int64_t v) {
@@ -163,12 +174,13 @@ __device__ __forceinline__ int64_t warp_sum(int64_t v) {
 }
 
 // The place `at` (< the number of tiles) as a cursor: prefix sums over 32 sequences at a time.
-__device__ __forceinline__ Cursor cursor_at(const AttnParams& p, int units, int64_t at, int lane) {
-  Cursor c;
+template <typename S>
+__device__ __forceinline__ Cursor<S> cursor_at(const AttnParams& p, int units, int64_t at, int lane) {
+  Cursor<S> c;
   int64_t base = 0;
   for (int b0 = 0;; b0 += 32) {
     Range r{};
-    if (b0 + lane < p.B) r = range_of(p, b0 + lane);
+    if (b0 + lane < p.B) r = range_of<S>(p, b0 + lane);
     const int64_t n = static_cast<int64_t>(r.last - r.first) * units;
     int64_t incl = n;
 #pragma unroll
@@ -181,10 +193,12 @@ __device__ __forceinline__ Cursor cursor_at(const AttnParams& p, int units, int6
       const int src = __ffs(past) - 1;
       const int64_t start = base + __shfl_sync(0xffffffffu, incl - n, src);
       c.b = b0 + src;
-      c.r = range_of(p, c.b);
+      c.r = range_of<S>(p, c.b);
       const int per = c.r.last - c.r.first;
-      c.unit = static_cast<int>((at - start) / per);
-      c.unit_pos = start + static_cast<int64_t>(c.unit) * per;
+      const int unit = static_cast<int>(divide(at - start, per));
+      c.kvh = unit / p.blocks;
+      c.hb = unit % p.blocks;
+      c.unit_pos = start + static_cast<int64_t>(unit) * per;
       c.tile = c.r.first + static_cast<int>(at - c.unit_pos);
       return c;
     }
@@ -194,13 +208,20 @@ __device__ __forceinline__ Cursor cursor_at(const AttnParams& p, int units, int6
 
 template <typename S>
 __global__ void __launch_bounds__(S::WARPS * 32, 1) paged_attention_kernel(const AttnParams p) {
-  constexpr int D = S::D, NT = S::NT, W = S::WARPS, kSteps = D / 16;
+  constexpr int D = S::D, NT = S::NT, MT = S::MT, W = S::WARPS, kSteps = D / 16, kTile = S::kTile;
+  constexpr unsigned kAll = kTile == 32 ? 0xFFFFFFFFu : 0xFFFFu;
   constexpr bool INT8 = S::INT8;
   griddep_wait();
   griddep_launch_dependents();
   extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ int64_t s_unit[2 * W][3];  // of a warp's partial states: unit, its first place, the place after its last
-  __shared__ unsigned s_last;
+  // a warp's partial states (2 w: the one that began inside its unit, 2 w + 1: the one that breaks
+  // off): unit or -1, sequence, key head, block; the unit's first place and the one after its last
+  __shared__ int4 s_unit[2 * W];
+  __shared__ int64_t s_span[2 * W][2];
+  __shared__ float s_factor[2 * W][S::kHeads], s_sum[2 * W][S::kHeads], s_top[2 * W][S::kHeads];
+  __shared__ int64_t s_from;
+  __shared__ int s_count;
+  __shared__ bool s_last;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int units = p.c.heads * p.blocks;
   uint8_t* ring = smem + warp * S::kRing;
@@ -210,20 +231,21 @@ __global__ void __launch_bounds__(S::WARPS * 32, 1) paged_attention_kernel(const
   // this CTA's and this warp's piece of the line
   int64_t total = 0;
   for (int b = lane; b < p.B; b += 32) {
-    const Range r = range_of(p, b);
+    const Range r = range_of<S>(p, b);
     if (blockIdx.x == 0 && warp == 0 && r.len != __ldg(p.seq_lens + b)) atomicOr(p.status, kErrIndex);
     total += static_cast<int64_t>(r.last - r.first) * units;
   }
   total = warp_sum(total);
-  const int64_t ctas = min(static_cast<int64_t>(gridDim.x), (total + W - 1) / W);
+  const int64_t ctas = min(static_cast<int64_t>(gridDim.x), divide(total + W - 1, W));
   const bool works = blockIdx.x < ctas;
-  const int64_t cta0 = works ? total * blockIdx.x / ctas : 0, cta1 = works ? total * (blockIdx.x + 1) / ctas : 0;
-  const int64_t p0 = cta0 + (cta1 - cta0) * warp / W, p1 = cta0 + (cta1 - cta0) * (warp + 1) / W;
-  if (lane < 2) s_unit[2 * warp + lane][0] = -1;
+  const int64_t cta0 = works ? divide(total * blockIdx.x, ctas) : 0;
+  const int64_t cta1 = works ? divide(total * (blockIdx.x + 1), ctas) : 0;
+  const int64_t p0 = cta0 + divide((cta1 - cta0) * warp, W), p1 = cta0 + divide((cta1 - cta0) * (warp + 1), W);
+  if (lane < 2) s_unit[2 * warp + lane].x = -1;
   __syncwarp();
 
   if (p0 < p1) {
-    Cursor load = cursor_at(p, units, p0, lane), cur = load;
+    Cursor<S> load = cursor_at<S>(p, units, p0, lane), cur = load;
     const int n = static_cast<int>(p1 - p0);
     const int shift = p.c.page_shift;
     // page table entries window .. window + 63 of sequence window_b, one of each half per lane
@@ -231,10 +253,16 @@ __global__ void __launch_bounds__(S::WARPS * 32, 1) paged_attention_kernel(const
     auto entry = [&](int b, int64_t i) {
       return i < p.max_pages ? __ldg(p.table + b * p.ld_table + i) : -1;
     };
+    const bool paged = (1 << shift) >= kTile;  // a tile lies in one page, its rows one after another
+    constexpr int kChunks = S::kRowBytes / 16, kCopies = kTile * kChunks / 32;
+    // place of copy i of this lane: row (32 i + lane) / kChunks
+    auto in_stage = [&](int i) {
+      return static_cast<uint32_t>((i * 32 + lane) / kChunks * S::kRow + (i * 32 + lane) % kChunks * 16);
+    };
     auto issue = [&](int stage) {
-      const int64_t tok = static_cast<int64_t>(load.tile) * kTile + (lane & 15);
-      const int first_page = static_cast<int>((static_cast<int64_t>(load.tile) * kTile) >> shift);
-      const int last_page = static_cast<int>((static_cast<int64_t>(load.tile) * kTile + kTile - 1) >> shift);
+      const int64_t tok0 = static_cast<int64_t>(load.tile) * kTile;
+      const int first_page = static_cast<int>(tok0 >> shift);
+      const int last_page = static_cast<int>((tok0 + kTile - 1) >> shift);
       if (load.b != window_b || first_page < window || last_page >= window + 64) {
         window = first_page;
         window_b = load.b;
@@ -245,31 +273,60 @@ __global__ void __launch_bounds__(S::WARPS * 32, 1) paged_attention_kernel(const
         pages0 = pages1;
         pages1 = entry(load.b, static_cast<int64_t>(window) + 32 + lane);
       }
-      const int at = static_cast<int>(tok >> shift) - window;
-      const int e0 = __shfl_sync(0xffffffffu, pages0, at & 31), e1 = __shfl_sync(0xffffffffu, pages1, at & 31);
-      const int64_t page = at < 32 ? e0 : e1;
-      const bool in = tok >= load.r.lo && tok < load.r.len;
-      const bool valid = in && page >= 0 && page < p.c.num_pages;
-      if (in && !valid) atomicOr(p.status, kErrIndex);
-      const unsigned mask = __ballot_sync(0xffffffffu, valid) & 0xFFFFu;
-      const int64_t row = (static_cast<int64_t>(load.unit / p.blocks) << shift) + (tok & ((1 << shift) - 1));
-      const int64_t off = valid ? (page * p.c.page_stride + row * D) * (INT8 ? 1 : 2) : 0;
       const uint32_t dst = ring32 + stage * S::kStage;
-      constexpr int kChunks = S::kRowBytes / 16;
+      const uint8_t *k = static_cast<const uint8_t*>(p.c.k), *v = static_cast<const uint8_t*>(p.c.v);
+      const int64_t row0 = static_cast<int64_t>(load.kvh) << shift;
+      unsigned mask = kAll;
+      const int64_t one = __shfl_sync(0xffffffffu, pages0, (first_page - window) & 31);
+      if (paged && first_page < window + 32 && tok0 >= load.r.lo && tok0 + kTile <= load.r.len && one >= 0 &&
+          one < p.c.num_pages) {
+        // whole tile: contiguous
+        const int64_t row = row0 + (tok0 & ((1 << shift) - 1));
+        const int64_t off = (one * p.c.page_stride + row * D) * (INT8 ? 1 : 2) + lane * 16;
+        k += off;
+        v += off;
 #pragma unroll
-      for (int i = 0; i < kTile * kChunks / 32; ++i) {
-        const int r = (i * 32 + lane) / kChunks, ch = (i * 32 + lane) % kChunks;
-        const int64_t o = __shfl_sync(0xffffffffu, off, r) + ch * 16;
-        const bool ok = (mask >> r) & 1;
-        cp_async16(dst + r * S::kRow + ch * 16, static_cast<const uint8_t*>(p.c.k) + o, ok);
-        cp_async16(dst + S::kHalf + r * S::kRow + ch * 16, static_cast<const uint8_t*>(p.c.v) + o, ok);
-      }
-      if (INT8) {
-        const float* sc = lane < 16 ? p.c.k_scale : p.c.v_scale;
-        cp_async4(dst + 2 * S::kHalf + lane * 4, sc + (valid ? page * p.c.scale_page_stride + row : 0), valid);
+        for (int i = 0; i < kCopies; ++i) cp_async16(dst + in_stage(i), k + i * 512, true);
+#pragma unroll
+        for (int i = 0; i < kCopies; ++i) cp_async16(dst + S::kHalf + in_stage(i), v + i * 512, true);
+        if (INT8) {
+          const int64_t at = one * p.c.scale_page_stride + row;
+          if (kTile == 32) {
+            cp_async4(dst + 2 * S::kHalf + lane * 4, p.c.k_scale + at + lane, true);
+            cp_async4(dst + 2 * S::kHalf + 128 + lane * 4, p.c.v_scale + at + lane, true);
+          } else {
+            cp_async4(dst + 2 * S::kHalf + lane * 4, (lane < 16 ? p.c.k_scale : p.c.v_scale) + at + (lane & 15), true);
+          }
+        }
+      } else {
+        // row by row: lane r (mod the tile) looks up row r
+        const int64_t tok = tok0 + (lane & (kTile - 1));
+        const int at = static_cast<int>(tok >> shift) - window;
+        const int e0 = __shfl_sync(0xffffffffu, pages0, at & 31), e1 = __shfl_sync(0xffffffffu, pages1, at & 31);
+        const int64_t page = at < 32 ? e0 : e1;
+        const bool in = tok >= load.r.lo && tok < load.r.len;
+        const bool valid = in && page >= 0 && page < p.c.num_pages;
+        if (in && !valid) atomicOr(p.status, kErrIndex);
+        mask = __ballot_sync(0xffffffffu, valid) & kAll;
+        const int64_t row = row0 + (tok & ((1 << shift) - 1));
+        const int64_t off = valid ? (page * p.c.page_stride + row * D) * (INT8 ? 1 : 2) : 0;
+#pragma unroll
+        for (int i = 0; i < kCopies; ++i) {
+          const int r = (i * 32 + lane) / kChunks, ch = (i * 32 + lane) % kChunks;
+          const int64_t o = __shfl_sync(0xffffffffu, off, r) + ch * 16;
+          const bool ok = (mask >> r) & 1;
+          cp_async16(dst + in_stage(i), k + o, ok);
+          cp_async16(dst + S::kHalf + in_stage(i), v + o, ok);
+        }
+        if (INT8) {
+          const int64_t sat = valid ? page * p.c.scale_page_stride + row : 0;
+          if (kTile == 32 || lane < 16) cp_async4(dst + 2 * S::kHalf + (lane & (kTile - 1)) * 4, p.c.k_scale + sat, valid);
+          if (kTile == 32 || lane >= 16)
+            cp_async4(dst + 2 * S::kHalf + (kTile + (lane & (kTile - 1))) * 4, p.c.v_scale + sat, valid);
+        }
       }
       if (lane == 0) *reinterpret_cast<unsigned*>(ring + stage * S::kStage + S::kStage - 16) = mask;
-      load.next(p, units);
+      load.next(p);
     };
 
 #pragma unroll
@@ -283,11 +340,7 @@ __global__ void __launch_bounds__(S::WARPS * 32, 1) paged_attention_kernel(const
     int stage = 0, free_stage = S::STAGES - 1;
     bool fresh = true, from_start = false;
     for (int i = 0; i < n; ++i) {
-      cp_async_wait<S::STAGES - 2>();
-      __syncwarp();
-      if (i + S::STAGES - 1 < n) issue(free_stage);
-      cp_async_commit();
-      const int kvh = cur.unit / p.blocks, hb = cur.unit % p.blocks;
+      const int kvh = cur.kvh, hb = cur.hb;
       if (fresh) {  // the unit's queries; columns past its heads are zero
         from_start = cur.tile == cur.r.first;
         fresh = false;
@@ -313,52 +366,68 @@ __global__ void __launch_bounds__(S::WARPS * 32, 1) paged_attention_kernel(const
           l[nt][0] = l[nt][1] = 0.0f;
         }
       }
+      cp_async_wait<S::STAGES - 2>();
+      __syncwarp();
+      if (i + S::STAGES - 1 < n) issue(free_stage);
+      cp_async_commit();
       const uint32_t src = ring32 + stage * S::kStage;
       const uint8_t* src_p = ring + stage * S::kStage;
       const uint32_t frag = src + (lane & 15) * S::kRow + (lane >> 4) * 16;
 
-      // scores of 16 tokens x 8 heads: c0 (token g, head 2t), c1 (g, 2t + 1), c2, c3 (g + 8)
-      float s[NT][2][4];
+      // scores of 16 tokens x 8 heads: c0 (token g, head 2t), c1 (g, 2t + 1), c2, c3 (g + 8); two
+      // sums side by side, so that no instruction waits for the one before it
+      float s[MT][NT][2][4];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[nt][0][e] = s[nt][1][e] = 0.0f;
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[mt][nt][0][e] = s[mt][nt][1][e] = 0.0f;
 #pragma unroll
       for (int j = 0; j < S::kRowBytes / 32; ++j) {
-        uint32_t r[4];
-        ldmatrix(r, frag + j * 32);
-        if (INT8) {
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint32_t a0 = bytes_to_bf16(r[2 * h]), a1 = bytes_to_bf16(r[2 * h + 1]);
-            const uint32_t a2 = bytes_to_bf16(r[2 * h] >> 8), a3 = bytes_to_bf16(r[2 * h + 1] >> 8);
+        for (int mt = 0; mt < MT; ++mt) {
+          uint32_t r[4];
+          ldmatrix(r, frag + mt * 16 * S::kRow + j * 32);
+          if (INT8) {
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) mma_bf16(s[nt][h], a0, a1, a2, a3, qf[nt][2 * j + h][0], qf[nt][2 * j + h][1]);
+            for (int h = 0; h < 2; ++h) {
+              const uint32_t a0 = bytes_to_bf16(r[2 * h]), a1 = bytes_to_bf16(r[2 * h + 1]);
+              const uint32_t a2 = bytes_to_bf16(r[2 * h] >> 8), a3 = bytes_to_bf16(r[2 * h + 1] >> 8);
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+                mma_bf16(s[mt][nt][h], a0, a1, a2, a3, qf[nt][2 * j + h][0], qf[nt][2 * j + h][1]);
+            }
+          } else {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+              mma_bf16(s[mt][nt][j & 1], r[0], r[1], r[2], r[3], qf[nt][j][0], qf[nt][j][1]);
           }
-        } else {
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) mma_bf16(s[nt][j & 1], r[0], r[1], r[2], r[3], qf[nt][j][0], qf[nt][j][1]);
         }
       }
-      float ks0 = p.scale, ks1 = p.scale, vs0 = 1.0f, vs1 = 1.0f;
-      if (INT8) {
-        const float* sc = reinterpret_cast<const float*>(src_p + 2 * S::kHalf);
-        ks0 *= sc[g];
-        ks1 *= sc[g + 8];
-        vs0 = sc[16 + g];
-        vs1 = sc[24 + g];
-      }
       const unsigned mask = *reinterpret_cast<const unsigned*>(src_p + S::kStage - 16);
-      const bool ok0 = (mask >> g) & 1, ok1 = (mask >> (g + 8)) & 1;
-      uint32_t ph[NT][2], pl[NT][2];
+      const float* sc = reinterpret_cast<const float*>(src_p + 2 * S::kHalf);
+      uint32_t ph[MT][NT][2], pl[MT][NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        float x[4];
+        float x[MT][4], mn[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-        for (int e = 0; e < 4; ++e) x[e] = (s[nt][0][e] + s[nt][1][e]) * (e < 2 ? ks0 : ks1);
-        if (!ok0) x[0] = x[1] = -INFINITY;
-        if (!ok1) x[2] = x[3] = -INFINITY;
-        float mn[2] = {fmaxf(x[0], x[2]), fmaxf(x[1], x[3])};
+        for (int mt = 0; mt < MT; ++mt) {
+          const float k0 = INT8 ? p.scale * sc[mt * 16 + g] : p.scale, k1 = INT8 ? p.scale * sc[mt * 16 + g + 8] : p.scale;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[mt][e] = (s[mt][nt][0][e] + s[mt][nt][1][e]) * (e < 2 ? k0 : k1);
+        }
+        if (mask != kAll) {
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (!((mask >> (mt * 16 + g + (e < 2 ? 0 : 8))) & 1)) x[mt][e] = -INFINITY;
+        }
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) mn[e & 1] = fmaxf(mn[e & 1], x[mt][e]);
 #pragma unroll
         for (int w = 4; w < 32; w <<= 1) {
           mn[0] = fmaxf(mn[0], __shfl_xor_sync(0xffffffffu, mn[0], w));
@@ -378,41 +447,49 @@ __global__ void __launch_bounds__(S::WARPS * 32, 1) paged_attention_kernel(const
             }
           }
         }
+        const float top[2] = {m[nt][0] == -INFINITY ? 0.0f : m[nt][0], m[nt][1] == -INFINITY ? 0.0f : m[nt][1]};
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float top = m[nt][e & 1];
-          x[e] = exp2_approx(x[e] - (top == -INFINITY ? 0.0f : top));
-          l[nt][e & 1] += x[e];
-          x[e] *= e < 2 ? vs0 : vs1;
-        }
+        for (int mt = 0; mt < MT; ++mt) {
+          const float v0 = INT8 ? sc[kTile + mt * 16 + g] : 1.0f, v1 = INT8 ? sc[kTile + mt * 16 + g + 8] : 1.0f;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint32_t hi = pack_bf16(x[2 * h], x[2 * h + 1]);
-          const uint32_t lo = pack_bf16(x[2 * h] - __uint_as_float(hi << 16), x[2 * h + 1] - __uint_as_float(hi & 0xFFFF0000u));
-          ph[nt][h] = transpose8x8(hi);
-          pl[nt][h] = transpose8x8(lo);
+          for (int e = 0; e < 4; ++e) {
+            x[mt][e] = exp2_approx(x[mt][e] - top[e & 1]);
+            l[nt][e & 1] += x[mt][e];
+            if (INT8) x[mt][e] *= e < 2 ? v0 : v1;
+          }
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float y0 = x[mt][2 * h], y1 = x[mt][2 * h + 1];
+            const uint32_t hi = pack_bf16(y0, y1);
+            const uint32_t lo = pack_bf16(y0 - __uint_as_float(hi << 16), y1 - __uint_as_float(hi & 0xFFFF0000u));
+            ph[mt][nt][h] = transpose8x8(hi);
+            pl[mt][nt][h] = transpose8x8(lo);
+          }
         }
       }
 #pragma unroll
-      for (int j = 0; j < S::kRowBytes / 32; ++j) {
-        uint32_t r[4];
-        ldmatrix_t(r, frag + S::kHalf + j * 32);
-        if (INT8) {
+      for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint32_t a0 = bytes_to_bf16(r[2 * h]), a1 = bytes_to_bf16(r[2 * h] >> 8);
-            const uint32_t a2 = bytes_to_bf16(r[2 * h + 1]), a3 = bytes_to_bf16(r[2 * h + 1] >> 8);
+        for (int j = 0; j < S::kRowBytes / 32; ++j) {
+          uint32_t r[4];
+          ldmatrix_t(r, frag + S::kHalf + mt * 16 * S::kRow + j * 32);
+          if (INT8) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const uint32_t a0 = bytes_to_bf16(r[2 * h]), a1 = bytes_to_bf16(r[2 * h] >> 8);
+              const uint32_t a2 = bytes_to_bf16(r[2 * h + 1]), a3 = bytes_to_bf16(r[2 * h + 1] >> 8);
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                mma_bf16(o[nt][2 * j + h], a0, a1, a2, a3, ph[mt][nt][0], ph[mt][nt][1]);
+                mma_bf16(o[nt][2 * j + h], a0, a1, a2, a3, pl[mt][nt][0], pl[mt][nt][1]);
+              }
+            }
+          } else {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-              mma_bf16(o[nt][2 * j + h], a0, a1, a2, a3, ph[nt][0], ph[nt][1]);
-              mma_bf16(o[nt][2 * j + h], a0, a1, a2, a3, pl[nt][0], pl[nt][1]);
+              mma_bf16(o[nt][j], r[0], r[2], r[1], r[3], ph[mt][nt][0], ph[mt][nt][1]);
+              mma_bf16(o[nt][j], r[0], r[2], r[1], r[3], pl[mt][nt][0], pl[mt][nt][1]);
             }
-          }
-        } else {
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            mma_bf16(o[nt][j], r[0], r[2], r[1], r[3], ph[nt][0], ph[nt][1]);
-            mma_bf16(o[nt][j], r[0], r[2], r[1], r[3], pl[nt][0], pl[nt][1]);
           }
         }
       }
@@ -429,10 +506,10 @@ __global__ void __launch_bounds__(S::WARPS * 32, 1) paged_attention_kernel(const
         if (!whole) {
           __syncwarp();
           if (lane == 0) {
-            int64_t* u = s_unit[2 * warp + (from_start ? 1 : 0)];
-            u[0] = static_cast<int64_t>(cur.b) * units + cur.unit;
-            u[1] = cur.unit_pos;
-            u[2] = cur.unit_pos + (cur.r.last - cur.r.first);
+            const int slot = 2 * warp + (from_start ? 1 : 0);
+            s_unit[slot] = make_int4(cur.b * units + kvh * p.blocks + hb, cur.b, kvh, hb);
+            s_span[slot][0] = cur.unit_pos;
+            s_span[slot][1] = cur.unit_pos + (cur.r.last - cur.r.first);
           }
         }
 #pragma unroll
@@ -474,119 +551,128 @@ __global__ void __launch_bounds__(S::WARPS * 32, 1) paged_attention_kernel(const
           }
         }
       }
-      cur.next(p, units);
+      cur.next(p);
     }
     cp_async_wait<0>();
   }
   __syncthreads();
 
-  // the k-th partial state (warp k / 2) in shared memory
+  // the k-th partial state in shared memory
   auto part_of = [&](int k) -> const float* {
     return k & 1 ? reinterpret_cast<const float*>(smem + (k >> 1) * S::kRing)
                  : reinterpret_cast<const float*>(smem + W * S::kRing) + (k >> 1) * S::kPart;
   };
-  // one element of a whole unit
-  auto write_out = [&](int64_t unit, int hi, int d, float acc, float top, float sum) {
-    const int64_t b = unit / units;
-    const int u = static_cast<int>(unit % units), hl = u % p.blocks * S::kHeads + hi;
+  // elements d .. d + 3 of head hi of a whole unit
+  auto write_out = [&](int4 u, int hi, int d, float4 acc, float top, float sum) {
+    const int hl = u.w * S::kHeads + hi;
     if (hl >= p.group) return;
-    const int64_t h = b * p.H + static_cast<int64_t>(u / p.blocks) * p.group + hl;
-    p.out[h * D + d] = __bfloat16_as_ushort(__float2bfloat16_rn(sum != 0.0f ? acc / sum : 0.0f));
+    const int64_t h = static_cast<int64_t>(u.y) * p.H + u.z * p.group + hl;
+    const float inv = sum != 0.0f ? 1.0f / sum : 0.0f;
+    *reinterpret_cast<uint2*>(p.out + h * D + d) =
+        make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
     if (d == 0 && p.lse != nullptr) p.lse[h] = sum != 0.0f ? (top + log2f(sum)) * 0.693147180559945309f : -INFINITY;
   };
-
+  auto add = [](float4& acc, float f, float4 v) {
+    acc.x = fmaf(f, v.x, acc.x);
+    acc.y = fmaf(f, v.y, acc.y);
+    acc.z = fmaf(f, v.z, acc.z);
+    acc.w = fmaf(f, v.w, acc.w);
+  };
 
   // ---- joining within the CTA: parts of one unit follow each other in the order of the line.
-  // What is whole then is written out; at most two units reach beyond the CTA's piece (its
-  // first and its last), and leave a part in the workspace.
-  int64_t open_unit[2] = {-1, -1}, open_first[2], open_end[2];
-  for (int k = 0; k < 2 * W;) {
-    const int64_t unit = s_unit[k][0];
-    int k1 = k + 1;
-    if (unit >= 0) {
-      while (k1 < 2 * W && (s_unit[k1][0] < 0 || s_unit[k1][0] == unit)) ++k1;
-      const int64_t first = s_unit[k][1], end = s_unit[k][2];
-      const bool whole = first >= cta0 && end <= cta1;
-      const int side = first >= cta0 ? 1 : 0;
-      if (!whole) open_unit[side] = unit, open_first[side] = first, open_end[side] = end;
-      float* to = p.parts + (static_cast<int64_t>(blockIdx.x) * 2 + side) * S::kPart;
-      for (int i = threadIdx.x; i < S::kHeads * D; i += W * 32) {
-        const int hi = i / D;
-        float top = -INFINITY, sum = 0.0f, acc = 0.0f;
-        for (int j = k; j < k1; ++j)
-          if (s_unit[j][0] == unit) top = fmaxf(top, part_of(j)[S::kHeads * D + hi]);
-        for (int j = k; j < k1; ++j) {
-          if (s_unit[j][0] != unit) continue;
-          const float* part = part_of(j);
-          const float f = shrink(part[S::kHeads * D + hi], top);
-          sum = fmaf(f, part[S::kHeads * (D + 1) + hi], sum);
-          acc = fmaf(f, part[i], acc);
-        }
-        if (whole) {
-          write_out(unit, hi, i % D, acc, top, sum);
-        } else {
-          to[i] = acc;
-          if (i % D == 0) to[S::kHeads * D + hi] = top, to[S::kHeads * (D + 1) + hi] = sum;
-        }
+  // What is whole then is written out; at most two units reach beyond the CTA's piece (side 0:
+  // its first, begun before it, side 1: its last) and leave a part in the workspace.
+  static_assert(2 * W <= 32, "one lane per part");
+  const int my_unit = lane < 2 * W ? s_unit[lane].x : -1;
+  const unsigned parts = __ballot_sync(0xffffffffu, my_unit >= 0), below = parts & ((1u << lane) - 1u);
+  const int before = __shfl_sync(0xffffffffu, my_unit, below != 0 ? 31 - __clz(below) : 0);
+  const unsigned heads_of_groups = __ballot_sync(0xffffffffu, my_unit >= 0 && (below == 0 || before != my_unit));
+  // every part's factor exp2(its maximum - its unit's), a thread per part and head
+  for (int i = threadIdx.x; i < 2 * W * S::kHeads; i += W * 32) {
+    const int k = i / S::kHeads, hi = i % S::kHeads;
+    if (!((parts >> k) & 1)) continue;
+    const unsigned upto = heads_of_groups & (0xffffffffu >> (31 - k));
+    const int k0 = 31 - __clz(upto);
+    const unsigned after = k == 31 ? 0u : heads_of_groups >> (k + 1);
+    const int k1 = after != 0 ? k + __ffs(after) : 2 * W;
+    float top = -INFINITY, sum = 0.0f;
+    for (int j = k0; j < k1; ++j)
+      if ((parts >> j) & 1) top = fmaxf(top, part_of(j)[S::kHeads * D + hi]);
+    for (int j = k0; j < k1; ++j)
+      if ((parts >> j) & 1)
+        sum = fmaf(shrink(part_of(j)[S::kHeads * D + hi], top), part_of(j)[S::kHeads * (D + 1) + hi], sum);
+    s_factor[k][hi] = shrink(part_of(k)[S::kHeads * D + hi], top);
+    s_top[k][hi] = top;
+    s_sum[k][hi] = sum;
+  }
+  __syncthreads();
+  int open[2] = {-1, -1};  // the part that starts the unit left open
+  for (unsigned left = heads_of_groups; left != 0; left &= left - 1) {
+    const int k0 = __ffs(left) - 1;
+    const int k1 = (left & (left - 1)) != 0 ? __ffs(left & (left - 1)) - 1 : 2 * W;
+    const bool begun = s_span[k0][0] < cta0, whole = !begun && s_span[k0][1] <= cta1;
+    if (!whole) open[0] = begun ? k0 : open[0], open[1] = begun ? open[1] : k0;
+    float* to = p.parts + (static_cast<int64_t>(blockIdx.x) * 2 + (begun ? 0 : 1)) * S::kPart;
+    for (int i = threadIdx.x * 4; i < S::kHeads * D; i += W * 32 * 4) {
+      const int hi = i / D;
+      float4 acc = make_float4(0, 0, 0, 0);
+      for (int j = k0; j < k1; ++j)
+        if ((parts >> j) & 1) add(acc, s_factor[j][hi], *reinterpret_cast<const float4*>(part_of(j) + i));
+      if (whole) {
+        write_out(s_unit[k0], hi, i % D, acc, s_top[k0][hi], s_sum[k0][hi]);
+      } else {
+        *reinterpret_cast<float4*>(to + i) = acc;
+        if (i % D == 0) to[S::kHeads * D + hi] = s_top[k0][hi], to[S::kHeads * (D + 1) + hi] = s_sum[k0][hi];
       }
     }
-    k = k1;
   }
 
   // ---- joining across CTAs: the last one to bring its part adds them all up in order.
 #pragma unroll
   for (int side = 0; side < 2; ++side) {
-    if (open_unit[side] < 0) continue;  // uniform over the CTA
-    const int64_t unit = open_unit[side];
-    const int64_t c0 = ((open_first[side] + 1) * ctas - 1) / total, c1 = (open_end[side] * ctas - 1) / total;
-    const int count = static_cast<int>(c1 - c0 + 1);
+    if (open[side] < 0) continue;  // uniform over the CTA
+    const int4 unit = s_unit[open[side]];
     __threadfence();
     __syncthreads();
     if (threadIdx.x == 0) {
-      const bool last = atomicAdd(p.counters + unit, 1u) == static_cast<unsigned>(count - 1);
-      if (last) p.counters[unit] = 0;  // as the next call needs it
+      const int64_t c0 = divide((s_span[open[side]][0] + 1) * ctas - 1, total);
+      const int count = static_cast<int>(divide(s_span[open[side]][1] * ctas - 1, total) - c0) + 1;
+      const bool last = atomicAdd(p.counters + unit.x, 1u) == static_cast<unsigned>(count - 1);
+      if (last) p.counters[unit.x] = 0;  // as the next call needs it
+      s_from = c0;
+      s_count = count;
       s_last = last;
     }
     __syncthreads();
-    if (s_last) {
-      __threadfence();
-      // part of CTA c0 + k: its last unit (side 1) in the CTA where the unit starts, else its first
-      auto part = [&](int k) { return p.parts + ((c0 + k) * 2 + (k == 0 ? 1 : 0)) * S::kPart; };
-      float* factor = reinterpret_cast<float*>(smem);  // [heads][count]; the rings are done with
-      float* sums = factor + S::kHeads * count;        // [heads]
-      for (int hi = warp; hi < S::kHeads; hi += W) {
-        float top = -INFINITY, sum = 0.0f;
-        for (int k = lane; k < count; k += 32) top = fmaxf(top, __ldcg(part(k) + S::kHeads * D + hi));
+    if (!s_last) continue;
+    __threadfence();
+    const int count = s_count;
+    // part of the k-th CTA: side 1 in the one where the unit starts, side 0 in the others
+    const float* parts0 = p.parts + s_from * 2 * S::kPart;
+    auto part = [&](int k) { return parts0 + (2 * k + (k == 0 ? 1 : 0)) * S::kPart; };
+    float* factor = reinterpret_cast<float*>(smem);  // [heads][count]; the rings are done with
+    for (int hi = warp; hi < S::kHeads; hi += W) {
+      float top = -INFINITY, sum = 0.0f;
+      for (int k = lane; k < count; k += 32) top = fmaxf(top, __ldcg(part(k) + S::kHeads * D + hi));
 #pragma unroll
-        for (int w = 16; w > 0; w >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
-        for (int k = lane; k < count; k += 32) {
-          const float f = shrink(__ldcg(part(k) + S::kHeads * D + hi), top);
-          factor[hi * count + k] = f;
-          sum = fmaf(f, __ldcg(part(k) + S::kHeads * (D + 1) + hi), sum);
-        }
-#pragma unroll
-        for (int w = 16; w > 0; w >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
-        if (lane == 0) sums[hi] = sum, sums[S::kHeads + hi] = top;
+      for (int w = 16; w > 0; w >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
+      for (int k = lane; k < count; k += 32) {
+        const float f = shrink(__ldcg(part(k) + S::kHeads * D + hi), top);
+        factor[hi * count + k] = f;
+        sum = fmaf(f, __ldcg(part(k) + S::kHeads * (D + 1) + hi), sum);
       }
-      __syncthreads();
-      for (int i = threadIdx.x * 4; i < S::kHeads * D; i += W * 32 * 4) {
-        const int hi = i / D;
-        float4 acc = make_float4(0, 0, 0, 0);
+#pragma unroll
+      for (int w = 16; w > 0; w >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
+      if (lane == 0) s_sum[0][hi] = sum, s_top[0][hi] = top;
+    }
+    __syncthreads();
+    for (int i = threadIdx.x * 4; i < S::kHeads * D; i += W * 32 * 4) {
+      const int hi = i / D;
+      float4 acc = make_float4(0, 0, 0, 0);
 #pragma unroll 8
-        for (int k = 0; k < count; ++k) {
-          const float4 v = __ldcg(reinterpret_cast<const float4*>(part(k) + i));
-          const float f = factor[hi * count + k];
-          acc.x = fmaf(f, v.x, acc.x);
-          acc.y = fmaf(f, v.y, acc.y);
-          acc.z = fmaf(f, v.z, acc.z);
-          acc.w = fmaf(f, v.w, acc.w);
-        }
-        const float top = sums[S::kHeads + hi], sum = sums[hi];
-        write_out(unit, hi, i % D, acc.x, top, sum);
-        write_out(unit, hi, i % D + 1, acc.y, top, sum);
-        write_out(unit, hi, i % D + 2, acc.z, top, sum);
-        write_out(unit, hi, i % D + 3, acc.w, top, sum);
-      }
+      for (int k = 0; k < count; ++k)
+        add(acc, factor[hi * count + k], __ldcg(reinterpret_cast<const float4*>(part(k) + i)));
+      write_out(unit, hi, i % D, acc, s_top[0][hi], s_sum[0][hi]);
     }
   }
 
@@ -594,7 +680,7 @@ __global__ void __launch_bounds__(S::WARPS * 32, 1) paged_attention_kernel(const
   for (int b0 = (blockIdx.x * W + warp) * 32; b0 < p.B; b0 += gridDim.x * W * 32) {
     bool none = false;
     if (b0 + lane < p.B) {
-      const Range r = range_of(p, b0 + lane);
+      const Range r = range_of<S>(p, b0 + lane);
       none = r.first == r.last;
     }
     for (unsigned left = __ballot_sync(0xffffffffu, none); left != 0; left &= left - 1) {
@@ -658,17 +744,17 @@ cudaError_t launch_paged_attention(const PagedAttentionArgs& a, cudaStream_t str
   const bool wide = p.group > 8;  // 16 query heads at a time: keys and values are read half as often
   if (a.cache.int8) {
     switch (a.cache.head_dim) {
-      case 64: return wide ? launch_shape<Shape<64, true, 2, 8, 8>>(p, a, stream) : launch_shape<Shape<64, true, 1, 8, 8>>(p, a, stream);
-      case 96: return wide ? launch_shape<Shape<96, true, 2, 8, 5>>(p, a, stream) : launch_shape<Shape<96, true, 1, 8, 6>>(p, a, stream);
-      case 128: return wide ? launch_shape<Shape<128, true, 2, 8, 4>>(p, a, stream) : launch_shape<Shape<128, true, 1, 8, 5>>(p, a, stream);
-      default: return launch_shape<Shape<256, true, 1, 4, 5>>(p, a, stream);
+      case 64: return wide ? launch_shape<Shape<64, true, 2, 2, 8, 4>>(p, a, stream) : launch_shape<Shape<64, true, 1, 2, 8, 4>>(p, a, stream);
+      case 96: return wide ? launch_shape<Shape<96, true, 2, 2, 8, 2>>(p, a, stream) : launch_shape<Shape<96, true, 1, 2, 8, 3>>(p, a, stream);
+      case 128: return wide ? launch_shape<Shape<128, true, 2, 2, 8, 2>>(p, a, stream) : launch_shape<Shape<128, true, 1, 2, 8, 2>>(p, a, stream);
+      default: return launch_shape<Shape<256, true, 1, 1, 4, 5>>(p, a, stream);
     }
   }
   switch (a.cache.head_dim) {
-    case 64: return wide ? launch_shape<Shape<64, false, 2, 8, 5>>(p, a, stream) : launch_shape<Shape<64, false, 1, 8, 5>>(p, a, stream);
-    case 96: return wide ? launch_shape<Shape<96, false, 2, 8, 3>>(p, a, stream) : launch_shape<Shape<96, false, 1, 8, 3>>(p, a, stream);
-    case 128: return wide ? launch_shape<Shape<128, false, 2, 4, 5>>(p, a, stream) : launch_shape<Shape<128, false, 1, 4, 5>>(p, a, stream);
-    default: return launch_shape<Shape<256, false, 1, 3, 4>>(p, a, stream);
+    case 64: return wide ? launch_shape<Shape<64, false, 2, 2, 8, 2>>(p, a, stream) : launch_shape<Shape<64, false, 1, 2, 8, 2>>(p, a, stream);
+    case 96: return wide ? launch_shape<Shape<96, false, 2, 1, 8, 3>>(p, a, stream) : launch_shape<Shape<96, false, 1, 1, 8, 3>>(p, a, stream);
+    case 128: return wide ? launch_shape<Shape<128, false, 2, 1, 4, 5>>(p, a, stream) : launch_shape<Shape<128, false, 1, 1, 4, 5>>(p, a, stream);
+    default: return launch_shape<Shape<256, false, 1, 1, 3, 4>>(p, a, stream);
   }
 }
 
