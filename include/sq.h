@@ -461,7 +461,8 @@ SQ_API sq_status sq_rope_kv_append(const void* q_bf16, int64_t ldq, const void* 
  * included) are never used. The work is split over the sequences' lengths and joined in a
  * fixed order: the same inputs give the same bits.
  * q: bf16 [B, H, head_dim], sequence stride ldq (a multiple of 8). H a multiple of the cache's
- * heads. block_table: int32 [B, max_pages], row stride ld_table. seq_lens: int32 [B].
+ * heads. block_table: int32 [B, max_pages], row stride ld_table,
+ * max_pages * page_size < 2^31 - 64. seq_lens: int32 [B].
  * out: bf16 [B, H, head_dim] dense. lse: fp32 [B, H] or NULL. 1 <= B <= 65535.
  * A page index out of range hides its tokens, a negative length counts as 0 and one past
  * max_pages * page_size as that; each records SQ_ERR_BOUNDS (see sq_sync_status).

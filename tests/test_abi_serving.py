@@ -108,7 +108,7 @@ def test_append_refusals(bad, code):
 @pytest.mark.parametrize("bad,code", [
     (dict(q=None), INV), (dict(ldq=128), INV), (dict(ldq=260), ALIGN), (dict(B=0), INV), (dict(B=65536), INV),
     (dict(H=0), INV), (dict(H=3), INV), (dict(H=1026), INV), (dict(table=None), INV), (dict(table=FAKE + 1), ALIGN),
-    (dict(ld=4), INV), (dict(pages=0), INV), (dict(lens=None), INV), (dict(window=-1), INV),
+    (dict(ld=4), INV), (dict(pages=0), INV), (dict(pages=1 << 27, ld=1 << 27), INV), (dict(lens=None), INV), (dict(window=-1), INV),
     (dict(scale=float("nan")), INV), (dict(scale=float("inf")), INV), (dict(out=None), INV), (dict(out=FAKE + 8), ALIGN),
     (dict(lse=FAKE + 2), ALIGN)])
 def test_attention_refusals(bad, code):

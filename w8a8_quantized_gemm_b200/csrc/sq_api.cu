@@ -687,8 +687,9 @@ sq_status sq_paged_attention(const void* q_bf16, int64_t ldq, int64_t B, int64_t
   if (lse != nullptr && (reinterpret_cast<uintptr_t>(lse) & 3u)) return fail(SQ_ERR_ALIGN, "%s: lse not aligned", fn);
   if ((st = check_index(fn, "block_table", block_table)) != SQ_OK) return st;
   if ((st = check_index(fn, "seq_lens", seq_lens)) != SQ_OK) return st;
-  if (max_pages < 1 || max_pages > kMaxRows || ld_table < max_pages)
-    return fail(SQ_ERR_INVALID, "%s: max_pages=%lld, row stride %lld", fn, static_cast<long long>(max_pages),
+  if (max_pages < 1 || max_pages > (kMaxRows - 64) / cache->page_size || ld_table < max_pages)
+    return fail(SQ_ERR_INVALID, "%s: max_pages=%lld must be positive, max_pages * page_size below 2^31 - 64 and the "
+                "table's row stride %lld at least max_pages", fn, static_cast<long long>(max_pages),
                 static_cast<long long>(ld_table));
   if (window < 0) return fail(SQ_ERR_INVALID, "%s: window must not be negative", fn);
   if (!(scale == scale) || scale == INFINITY || scale == -INFINITY)

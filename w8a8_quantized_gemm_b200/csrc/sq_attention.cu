@@ -14,17 +14,26 @@
 // the last CTA to arrive adds the parts up in the order of the line. So results do not depend
 // on which CTA is last.
 //
-// Matrix instructions (16x8x16, bf16 in, fp32 sums): scores are K (16 tokens x head_dim) times
-// q^T (head_dim x 8 heads), outputs V^T (16 elements x 16 tokens) times p^T (16 tokens x 8
-// heads): tokens and elements fill the 16 rows, heads the 8 columns. int8 codes become bf16
-// exactly in registers: with s the sign bit of a byte, 128 + (low 7 bits) and 128 + 128 s are
-// both bf16 numbers made by one logic operation each, and their difference is the code. The
-// fp32 probabilities (times a token's value scale) enter as two bf16 parts, high and low, so
-// that the rounding of out to bf16 is the only one that counts.
+// Matrix instructions: scores are K (16 tokens x head_dim) times q^T (head_dim x 8 heads), outputs
+// V^T (16 elements x 16 tokens) times p^T (16 tokens x 8 heads): tokens and elements fill the 16
+// rows, heads the 8 columns, all sums fp32 (int8 scores: int32). A bf16 cache takes 16x8x16
+// instructions as it is. For an int8 cache, turning codes into 16-bit floats costs more
+// instructions than all the rest, so
+//   - scores use the 16x8x32 int8 instructions: a query, scaled by a power of two to 23 bits,
+//     is split into three signed bytes and the three exact products are put together again
+//     (elements down to 2^-14 of the head's largest are exact, smaller ones off by 2^-23 of it);
+//   - values become fp16 exactly: (byte ^ 0x80) + 1024 has the byte's bits as its mantissa, one
+//     logic operation, and 1152 less is the code.
+// The probabilities enter as a high and a low 16-bit part, so that the rounding of out to bf16
+// is the only one that counts. For an int8 cache they carry the token's value scale vs: the
+// running maximum is then that of s + log2(vs), which keeps the products within [0, 1], in
+// fp16's range whatever the scales.
 #include "sq_internal.h"
 #include "sq_ptx.cuh"
+#include "sq_rows.cuh"
 
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 
 #include <algorithm>
 #include <cmath>
@@ -38,9 +47,10 @@ struct AttnParams {
   int B, H;
   KvView c;
   const int32_t* table;
-  int64_t ld_table, max_pages;
+  int64_t ld_table;
+  int max_pages, max_len;  // max_len: what the table's rows can hold, at most 2^31 - 1
   const int32_t* seq_lens;
-  int64_t window;
+  int window;   // 2^31 - 1: the whole sequence
   float scale;  // times log2(e)
   uint16_t* out;
   float* lse;
@@ -102,6 +112,19 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_s8(int (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
 __device__ __forceinline__ float exp2_approx(float x) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -111,29 +134,40 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 r = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&r);
 }
-// The signed bytes 0 and 2 of w as a bf16 pair, exactly.
-__device__ __forceinline__ uint32_t bytes_to_bf16(uint32_t w) {
-  const uint32_t a = (w & 0x007F007Fu) | 0x43004300u, b = (w & 0x00800080u) | 0x43004300u;
-  const __nv_bfloat162 r =
-      __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
+__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+// The signed bytes 0 and 2 of w as an fp16 pair, exactly: byte + 1152, less 1152.
+__device__ __forceinline__ uint32_t bytes_to_f16(uint32_t w) {
+  const uint32_t a = (w & 0x00FF00FFu) ^ 0x64806480u, b = 0x64806480u;
+  const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
   return *reinterpret_cast<const uint32_t*>(&r);
+}
+// Pairs of values as the sum of a high and a low 16-bit float.
+__device__ __forceinline__ void split_f16(float a, float b, uint32_t& hi, uint32_t& lo) {
+  const __half2 h = __floats2half2_rn(a, b);
+  const float2 f = __half22float2(h);
+  const __half2 r = __floats2half2_rn(a - f.x, b - f.y);
+  hi = *reinterpret_cast<const uint32_t*>(&h);
+  lo = *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ void split_bf16(float a, float b, uint32_t& hi, uint32_t& lo) {
+  hi = pack_bf16(a, b);
+  lo = pack_bf16(a - bf16_lo(hi), b - bf16_hi(hi));
 }
 // exp2(a - b) of two running maxima; nothing came before a maximum of -inf.
 __device__ __forceinline__ float shrink(float a, float b) { return a == -INFINITY ? 0.0f : exp2_approx(a - b); }
 
 // The tokens lo <= t < len that sequence b attends to, and its tiles first <= i < last.
 struct Range {
-  int64_t lo, len;
-  int first, last;
+  int lo, len, first, last;
 };
 template <typename S>
 __device__ __forceinline__ Range range_of(const AttnParams& p, int b) {
   Range r;
-  r.len = __ldg(p.seq_lens + b);
-  r.len = min(max(r.len, int64_t(0)), p.max_pages << p.c.page_shift);
-  r.lo = p.window > 0 && r.len > p.window ? r.len - p.window : 0;
-  r.first = static_cast<int>(r.lo / S::kTile);
-  r.last = r.len > 0 ? static_cast<int>((r.len + S::kTile - 1) / S::kTile) : r.first;
+  r.len = min(max(__ldg(p.seq_lens + b), 0), p.max_len);
+  r.lo = r.len > p.window ? r.len - p.window : 0;
+  r.first = static_cast<unsigned>(r.lo) / S::kTile;
+  r.last = r.len > 0 ? static_cast<int>((static_cast<unsigned>(r.len) + S::kTile - 1) / S::kTile) : r.first;
   return r;
 }
 
@@ -248,11 +282,9 @@ __global__ void __launch_bounds__(S::WARPS * 32, 1) paged_attention_kernel(const
     Cursor<S> load = cursor_at<S>(p, units, p0, lane), cur = load;
     const int n = static_cast<int>(p1 - p0);
     const int shift = p.c.page_shift;
-    // page table entries window .. window + 63 of sequence window_b, one of each half per lane
-    int window = 0, window_b = -1, pages0 = 0, pages1 = 0;
-    auto entry = [&](int b, int64_t i) {
-      return i < p.max_pages ? __ldg(p.table + b * p.ld_table + i) : -1;
-    };
+    // page table entries win .. win + 63 of sequence win_b, one of each half per lane
+    int win = 0, win_b = -1, pages0 = 0, pages1 = 0;
+    auto entry = [&](int b, int i) { return i < p.max_pages ? __ldg(p.table + b * p.ld_table + i) : -1; };
     const bool paged = (1 << shift) >= kTile;  // a tile lies in one page, its rows one after another
     constexpr int kChunks = S::kRowBytes / 16, kCopies = kTile * kChunks / 32;
     // place of copy i of this lane: row (32 i + lane) / kChunks
@@ -260,29 +292,28 @@ __global__ void __launch_bounds__(S::WARPS * 32, 1) paged_attention_kernel(const
       return static_cast<uint32_t>((i * 32 + lane) / kChunks * S::kRow + (i * 32 + lane) % kChunks * 16);
     };
     auto issue = [&](int stage) {
-      const int64_t tok0 = static_cast<int64_t>(load.tile) * kTile;
-      const int first_page = static_cast<int>(tok0 >> shift);
-      const int last_page = static_cast<int>((tok0 + kTile - 1) >> shift);
-      if (load.b != window_b || first_page < window || last_page >= window + 64) {
-        window = first_page;
-        window_b = load.b;
-        pages0 = entry(load.b, static_cast<int64_t>(window) + lane);
-        pages1 = entry(load.b, static_cast<int64_t>(window) + 32 + lane);
-      } else if (first_page >= window + 32) {
-        window += 32;
+      const int tok0 = load.tile * kTile;
+      const int first_page = tok0 >> shift, last_page = (tok0 + (kTile - 1)) >> shift;
+      if (load.b != win_b || first_page < win || last_page >= win + 64) {
+        win = first_page;
+        win_b = load.b;
+        pages0 = entry(win_b, win + lane);
+        pages1 = entry(win_b, win + 32 + lane);
+      } else if (first_page >= win + 32) {
+        win += 32;
         pages0 = pages1;
-        pages1 = entry(load.b, static_cast<int64_t>(window) + 32 + lane);
+        pages1 = entry(win_b, win + 32 + lane);
       }
       const uint32_t dst = ring32 + stage * S::kStage;
       const uint8_t *k = static_cast<const uint8_t*>(p.c.k), *v = static_cast<const uint8_t*>(p.c.v);
       const int64_t row0 = static_cast<int64_t>(load.kvh) << shift;
       unsigned mask = kAll;
-      const int64_t one = __shfl_sync(0xffffffffu, pages0, (first_page - window) & 31);
-      if (paged && first_page < window + 32 && tok0 >= load.r.lo && tok0 + kTile <= load.r.len && one >= 0 &&
+      const int one = __shfl_sync(0xffffffffu, pages0, (first_page - win) & 31);
+      if (paged && first_page < win + 32 && tok0 >= load.r.lo && tok0 + kTile <= load.r.len && one >= 0 &&
           one < p.c.num_pages) {
         // whole tile: contiguous
         const int64_t row = row0 + (tok0 & ((1 << shift) - 1));
-        const int64_t off = (one * p.c.page_stride + row * D) * (INT8 ? 1 : 2) + lane * 16;
+        const int64_t off = (p.c.page_stride * one + row * D) * (INT8 ? 1 : 2) + lane * 16;
         k += off;
         v += off;
 #pragma unroll
@@ -290,7 +321,7 @@ __global__ void __launch_bounds__(S::WARPS * 32, 1) paged_attention_kernel(const
 #pragma unroll
         for (int i = 0; i < kCopies; ++i) cp_async16(dst + S::kHalf + in_stage(i), v + i * 512, true);
         if (INT8) {
-          const int64_t at = one * p.c.scale_page_stride + row;
+          const int64_t at = p.c.scale_page_stride * one + row;
           if (kTile == 32) {
             cp_async4(dst + 2 * S::kHalf + lane * 4, p.c.k_scale + at + lane, true);
             cp_async4(dst + 2 * S::kHalf + 128 + lane * 4, p.c.v_scale + at + lane, true);
@@ -300,8 +331,7 @@ __global__ void __launch_bounds__(S::WARPS * 32, 1) paged_attention_kernel(const
         }
       } else {
         // row by row: lane r (mod the tile) looks up row r
-        const int64_t tok = tok0 + (lane & (kTile - 1));
-        const int at = static_cast<int>(tok >> shift) - window;
+        const int tok = tok0 + (lane & (kTile - 1)), at = (tok >> shift) - win;
         const int e0 = __shfl_sync(0xffffffffu, pages0, at & 31), e1 = __shfl_sync(0xffffffffu, pages1, at & 31);
         const int64_t page = at < 32 ? e0 : e1;
         const bool in = tok >= load.r.lo && tok < load.r.len;
@@ -329,105 +359,170 @@ __global__ void __launch_bounds__(S::WARPS * 32, 1) paged_attention_kernel(const
       load.next(p);
     };
 
-#pragma unroll
-    for (int s = 0; s < S::STAGES - 1; ++s) {
-      if (s < n) issue(s);
-      cp_async_commit();
-    }
-
-    uint32_t qf[NT][kSteps][2];
-    float o[NT][kSteps][4], m[NT][2], l[NT][2];
-    int stage = 0, free_stage = S::STAGES - 1;
+    // the queries' operand fragments: bf16 pairs, or the three bytes' words; per head the factor
+    // that turns an int8 score into an exponent of 2
+    constexpr int kParts = INT8 ? 3 : 1, kWords = INT8 ? D / 32 : D / 16;
+    uint32_t qf[NT][kParts][kWords][2];
+    float o[NT][kSteps][4], m[NT][2], l[NT][2], factor[NT][2];
+    int stage = 0, load_stage = 0;
     bool fresh = true, from_start = false;
-    for (int i = 0; i < n; ++i) {
+    for (int i = 1 - S::STAGES; i < n; ++i) {
       const int kvh = cur.kvh, hb = cur.hb;
-      if (fresh) {  // the unit's queries; columns past its heads are zero
+      if (i >= 0 && fresh) {  // the unit's queries; columns past its heads are zero
         from_start = cur.tile == cur.r.first;
         fresh = false;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           const int hl = hb * S::kHeads + nt * 8 + g;
           const uint16_t* qr = p.q + cur.b * p.ldq + (static_cast<int64_t>(kvh) * p.group + hl) * D;
+          if (INT8) {
+            uint2 w[kWords][2];
+            float top = 0.0f;
 #pragma unroll
-          for (int j = 0; j < kSteps; ++j) {
-            if (INT8) {  // the order in which a byte row's words give their even and odd codes
-              uint2 w = make_uint2(0, 0);
-              if (hl < p.group) w = __ldg(reinterpret_cast<const uint2*>(qr + 16 * j + 4 * t));
-              qf[nt][j][0] = __byte_perm(w.x, w.y, 0x5410);
-              qf[nt][j][1] = __byte_perm(w.x, w.y, 0x7632);
-            } else {
-              qf[nt][j][0] = hl < p.group ? __ldg(reinterpret_cast<const uint32_t*>(qr + 16 * j + 2 * t)) : 0u;
-              qf[nt][j][1] = hl < p.group ? __ldg(reinterpret_cast<const uint32_t*>(qr + 16 * j + 8 + 2 * t)) : 0u;
-            }
+            for (int j = 0; j < kWords; ++j)
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                w[j][h] = make_uint2(0, 0);
+                if (hl < p.group) w[j][h] = __ldg(reinterpret_cast<const uint2*>(qr + 32 * j + 16 * h + 4 * t));
+              }
+#pragma unroll
+            for (int j = 0; j < kWords; ++j)
+#pragma unroll
+              for (int h = 0; h < 2; ++h)
+                top = fmaxf(fmaxf(top, fmaxf(fabsf(bf16_lo(w[j][h].x)), fabsf(bf16_hi(w[j][h].x)))),
+                            fmaxf(fabsf(bf16_lo(w[j][h].y)), fabsf(bf16_hi(w[j][h].y))));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            // 2^up brings the largest below 2^22
+            const int up = min(22 + 126 - static_cast<int>(__float_as_uint(top) >> 23), 120);
+            const float mul = __uint_as_float(static_cast<uint32_t>(up + 127) << 23);
+#pragma unroll
+            for (int j = 0; j < kWords; ++j)
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const int v[4] = {__float2int_rn(bf16_lo(w[j][h].x) * mul), __float2int_rn(bf16_hi(w[j][h].x) * mul),
+                                  __float2int_rn(bf16_lo(w[j][h].y) * mul), __float2int_rn(bf16_hi(w[j][h].y) * mul)};
+                int a[4], b[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  b[e] = (v[e] - static_cast<int8_t>(v[e])) >> 8;
+                  a[e] = (b[e] - static_cast<int8_t>(b[e])) >> 8;
+                }
+                qf[nt][0][j][h] = rows::pack4(a[0], a[1], a[2], a[3]);
+                qf[nt][kParts / 2][j][h] = rows::pack4(b[0], b[1], b[2], b[3]);
+                qf[nt][kParts - 1][j][h] = rows::pack4(v[0], v[1], v[2], v[3]);
+              }
+            const float back = p.scale * __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
+            factor[nt][0] = __shfl_sync(0xffffffffu, back, 8 * t);
+            factor[nt][1] = __shfl_sync(0xffffffffu, back, 8 * t + 4);
+          } else {
+#pragma unroll
+            for (int j = 0; j < kWords; ++j)
+#pragma unroll
+              for (int h = 0; h < 2; ++h)
+                qf[nt][0][j][h] = hl < p.group ? __ldg(reinterpret_cast<const uint32_t*>(qr + 16 * j + 8 * h + 2 * t)) : 0u;
+            factor[nt][0] = factor[nt][1] = p.scale;
+          }
+#pragma unroll
+          for (int j = 0; j < kSteps; ++j)
 #pragma unroll
             for (int e = 0; e < 4; ++e) o[nt][j][e] = 0.0f;
-          }
           m[nt][0] = m[nt][1] = -INFINITY;
           l[nt][0] = l[nt][1] = 0.0f;
         }
       }
+      // the next tile's copies go where the previous tile was; the first rounds only start copies
       cp_async_wait<S::STAGES - 2>();
       __syncwarp();
-      if (i + S::STAGES - 1 < n) issue(free_stage);
+      if (i + S::STAGES - 1 < n) issue(load_stage);
       cp_async_commit();
+      load_stage = load_stage + 1 == S::STAGES ? 0 : load_stage + 1;
+      if (i < 0) continue;
       const uint32_t src = ring32 + stage * S::kStage;
       const uint8_t* src_p = ring + stage * S::kStage;
       const uint32_t frag = src + (lane & 15) * S::kRow + (lane >> 4) * 16;
 
-      // scores of 16 tokens x 8 heads: c0 (token g, head 2t), c1 (g, 2t + 1), c2, c3 (g + 8); two
-      // sums side by side, so that no instruction waits for the one before it
-      float s[MT][NT][2][4];
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) s[mt][nt][0][e] = s[mt][nt][1][e] = 0.0f;
-#pragma unroll
-      for (int j = 0; j < S::kRowBytes / 32; ++j) {
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-          uint32_t r[4];
-          ldmatrix(r, frag + mt * 16 * S::kRow + j * 32);
-          if (INT8) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const uint32_t a0 = bytes_to_bf16(r[2 * h]), a1 = bytes_to_bf16(r[2 * h + 1]);
-              const uint32_t a2 = bytes_to_bf16(r[2 * h] >> 8), a3 = bytes_to_bf16(r[2 * h + 1] >> 8);
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt)
-                mma_bf16(s[mt][nt][h], a0, a1, a2, a3, qf[nt][2 * j + h][0], qf[nt][2 * j + h][1]);
-            }
-          } else {
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-              mma_bf16(s[mt][nt][j & 1], r[0], r[1], r[2], r[3], qf[nt][j][0], qf[nt][j][1]);
-          }
-        }
-      }
-      const unsigned mask = *reinterpret_cast<const unsigned*>(src_p + S::kStage - 16);
-      const float* sc = reinterpret_cast<const float*>(src_p + 2 * S::kHalf);
-      uint32_t ph[MT][NT][2], pl[MT][NT][2];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        float x[MT][4], mn[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-          const float k0 = INT8 ? p.scale * sc[mt * 16 + g] : p.scale, k1 = INT8 ? p.scale * sc[mt * 16 + g + 8] : p.scale;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) x[mt][e] = (s[mt][nt][0][e] + s[mt][nt][1][e]) * (e < 2 ? k0 : k1);
-        }
-        if (mask != kAll) {
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (!((mask >> (mt * 16 + g + (e < 2 ? 0 : 8))) & 1)) x[mt][e] = -INFINITY;
-        }
+      // scores of 16 tokens x 8 heads: c0 (token g, head 2t), c1 (g, 2t + 1), c2, c3 (g + 8)
+      float x[MT][NT][4];
+      if constexpr (INT8) {
+        int c[MT][NT][3][4];
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) mn[e & 1] = fmaxf(mn[e & 1], x[mt][e]);
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 12; ++e) c[mt][nt][e / 4][e % 4] = 0;
+#pragma unroll
+        for (int j = 0; j < kWords; ++j)
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            uint32_t r[4];
+            ldmatrix(r, frag + mt * 16 * S::kRow + j * 32);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int d = 0; d < 3; ++d) mma_s8(c[mt][nt][d], r, qf[nt][d][j][0], qf[nt][d][j][1]);
+          }
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              x[mt][nt][e] = fmaf(static_cast<float>(c[mt][nt][0][e] * 256 + c[mt][nt][1][e]), 256.0f,
+                                  static_cast<float>(c[mt][nt][2][e]));
+      } else {
+        float c[MT][NT][2][4];  // two sums side by side, so that no instruction waits for the one before it
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) c[mt][nt][e / 4][e % 4] = 0.0f;
+#pragma unroll
+        for (int j = 0; j < kWords; ++j)
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            uint32_t r[4];
+            ldmatrix(r, frag + mt * 16 * S::kRow + j * 32);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+              mma_bf16(c[mt][nt][j & 1], r[0], r[1], r[2], r[3], qf[nt][0][j][0], qf[nt][0][j][1]);
+          }
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[mt][nt][e] = c[mt][nt][0][e] + c[mt][nt][1][e];
+      }
+      const unsigned mask = *reinterpret_cast<const unsigned*>(src_p + S::kStage - 16);
+      const float* sc = reinterpret_cast<const float*>(src_p + 2 * S::kHalf);
+      // per token of this lane (rows g and g + 8 of each 16): the key's scale, the value's and its log2
+      float ks[MT][2], vs[MT][2], lv[MT][2];
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int row = mt * 16 + h * 8 + g;
+          ks[mt][h] = INT8 ? sc[row] : 1.0f;
+          vs[mt][h] = INT8 ? sc[kTile + row] : 1.0f;
+          lv[mt][h] = INT8 ? __log2f(fmaxf(vs[mt][h], 7.888609e-31f)) : 0.0f;  // 2^-100: finite for a row of zeros
+          vs[mt][h] *= INT8 ? 16384.0f : 1.0f;
+        }
+      uint32_t ph[MT][NT][2], pl[MT][NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float mn[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float& v = x[mt][nt][e];
+            v *= INT8 ? factor[nt][e & 1] * ks[mt][e / 2] : factor[nt][e & 1];
+            if (mask != kAll && !((mask >> (mt * 16 + (e / 2) * 8 + g)) & 1)) v = -INFINITY;
+            mn[e & 1] = fmaxf(mn[e & 1], v + lv[mt][e / 2]);
+          }
 #pragma unroll
         for (int w = 4; w < 32; w <<= 1) {
           mn[0] = fmaxf(mn[0], __shfl_xor_sync(0xffffffffu, mn[0], w));
@@ -450,18 +545,16 @@ __global__ void __launch_bounds__(S::WARPS * 32, 1) paged_attention_kernel(const
         const float top[2] = {m[nt][0] == -INFINITY ? 0.0f : m[nt][0], m[nt][1] == -INFINITY ? 0.0f : m[nt][1]};
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
-          const float v0 = INT8 ? sc[kTile + mt * 16 + g] : 1.0f, v1 = INT8 ? sc[kTile + mt * 16 + g + 8] : 1.0f;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            x[mt][e] = exp2_approx(x[mt][e] - top[e & 1]);
-            l[nt][e & 1] += x[mt][e];
-            if (INT8) x[mt][e] *= e < 2 ? v0 : v1;
-          }
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const float y0 = x[mt][2 * h], y1 = x[mt][2 * h + 1];
-            const uint32_t hi = pack_bf16(y0, y1);
-            const uint32_t lo = pack_bf16(y0 - __uint_as_float(hi << 16), y1 - __uint_as_float(hi & 0xFFFF0000u));
+            const float e0 = exp2_approx(x[mt][nt][2 * h] - top[0]), e1 = exp2_approx(x[mt][nt][2 * h + 1] - top[1]);
+            l[nt][0] += e0;
+            l[nt][1] += e1;
+            uint32_t hi, lo;
+            if (INT8)
+              split_f16(e0 * vs[mt][h], e1 * vs[mt][h], hi, lo);
+            else
+              split_bf16(e0, e1, hi, lo);
             ph[mt][nt][h] = transpose8x8(hi);
             pl[mt][nt][h] = transpose8x8(lo);
           }
@@ -473,15 +566,15 @@ __global__ void __launch_bounds__(S::WARPS * 32, 1) paged_attention_kernel(const
         for (int j = 0; j < S::kRowBytes / 32; ++j) {
           uint32_t r[4];
           ldmatrix_t(r, frag + S::kHalf + mt * 16 * S::kRow + j * 32);
-          if (INT8) {
+          if constexpr (INT8) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              const uint32_t a0 = bytes_to_bf16(r[2 * h]), a1 = bytes_to_bf16(r[2 * h] >> 8);
-              const uint32_t a2 = bytes_to_bf16(r[2 * h + 1]), a3 = bytes_to_bf16(r[2 * h + 1] >> 8);
+              const uint32_t a0 = bytes_to_f16(r[2 * h]), a1 = bytes_to_f16(r[2 * h] >> 8);
+              const uint32_t a2 = bytes_to_f16(r[2 * h + 1]), a3 = bytes_to_f16(r[2 * h + 1] >> 8);
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt) {
-                mma_bf16(o[nt][2 * j + h], a0, a1, a2, a3, ph[mt][nt][0], ph[mt][nt][1]);
-                mma_bf16(o[nt][2 * j + h], a0, a1, a2, a3, pl[mt][nt][0], pl[mt][nt][1]);
+                mma_f16(o[nt][2 * j + h], a0, a1, a2, a3, ph[mt][nt][0], ph[mt][nt][1]);
+                mma_f16(o[nt][2 * j + h], a0, a1, a2, a3, pl[mt][nt][0], pl[mt][nt][1]);
               }
             }
           } else {
@@ -493,7 +586,6 @@ __global__ void __launch_bounds__(S::WARPS * 32, 1) paged_attention_kernel(const
           }
         }
       }
-      free_stage = stage;
       stage = stage + 1 == S::STAGES ? 0 : stage + 1;
 
       const bool ends = cur.tile + 1 == cur.r.last;
@@ -521,15 +613,16 @@ __global__ void __launch_bounds__(S::WARPS * 32, 1) paged_attention_kernel(const
             for (int w = 4; w < 32; w <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
             const int hi = nt * 8 + 2 * t + e, hl = hb * S::kHeads + hi;  // head in the unit, in its group
             const int h = kvh * p.group + hl;
-            const float inv = sum != 0.0f ? 1.0f / sum : 0.0f;
+            const float unit = INT8 ? 1.0f / 16384 : 1.0f;  // of the probabilities' parts
+            const float inv = sum != 0.0f ? unit / sum : 0.0f;
             uint16_t* out = p.out + (static_cast<int64_t>(cur.b) * p.H + h) * D;
 #pragma unroll
             for (int j = 0; j < kSteps; ++j) {
               const int d0 = 16 * j + (INT8 ? 2 * g : g), d1 = INT8 ? d0 + 1 : d0 + 8;
               const float v0 = o[nt][j][e], v1 = o[nt][j][e + 2];
               if (!whole) {
-                part[hi * D + d0] = v0;
-                part[hi * D + d1] = v1;
+                part[hi * D + d0] = v0 * unit;
+                part[hi * D + d1] = v1 * unit;
               } else if (hl < p.group) {
                 if (INT8) {
                   *reinterpret_cast<uint32_t*>(out + d0) = pack_bf16(v0 * inv, v1 * inv);
@@ -628,15 +721,16 @@ __global__ void __launch_bounds__(S::WARPS * 32, 1) paged_attention_kernel(const
   }
 
   // ---- joining across CTAs: the last one to bring its part adds them all up in order.
-#pragma unroll
+#pragma unroll 1
   for (int side = 0; side < 2; ++side) {
-    if (open[side] < 0) continue;  // uniform over the CTA
-    const int4 unit = s_unit[open[side]];
+    const int mine = side == 0 ? open[0] : open[1];
+    if (mine < 0) continue;  // uniform over the CTA
+    const int4 unit = s_unit[mine];
     __threadfence();
     __syncthreads();
     if (threadIdx.x == 0) {
-      const int64_t c0 = divide((s_span[open[side]][0] + 1) * ctas - 1, total);
-      const int count = static_cast<int>(divide(s_span[open[side]][1] * ctas - 1, total) - c0) + 1;
+      const int64_t c0 = divide((s_span[mine][0] + 1) * ctas - 1, total);
+      const int count = static_cast<int>(divide(s_span[mine][1] * ctas - 1, total) - c0) + 1;
       const bool last = atomicAdd(p.counters + unit.x, 1u) == static_cast<unsigned>(count - 1);
       if (last) p.counters[unit.x] = 0;  // as the next call needs it
       s_from = c0;
@@ -731,9 +825,10 @@ cudaError_t launch_paged_attention(const PagedAttentionArgs& a, cudaStream_t str
   p.c = a.cache;
   p.table = a.table;
   p.ld_table = a.ld_table;
-  p.max_pages = a.max_pages;
+  p.max_pages = static_cast<int>(a.max_pages);
+  p.max_len = static_cast<int>(std::min<int64_t>(a.max_pages << a.cache.page_shift, INT32_MAX));
   p.seq_lens = a.seq_lens;
-  p.window = a.window;
+  p.window = a.window == 0 ? INT32_MAX : static_cast<int>(std::min<int64_t>(a.window, INT32_MAX));
   p.scale = a.scale * 1.44269504088896341f;
   p.out = a.out;
   p.lse = a.lse;
