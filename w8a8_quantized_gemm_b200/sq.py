@@ -308,30 +308,38 @@ def sq_weight_row_sums(Wq, rowsum, stream=None):
 
 
 # ---------------------------------------------------------------- 4-bit weights
-def _here(*tensors):
-    """The device index of the given tensors (None entries skipped), which must be CUDA tensors
-    on the current device: the library launches there."""
+# These calls run once per layer and token, so their checks are kept to a few microseconds.
+def _device(t, name):
+    """Device index of a CUDA tensor, which must be the current device: the library launches there."""
     torch = _torch()
-    dev = None
-    for t in tensors:
-        if t is None:
-            continue
-        if not isinstance(t, torch.Tensor) or not t.is_cuda:
-            raise TypeError("tensors must be CUDA tensors")
-        dev = torch.cuda.current_device() if dev is None else dev
-        if t.get_device() != dev:
-            raise ValueError(f"tensor on {t.device}, but the current device is cuda:{dev}")
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    dev = t.get_device()
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, but the current device is cuda:{torch.cuda.current_device()}")
     return dev
 
 
-def _dense(t, dtype, shape, name):
+def _on(stream, dev):
+    """The handle of `stream`, or of the current one (without making a Stream object for it)."""
+    raw = getattr(_torch()._C, "_cuda_getCurrentRawStream", None)
+    return raw(dev) if stream is None and raw is not None else _stream(stream)
+
+
+def _typed(t, dtype, name, dev):
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, other tensors on cuda:{dev}")
+
+
+def _dense(t, dtype, shape, name, dev):
     """Data pointer of a contiguous tensor of exactly this type and shape (None passes)."""
     if t is None:
         return None
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    _typed(t, dtype, name, dev)
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     return t.data_ptr()
@@ -341,46 +349,46 @@ def sq_int4_weight_bytes(N: int, K: int) -> int:
     return int(_lib.sq_int4_weight_bytes(int(N), int(K)))
 
 
-def _int4(Wp, w_scale, w_zero, group, N, K):
+def _int4(Wp, w_scale, w_zero, group, N, K, dev):
     torch = _torch()
-    groups = -(-K // group) if group > 0 else 0
-    return (_dense(Wp, torch.uint8, (sq_int4_weight_bytes(N, K),), "Wp"),
-            _dense(w_scale, torch.bfloat16, (groups, N), "w_scale"),
-            _dense(w_zero, torch.uint8, (groups, N), "w_zero"))
+    groups = (-(-K // group) if group > 0 else 0, N)
+    return (_dense(Wp, torch.uint8, (-(-N // 16) * -(-K // 128) * 1024,), "Wp", dev),
+            _dense(w_scale, torch.bfloat16, groups, "w_scale", dev), _dense(w_zero, torch.uint8, groups, "w_zero", dev))
 
 
 def sq_quant_weight_int4(W, s, group: int, Wp, w_scale, w_zero=None, stream=None):
     """4-bit codes and group scales of W [N, K] (times s); with w_zero, zero points too."""
     torch = _torch()
+    dev = _device(W, "W")
+    w = _ptr(W, torch.bfloat16, "W", True)
     N, K = W.shape
-    _here(W, s, Wp, w_scale, w_zero)
-    p, e, z = _int4(Wp, w_scale, w_zero, group, N, K)
-    _check(_lib.sq_quant_weight_int4(_ptr(W, torch.bfloat16, "W", True), N, K, W.stride(0),
-                                     _dense(s, torch.float32, (K,), "s"), int(group), p, e, z, _stream(stream)))
+    p, e, z = _int4(Wp, w_scale, w_zero, group, N, K, dev)
+    _check(_lib.sq_quant_weight_int4(w, N, K, W.stride(0), _dense(s, torch.float32, (K,), "s", dev), group, p, e, z,
+                                     _on(stream, dev)))
     return Wp, w_scale, w_zero
 
 
 def sq_dequant_weight_int4(Wp, w_scale, w_zero, group: int, out, stream=None):
     """The bf16 values [N, K] (the shape of `out`) that a 4-bit weight stands for."""
     torch = _torch()
+    dev = _device(out, "out")
+    o = _ptr(out, torch.bfloat16, "out")
     N, K = out.shape
-    _here(Wp, w_scale, w_zero, out)
-    p, e, z = _int4(Wp, w_scale, w_zero, group, N, K)
-    _check(_lib.sq_dequant_weight_int4(p, e, z, int(group), N, K, _dense(out, torch.bfloat16, (N, K), "out"),
-                                       _stream(stream)))
+    p, e, z = _int4(Wp, w_scale, w_zero, group, N, K, dev)
+    _check(_lib.sq_dequant_weight_int4(p, e, z, group, N, K, o, _on(stream, dev)))
     return out
 
 
 def sq_int4_linear(X, Wp, w_scale, w_zero, group: int, bias, Y, stream=None):
     """Y [M, N] = X [M, K] times the 4-bit weight, plus bias; M <= 64."""
     torch = _torch()
+    dev = _device(X, "X")
+    x = _ptr(X, torch.bfloat16, "X", True)
     M, K = X.shape
     N = Y.shape[-1]
-    _here(X, Wp, w_scale, w_zero, bias, Y)
-    p, e, z = _int4(Wp, w_scale, w_zero, group, N, K)
-    _check(_lib.sq_int4_linear(_ptr(X, torch.bfloat16, "X", True), M, K, X.stride(0), p, e, z, int(group),
-                               _dense(bias, torch.bfloat16, (N,), "bias"), _dense(Y, torch.bfloat16, (M, N), "Y"), N,
-                               _stream(stream)))
+    p, e, z = _int4(Wp, w_scale, w_zero, group, N, K, dev)
+    _check(_lib.sq_int4_linear(x, M, K, X.stride(0), p, e, z, group, _dense(bias, torch.bfloat16, (N,), "bias", dev),
+                               _dense(Y, torch.bfloat16, (M, N), "Y", dev), N, _on(stream, dev)))
     return Y
 
 
@@ -404,15 +412,14 @@ class KvCache:
             raise TypeError("k and v must be 4-D, both bfloat16 or both int8")
         if int8 != (k_scale is not None) or int8 != (v_scale is not None):
             raise ValueError("int8 caches have k_scale and v_scale, bf16 caches none")
+        if int8 and (k_scale.dtype != torch.float32 or v_scale.dtype != torch.float32):
+            raise TypeError("cache scales must be float32")
         pages, heads, page_size, dim = k.shape
         for t, shape, dense in ((k, k.shape, (page_size * dim, dim, 1)), (v, k.shape, (page_size * dim, dim, 1)),
                                 (k_scale, k.shape[:3], (page_size, 1)), (v_scale, k.shape[:3], (page_size, 1))):
-            if t is None:
-                continue
-            if t.shape != shape or any(s != d for s, d, n in zip(t.stride()[1:], dense, t.shape[1:]) if n > 1):
+            if t is not None and (t.shape != shape or any(s != d for s, d, n in zip(t.stride()[1:], dense, shape[1:])
+                                                          if n > 1)):
                 raise ValueError("cache tensors must have one shape and be dense within a page")
-            if dense[-2:] == (page_size, 1) and len(dense) == 2 and t.dtype != torch.float32:
-                raise TypeError("cache scales must be float32")
         if not k.is_cuda or any(t is not None and t.device != k.device for t in (v, k_scale, v_scale)):
             raise ValueError("cache tensors must be on one CUDA device")
 
@@ -430,18 +437,16 @@ class KvCache:
             SQ_KV_INT8 if int8 else SQ_KV_BF16, 0, k.data_ptr(), v.data_ptr(),
             k_scale.data_ptr() if int8 else None, v_scale.data_ptr() if int8 else None, pages, heads, page_size, dim,
             stride(k, v), stride(k_scale, v_scale) if int8 else 0)
-        self.ref = C.byref(self.struct)
+        self.ref = C.addressof(self.struct)
 
 
-def _heads(t, heads, dim, name):
-    """(data pointer, token stride) of a bf16 [T, heads, dim] tensor dense within a token."""
-    torch = _torch()
-    if t.dtype != torch.bfloat16:
-        raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim or t.stride(2) != 1 or \
-            (heads > 1 and t.stride(1) != dim):
+def _heads(t, heads, dim, name, dev):
+    """(data pointer, token stride) of a bf16 [tokens, heads, dim] tensor dense within a token."""
+    _typed(t, _torch().bfloat16, name, dev)
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3 or shape[1] != heads or shape[2] != dim or stride[2] != 1 or (heads > 1 and stride[1] != dim):
         raise ValueError(f"{name} must be [tokens, {heads}, {dim}], dense within a token")
-    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else heads * dim
+    return t.data_ptr(), stride[0] if shape[0] > 1 else heads * dim
 
 
 def sq_rope_kv_append(q, k, v, cos, sin, positions, slots, cache: KvCache, q_out, interleaved: bool = False,
@@ -449,29 +454,32 @@ def sq_rope_kv_append(q, k, v, cos, sin, positions, slots, cache: KvCache, q_out
     """Rotate q and k by position, write q_out, append k and v to the cache's slots. q and q_out
     may be None; cos, sin [max_pos, rot_dim / 2] and positions may be None (no rotation)."""
     torch = _torch()
-    if _here(q, k, v, cos, sin, positions, slots, q_out) != cache.device:
-        raise ValueError(f"cache on cuda:{cache.device}, which is not the current device")
-    T, Hkv, D = k.shape
-    if Hkv != cache.heads or D != cache.head_dim or v.shape != k.shape:
-        raise ValueError(f"k and v must be [tokens, {cache.heads}, {cache.head_dim}]")
-    kp, ldk = _heads(k, Hkv, D, "k")
-    vp, ldv = _heads(v, Hkv, D, "v")
+    dev = _device(k, "k")
+    if dev != cache.device:
+        raise ValueError(f"cache on cuda:{cache.device}, k on cuda:{dev}")
+    heads, D = cache.heads, cache.head_dim
+    kp, ldk = _heads(k, heads, D, "k", dev)
+    vp, ldv = _heads(v, heads, D, "v", dev)
+    T = k.shape[0]
     if (q is None) != (q_out is None):
         raise ValueError("q and q_out must be given together")
-    H, qp, ldq = 0, None, 0
-    if q is not None:
-        H = q.shape[1]
-        qp, ldq = _heads(q, H, D, "q")
-        if q.shape[0] != T:
-            raise ValueError("q and k must have the same number of tokens")
-    max_pos, half = (0, 0) if cos is None else cos.shape
     if (cos is None) != (sin is None) or (cos is None) != (positions is None):
         raise ValueError("cos, sin and positions must be given together")
-    _check(_lib.sq_rope_kv_append(
-        qp, ldq, kp, ldk, vp, ldv, T, H, _dense(cos, torch.float32, (max_pos, half), "cos"),
-        _dense(sin, torch.float32, (max_pos, half), "sin"), max_pos, 2 * half, int(bool(interleaved)),
-        _dense(positions, torch.int32, (T,), "positions"), _dense(slots, torch.int32, (T,), "slots"), cache.ref,
-        _dense(q_out, torch.bfloat16, (T, H, D), "q_out"), _stream(stream)))
+    H, qp, ldq, op = 0, None, 0, None
+    if q is not None:
+        H = q.shape[1]
+        qp, ldq = _heads(q, H, D, "q", dev)
+        op = _dense(q_out, torch.bfloat16, (T, H, D), "q_out", dev)
+    if v.shape[0] != T or (q is not None and q.shape[0] != T):
+        raise ValueError("q, k and v must have the same number of tokens")
+    max_pos, half, cp, sp, pp = 0, 0, None, None, None
+    if cos is not None:
+        max_pos, half = cos.shape
+        cp = _dense(cos, torch.float32, (max_pos, half), "cos", dev)
+        sp = _dense(sin, torch.float32, (max_pos, half), "sin", dev)
+        pp = _dense(positions, torch.int32, (T,), "positions", dev)
+    _check(_lib.sq_rope_kv_append(qp, ldq, kp, ldk, vp, ldv, T, H, cp, sp, max_pos, 2 * half, 1 if interleaved else 0, pp,
+                                  _dense(slots, torch.int32, (T,), "slots", dev), cache.ref, op, _on(stream, dev)))
     return q_out
 
 
@@ -479,23 +487,27 @@ def sq_paged_attention(q, cache: KvCache, block_table, seq_lens, scale: float, o
                        stream=None):
     """out [B, H, D]: attention of one token per sequence over the cache; lse [B, H] fp32 too."""
     torch = _torch()
-    if _here(q, block_table, seq_lens, out, lse, ws) != cache.device:
-        raise ValueError(f"cache on cuda:{cache.device}, which is not the current device")
+    dev = _device(q, "q")
+    if dev != cache.device:
+        raise ValueError(f"cache on cuda:{cache.device}, q on cuda:{dev}")
+    if q.dim() != 3:
+        raise ValueError("q must be [sequences, heads, head_dim]")
     B, H, D = q.shape
-    if D != cache.head_dim:
-        raise ValueError(f"q must have head dimension {cache.head_dim}")
-    qp, ldq = _heads(q, H, D, "q")
-    if block_table.dim() != 2 or block_table.shape[0] != B or (block_table.shape[1] > 1 and block_table.stride(1) != 1):
+    qp, ldq = _heads(q, H, cache.head_dim, "q", dev)
+    _typed(block_table, torch.int32, "block_table", dev)
+    shape, stride = block_table.shape, block_table.stride()
+    if len(shape) != 2 or shape[0] != B or (shape[1] > 1 and stride[1] != 1):
         raise ValueError(f"block_table must be [{B}, max_pages] with unit column stride")
-    if block_table.dtype != torch.int32:
-        raise TypeError("block_table must be torch.int32")
-    max_pages = block_table.shape[1]
-    wsp, wsb = _ws(ws)
+    wsp, wsb = None, 0
+    if ws is not None:
+        if ws.get_device() != dev or not ws.is_contiguous():
+            raise ValueError(f"ws must be a contiguous tensor on cuda:{dev}")
+        wsp, wsb = ws.data_ptr(), ws.numel() * ws.element_size()
     _check(_lib.sq_paged_attention(
-        qp, ldq, B, H, cache.ref, block_table.data_ptr(), block_table.stride(0) if B > 1 else max_pages, max_pages,
-        _dense(seq_lens, torch.int32, (B,), "seq_lens"), int(window), float(scale),
-        _dense(out, torch.bfloat16, (B, H, D), "out"), _dense(lse, torch.float32, (B, H), "lse"), wsp, wsb,
-        _stream(stream)))
+        qp, ldq, B, H, cache.ref, block_table.data_ptr(), stride[0] if B > 1 else shape[1], shape[1],
+        _dense(seq_lens, torch.int32, (B,), "seq_lens", dev), window, scale,
+        _dense(out, torch.bfloat16, (B, H, D), "out", dev), _dense(lse, torch.float32, (B, H), "lse", dev), wsp, wsb,
+        _on(stream, dev)))
     return out
 
 
