@@ -194,65 +194,243 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], 
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// One CTA per row tile and 8 tokens, its warps over the column blocks in turn.
-__global__ void __launch_bounds__(kInt4Threads)
-int4_linear_kernel(const uint16_t* __restrict__ X, int M, int64_t K, int64_t ldx, const uint8_t* __restrict__ Wp,
-                   const uint16_t* __restrict__ scale, const uint8_t* __restrict__ zero, int group,
-                   const uint16_t* __restrict__ bias, uint16_t* __restrict__ Y, int64_t N) {
+__device__ __forceinline__ void ldmatrix(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr));
+}
+template <int BYTES>
+__device__ __forceinline__ void cp_async(uint32_t dst, const void* src, bool valid) {
+  if constexpr (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(BYTES), "r"(valid ? BYTES : 0)
+                 : "memory");
+}
+__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+struct LinearParams {
+  const uint16_t* X;
+  int64_t ldx, N;
+  const uint8_t* Wp;
+  const uint16_t* scale;
+  const uint8_t* zero;
+  const uint16_t* bias;
+  uint16_t* Y;
+  int M, K, Kb, groups;
+  int split;   // CTAs of a cluster, which share a row block's columns
+  int stages;  // 1 when a CTA's columns are one chunk
+};
+
+// The tokens' product with the weight streams the codes once: 16x8x16 matrix instructions with
+// the weight rows as the 16 rows and up to 8 NT tokens as columns. A CTA takes RW row tiles, its
+// 8 / RW warps of a tile take the 128-column blocks in turn; each lane's fragments of a block
+// are two 16-byte loads, PF blocks ahead in registers. Activations, scales and zero points of a
+// chunk of columns are staged in shared memory by asynchronous copies, one chunk ahead. Codes
+// become bf16 exactly (128 + code, minus 128 + zero); a group's fp32 sum is scaled and added to
+// the total. Warps of a tile, and the CTAs of a cluster along K, are joined in a fixed order
+// through (distributed) shared memory.
+template <int NT, int G, bool ASYM, int RW, int PF>
+__global__ void __launch_bounds__(kInt4Threads) int4_linear_kernel(const LinearParams p) {
+  constexpr int W = kInt4Threads / 32, KW = W / RW, kBlocks = KW * PF, kCols = kBlocks * 128, kRows = RW * 16;
+  constexpr int kStride = (kCols + 8) * 2, kGroups = kCols / G;
+  extern __shared__ __align__(16) uint8_t smem[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int rw = warp % RW, kw = warp / RW;
+  const int rank = blockIdx.x % p.split;
+  const int64_t row_block = blockIdx.x / p.split, rt = row_block * RW + rw, n0 = row_block * kRows;
+  const int kb0 = static_cast<int>(static_cast<int64_t>(p.Kb) * rank / p.split);
+  const int kb1 = static_cast<int>(static_cast<int64_t>(p.Kb) * (rank + 1) / p.split);
+  const bool rows_in = rt * 16 < p.N;
+  const uint8_t* tiles = p.Wp + rt * p.Kb * kTileBytes;
+  // the weight does not depend on the kernel before in a decode step: its way into L2 starts
+  // before waiting for that kernel (a hint, safe even if that kernel wrote the weight)
+  if (rows_in && kw == 0 && lane == 0)
+    bulk_prefetch_l2(tiles + static_cast<int64_t>(kb0) * kTileBytes,
+                     static_cast<uint32_t>(min(kb1 - kb0, kBlocks)) * kTileBytes);
   griddep_wait();
   griddep_launch_dependents();
-  __shared__ float part[kInt4Threads / 32][8][16];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int64_t Kb = (K + 127) / 128, rt = blockIdx.x;
-  const int m = blockIdx.y * 8 + g;
-  float acc[4] = {0, 0, 0, 0};
-  for (int64_t kb = warp; kb < Kb; kb += kInt4Threads / 32) {
-    const uint8_t* tile = Wp + (rt * Kb + kb) * kTileBytes;
-    const uint4 u0 = __ldg(reinterpret_cast<const uint4*>(tile) + lane);
-    const uint4 u1 = __ldg(reinterpret_cast<const uint4*>(tile) + 32 + lane);
-    const uint32_t lo[4] = {u0.x, u0.y, u0.z, u0.w}, hi[4] = {u1.x, u1.y, u1.z, u1.w};
+
+  const int x_bytes = (p.M + 1) * kStride, stage_bytes = x_bytes + kGroups * kRows * (ASYM ? 3 : 2);
+  const uint32_t smem32 = smem_u32(smem);
+  auto stage_in = [&](int kb, int stage) {  // the chunk of columns from block kb on
+    const uint32_t dst = smem32 + stage * stage_bytes;
+    const int k0 = kb * 128, k1 = min(p.K, kb1 * 128);
+    for (int i = threadIdx.x; i < p.M * (kCols / 8); i += kInt4Threads) {
+      const int m = i / (kCols / 8), k = i % (kCols / 8) * 8;
+      const bool in = k0 + k < k1;
+      cp_async<16>(dst + m * kStride + k * 2, p.X + (in ? m * p.ldx + k0 + k : 0), in);
+    }
+    for (int i = threadIdx.x; i < kGroups * (kRows / 8); i += kInt4Threads) {
+      const int gr = k0 / G + i / (kRows / 8), r = i % (kRows / 8) * 8;
+      const bool in = gr < p.groups && n0 + r < p.N;
+      const int64_t at = in ? gr * p.N + n0 + r : 0;
+      cp_async<16>(dst + x_bytes + i * 16, p.scale + at, in);
+      if (ASYM) cp_async<8>(dst + x_bytes + kGroups * kRows * 2 + i * 8, p.zero + at, in);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  uint4 w[PF][2];
+  auto fetch = [&](int i, int kb) {
+    if (rows_in && kb < kb1) {
+      const uint4* src = reinterpret_cast<const uint4*>(tiles + static_cast<int64_t>(kb) * kTileBytes) + lane;
+      w[i][0] = __ldcs(src);
+      w[i][1] = __ldcs(src + 32);
+    }
+  };
 #pragma unroll
-    for (int a = 0; a < 4; ++a) {
-      const int64_t k0 = kb * 128 + a * 32;
-      if (k0 >= K) break;
-      const int64_t n0 = rt * 16 + g, n1 = n0 + 8, row = k0 / group * N;
-      const float e0 = n0 < N ? bf16_lo(__ldg(scale + row + n0)) : 0.0f, e1 = n1 < N ? bf16_lo(__ldg(scale + row + n1)) : 0.0f;
-      const uint32_t z0 = zero_pair(zero != nullptr && n0 < N ? __ldg(zero + row + n0) : 8u);
-      const uint32_t z1 = zero_pair(zero != nullptr && n1 < N ? __ldg(zero + row + n1) : 8u);
-      float d[4] = {0, 0, 0, 0};
+  for (int i = 0; i < PF; ++i) {
+    w[i][0] = w[i][1] = make_uint4(0, 0, 0, 0);
+    fetch(i, kb0 + i * KW + kw);
+  }
+  stage_in(kb0, 0);
+  // row M of each stage: zeros, for the tokens that fill up the last 8
+  for (int i = threadIdx.x; i < kStride / 16 * p.stages; i += kInt4Threads)
+    *reinterpret_cast<uint4*>(smem + (i / (kStride / 16)) * stage_bytes + p.M * kStride + i % (kStride / 16) * 16) =
+        make_uint4(0, 0, 0, 0);
+
+  float acc[NT][4];
+  uint32_t x_row[NT];  // this lane's row address for loading the activations' fragments
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int64_t k = k0 + j * 16 + 2 * t;
-        uint32_t af[4];
-        af[0] = sub_bf16x2(((lo[a] >> (8 * j)) & 0x000F000Fu) | 0x43004300u, z0);
-        af[1] = sub_bf16x2(((hi[a] >> (8 * j)) & 0x000F000Fu) | 0x43004300u, z1);
-        af[2] = sub_bf16x2(((lo[a] >> (8 * j + 4)) & 0x000F000Fu) | 0x43004300u, z0);
-        af[3] = sub_bf16x2(((hi[a] >> (8 * j + 4)) & 0x000F000Fu) | 0x43004300u, z1);
-        const uint16_t* x = X + m * ldx + k;
-        const uint32_t b0 = m < M && k < K ? __ldg(reinterpret_cast<const uint32_t*>(x)) : 0u;
-        const uint32_t b1 = m < M && k + 8 < K ? __ldg(reinterpret_cast<const uint32_t*>(x + 8)) : 0u;
-        mma_bf16(d, af, b0, b1);
+  for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[nt][e] = 0.0f;
+    x_row[nt] = smem32 + min(nt * 8 + (lane & 7), p.M) * kStride + (lane >> 3) * 16;
+  }
+  int stage = 0;
+  for (int kb = kb0; kb < kb1; kb += kBlocks) {
+    if (kb + kBlocks < kb1) {
+      stage_in(kb + kBlocks, stage ^ 1);
+      asm volatile("cp.async.wait_group 1;" ::: "memory");
+    } else {
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
+    }
+    __syncthreads();
+    const uint32_t base = stage * stage_bytes;
+    const uint16_t* es = reinterpret_cast<const uint16_t*>(smem + base + x_bytes) + rw * 16 + g;
+    const uint8_t* zs = smem + base + x_bytes + kGroups * kRows * 2 + rw * 16 + g;
+#pragma unroll
+    for (int i = 0; i < PF; ++i) {
+      const int block = i * KW + kw;  // of the chunk
+      if (kb + block < kb1) {
+        const uint32_t lo[4] = {w[i][0].x, w[i][0].y, w[i][0].z, w[i][0].w};
+        const uint32_t hi[4] = {w[i][1].x, w[i][1].y, w[i][1].z, w[i][1].w};
+        float d[NT][4];
+#pragma unroll
+        for (int a = 0; a < 4; ++a) {
+          const int gr = (block * 128 + a * 32) / G * kRows;
+          const uint32_t z0 = ASYM ? zero_pair(zs[gr]) : 0x43084308u, z1 = ASYM ? zero_pair(zs[gr + 8]) : 0x43084308u;
+          if (a * 32 % G == 0) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) d[nt][e] = 0.0f;
+          }
+          uint32_t f[2][4];
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            f[j][0] = sub_bf16x2(((lo[a] >> (8 * j)) & 0x000F000Fu) | 0x43004300u, z0);
+            f[j][1] = sub_bf16x2(((hi[a] >> (8 * j)) & 0x000F000Fu) | 0x43004300u, z1);
+            f[j][2] = sub_bf16x2(((lo[a] >> (8 * j + 4)) & 0x000F000Fu) | 0x43004300u, z0);
+            f[j][3] = sub_bf16x2(((hi[a] >> (8 * j + 4)) & 0x000F000Fu) | 0x43004300u, z1);
+          }
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            uint32_t x[4];
+            ldmatrix(x, x_row[nt] + base + block * 256 + a * 64);
+            mma_bf16(d[nt], f[0], x[0], x[1]);
+            mma_bf16(d[nt], f[1], x[2], x[3]);
+          }
+          if ((a + 1) * 32 % G == 0) {
+            const float e0 = bf16_lo(es[gr]), e1 = bf16_lo(es[gr + 8]);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              acc[nt][0] = fmaf(d[nt][0], e0, acc[nt][0]);
+              acc[nt][1] = fmaf(d[nt][1], e0, acc[nt][1]);
+              acc[nt][2] = fmaf(d[nt][2], e1, acc[nt][2]);
+              acc[nt][3] = fmaf(d[nt][3], e1, acc[nt][3]);
+            }
+          }
+        }
       }
-      acc[0] = fmaf(d[0], e0, acc[0]);
-      acc[1] = fmaf(d[1], e0, acc[1]);
-      acc[2] = fmaf(d[2], e1, acc[2]);
-      acc[3] = fmaf(d[3], e1, acc[3]);
+      fetch(i, kb + kBlocks + block);
     }
+    __syncthreads();
+    stage ^= 1;
   }
+
+  // [KW][M][kRows] partial sums in the staging area
+  float* part = reinterpret_cast<float*>(smem);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) part[warp][2 * t + (i & 1)][g + (i & 2) * 4] = acc[i];
-  __syncthreads();
-  if (threadIdx.x < 128) {
-    const int r = threadIdx.x & 15, tok = blockIdx.y * 8 + (threadIdx.x >> 4);
-    const int64_t n = rt * 16 + r;
-    float y = 0.0f;
+  for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-    for (int w = 0; w < kInt4Threads / 32; ++w) y += part[w][threadIdx.x >> 4][r];
-    if (tok < M && n < N) {
-      if (bias != nullptr) y += bf16_lo(__ldg(bias + n));
-      Y[tok * N + n] = __bfloat16_as_ushort(__float2bfloat16_rn(y));
+    for (int e = 0; e < 4; ++e) {
+      const int m = nt * 8 + 2 * t + (e & 1);
+      if (m < p.M) part[(kw * p.M + m) * kRows + rw * 16 + g + (e & 2) * 4] = acc[nt][e];
     }
+  if (p.split > 1)
+    cluster_sync();
+  else
+    __syncthreads();
+  const int share = kRows / 2 / p.split;  // row pairs that this CTA of the cluster finishes
+  for (int i = threadIdx.x; i < p.M * share; i += kInt4Threads) {
+    const int m = i / share, r = (rank * share + i % share) * 2;
+    const int64_t n = n0 + r;
+    if (n >= p.N) continue;
+    float y0 = 0.0f, y1 = 0.0f;
+    for (int c = 0; c < p.split; ++c) {
+#pragma unroll
+      for (int k = 0; k < KW; ++k) {
+        const float* at = part + (k * p.M + m) * kRows + r;
+        if (p.split > 1) {
+          const uint32_t a = mapa_shared(at, c);
+          y0 += ld_cluster_f32(a);
+          y1 += ld_cluster_f32(a + 4);
+        } else {
+          y0 += at[0];
+          y1 += at[1];
+        }
+      }
+    }
+    if (p.bias != nullptr) {
+      const uint32_t b = __ldg(reinterpret_cast<const uint32_t*>(p.bias + n));
+      y0 += bf16_lo(b);
+      y1 += bf16_hi(b);
+    }
+    const __nv_bfloat162 y = __floats2bfloat162_rn(y0, y1);
+    *reinterpret_cast<__nv_bfloat162*>(p.Y + m * p.N + n) = y;
   }
+  if (p.split > 1) cluster_sync();  // no CTA leaves while its sums are being read
+}
+
+template <int NT, int G, bool ASYM, int RW, int PF>
+cudaError_t launch_linear(LinearParams p, cudaStream_t stream) {
+  constexpr int kBlocks = kInt4Threads / 32 / RW * PF, kCols = kBlocks * 128, kRows = RW * 16;
+  const int64_t blocks = (p.N + kRows - 1) / kRows;
+  // split along K until two CTAs per SM exist, as long as every CTA keeps a chunk of columns
+  p.split = 1;
+  while (p.split < 8 && blocks * p.split < 2 * 148 && p.Kb >= 2 * p.split * kBlocks) p.split *= 2;
+  const int most = (p.Kb + p.split - 1) / p.split;
+  p.stages = most > kBlocks ? 2 : 1;
+  const size_t stage = (p.M + 1) * (kCols + 8) * 2 + kCols / G * kRows * (ASYM ? 3 : 2);
+  const size_t smem = std::max(stage * p.stages, static_cast<size_t>(p.M) * kRows * (kInt4Threads / 32 / RW) * 4);
+  auto kernel = int4_linear_kernel<NT, G, ASYM, RW, PF>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  if (e != cudaSuccess) return e;
+  return launch_kernel_clustered(kernel, dim3(static_cast<unsigned>(blocks * p.split)), dim3(kInt4Threads), smem, stream,
+                                 true, static_cast<unsigned>(p.split), p);
+}
+
+template <int G, bool ASYM>
+cudaError_t launch_linear_g(const LinearParams& p, cudaStream_t stream) {
+  if (p.M <= 8) return launch_linear<1, G, ASYM, 1, 4>(p, stream);
+  if (p.M <= 16) return launch_linear<2, G, ASYM, 8, 4>(p, stream);
+  if (p.M <= 32) return launch_linear<4, G, ASYM, 8, 4>(p, stream);
+  return launch_linear<8, G, ASYM, 8, 2>(p, stream);
 }
 
 // Grid of the two tile kernels: one column block per x, row tiles over y so that about eight
@@ -283,9 +461,25 @@ cudaError_t launch_int4_dequant(const uint8_t* Wp, const uint16_t* scale, const 
 }
 
 cudaError_t launch_int4_linear(const Int4LinearArgs& a, cudaStream_t stream) {
-  const dim3 grid(static_cast<unsigned>((a.N + 15) / 16), static_cast<unsigned>((a.M + 7) / 8));
-  return launch_kernel(int4_linear_kernel, grid, dim3(kInt4Threads), 0, stream, true, a.X, static_cast<int>(a.M), a.K,
-                       a.ldx, a.Wp, a.scale, a.zero, a.group, a.bias, a.Y, a.N);
+  LinearParams p{};
+  p.X = a.X;
+  p.ldx = a.ldx;
+  p.N = a.N;
+  p.Wp = a.Wp;
+  p.scale = a.scale;
+  p.zero = a.zero;
+  p.bias = a.bias;
+  p.Y = a.Y;
+  p.M = static_cast<int>(a.M);
+  p.K = static_cast<int>(a.K);
+  p.Kb = (p.K + 127) / 128;
+  p.groups = (p.K + a.group - 1) / a.group;
+  if (a.zero != nullptr) {
+    if (a.group == 32) return launch_linear_g<32, true>(p, stream);
+    return a.group == 64 ? launch_linear_g<64, true>(p, stream) : launch_linear_g<128, true>(p, stream);
+  }
+  if (a.group == 32) return launch_linear_g<32, false>(p, stream);
+  return a.group == 64 ? launch_linear_g<64, false>(p, stream) : launch_linear_g<128, false>(p, stream);
 }
 
 }  // namespace sq
