@@ -407,6 +407,312 @@ __global__ void __launch_bounds__(kInt4Threads) int4_linear_kernel(const LinearP
   if (p.split > 1) cluster_sync();  // no CTA leaves while its sums are being read
 }
 
+// ---- up to 8 tokens: int8 matrix instructions.
+// Making bf16 of 4-bit codes costs a logic operation, most of a shift and a subtraction per pair;
+// for a few tokens that is most of the work, and it bounds the kernel (measured: 230 instructions
+// for a 1024-byte block, 41 us at 1 x 28672 x 8192 whatever the copies do). Bytes are cheaper: a
+// word of eight codes masked with 0x0F0F0F0F, and shifted once, is two operands of four. So the
+// activations become integers instead, once: a token, scaled by a power of two to 23 bits, is
+// split into three signed bytes, three columns of the 16x8x32 instructions (elements down to
+// 2^-14 of the token's largest are exact, smaller ones off by 2^-23 of it). Products and a
+// group's sums are exact integers, and so is the zero point's part,
+//   sum_k x_k (code - zero) = sum_k x_k code - zero * sum_k x_k,
+// with the group's sums of x taken beforehand. A group's result is scaled and added in fp32.
+//
+// Teams of `kw` warps: each team on a row tile of its own, then on the next that is due (all
+// teams of the grid in turn); within a tile the warps take pairs of 128-column blocks in turn.
+// Every lane brings its own fragments into its warp's ring with asynchronous copies, across tiles
+// and with nothing to wait for but the copies. The team meets once a tile to add its warps' sums
+// up in order.
+constexpr int kTeamWarps = 16;  // of a CTA, one CTA per SM
+constexpr int64_t kSmemMax = 232448;
+
+struct TeamParams {
+  LinearParams p;
+  int kw;         // warps of a team
+  int sides;      // buffers of partial sums: 2 if a team has more than one tile
+  int ring;       // slots of a warp's ring, 2 to 4
+  int Kp;         // pairs of column blocks, the second of the last one may lie past K
+  int col_bytes;  // of a column of activation bytes
+};
+
+template <int G, bool ASYM>
+constexpr int team_slot_bytes() {  // a pair of blocks: codes, 16 scales and 16 zero points per group
+  return 2 * (kTileBytes + 128 / G * (ASYM ? 48 : 32));
+}
+
+__device__ __forceinline__ void mma_u8s8(int (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k32.row.col.s32.u8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// NT: columns / 8; column 3 m + d is byte d (0 the highest) of token m.
+template <int NT, int G, bool ASYM>
+__global__ void __launch_bounds__(kTeamWarps * 32, 1) int4_team_kernel(const TeamParams q) {
+  constexpr int kGroups = 256 / G, kSlot = team_slot_bytes<G, ASYM>(), kThreads = kTeamWarps * 32, kCols = NT * 8;
+  constexpr int kScales = 2 * kTileBytes, kZeros = kScales + kGroups * 32;
+  const LinearParams& p = q.p;
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ float s_top[kTeamWarps], s_mul[8], s_back[8];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int teams = kTeamWarps / q.kw, team = warp / q.kw, kw = warp % q.kw;
+  const int Nt = static_cast<int>((p.N + 15) / 16), step = gridDim.x * teams;
+  // tiles go to the SMs in turn; warps left over from the teams have none
+  const int rt0 = team < teams ? static_cast<int>(blockIdx.x + gridDim.x * team) : Nt;
+  // the weight does not depend on the kernel before in a decode step: its way into L2 starts
+  // before waiting for that kernel (a hint, safe even if that kernel wrote the weight)
+  if (kw == 0 && lane == 0 && rt0 < Nt)
+    bulk_prefetch_l2(p.Wp + static_cast<int64_t>(rt0) * p.Kb * kTileBytes,
+                     static_cast<uint32_t>(min(p.Kb, 2 * q.kw * q.ring)) * kTileBytes);
+  griddep_wait();
+  griddep_launch_dependents();
+
+  // shared memory: columns of bytes | [groups][kCols] sums of a group's bytes | rings | partial sums
+  const int sums_at = 3 * p.M * q.col_bytes, ring_at = sums_at + q.Kp * kGroups * kCols * 4;
+  const uint32_t ring32 = smem_u32(smem) + ring_at + warp * q.ring * kSlot;
+  int* sums = reinterpret_cast<int*>(smem + sums_at);
+  float* part = reinterpret_cast<float*>(smem + ring_at + kTeamWarps * q.ring * kSlot);  // [sides][warps][kCols][16]
+
+  // ---- the next pair to bring
+  int load_rt = kw < q.Kp ? rt0 : Nt, load_kp = kw;
+  const uint8_t* load_src = p.Wp + (static_cast<int64_t>(rt0) * p.Kb + 2 * kw) * kTileBytes + lane * 16;
+  const int64_t tile_jump = static_cast<int64_t>(step) * p.Kb * kTileBytes;
+  // this lane's part of a pair's scales: kScaleLanes lanes of kScaleBytes; of its zero points: 4 bytes
+  constexpr int kScaleBytes = G == 32 ? 8 : 4, kLanesPerGroup = 32 / kScaleBytes, kScaleLanes = kGroups * kLanesPerGroup;
+  const int e_group = lane / kLanesPerGroup, e_row = lane % kLanesPerGroup * (kScaleBytes / 2);
+  const int z_group = lane / 4, z_row = lane % 4 * 4;
+  auto fetch = [&](int slot) {
+    if (load_rt < Nt) {
+      const uint32_t dst = ring32 + slot * kSlot;
+      const bool second = 2 * load_kp + 1 < p.Kb;
+      cp_async<16>(dst + lane * 16, load_src, true);
+      cp_async<16>(dst + 512 + lane * 16, load_src + 512, true);
+      cp_async<16>(dst + 1024 + lane * 16, load_src + (second ? 1024 : 0), second);
+      cp_async<16>(dst + 1536 + lane * 16, load_src + (second ? 1536 : 0), second);
+      if (lane < kScaleLanes) {
+        const int gr = load_kp * kGroups + e_group, n = load_rt * 16 + e_row;
+        const bool in = gr < p.groups && n < p.N;
+        cp_async<kScaleBytes>(dst + kScales + lane * kScaleBytes, p.scale + (in ? gr * p.N + n : 0), in);
+      }
+      if (ASYM && lane < 4 * kGroups) {
+        const int gr = load_kp * kGroups + z_group, n = load_rt * 16 + z_row;
+        const bool in = gr < p.groups && n < p.N;
+        cp_async<4>(dst + kZeros + lane * 4, p.zero + (in ? gr * p.N + n : 0), in);
+      }
+      load_kp += q.kw;
+      load_src += 2 * q.kw * kTileBytes;
+      if (load_kp >= q.Kp) {  // on to the team's next tile
+        load_src += tile_jump - static_cast<int64_t>(load_kp - kw) * 2 * kTileBytes;
+        load_kp = kw;
+        load_rt += step;
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+#pragma unroll 1
+  for (int i = 0; i < q.ring - 1; ++i) fetch(i);
+
+  // ---- activations to bytes: the tokens' largest values, each by an equal share of the warps
+  const int share = kTeamWarps / p.M;  // warps of a token, at least 2
+  if (warp < share * p.M) {
+    const uint16_t* x = p.X + warp / share * p.ldx;
+    float top = 0.0f;
+#pragma unroll 4
+    for (int k = (warp % share * 32 + lane) * 8; k < p.K; k += share * 256) {
+      const uint4 v = __ldg(reinterpret_cast<const uint4*>(x + k));
+      const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) top = fmaxf(top, fmaxf(fabsf(bf16_lo(u[i])), fabsf(bf16_hi(u[i]))));
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if (lane == 0) s_top[warp] = top;
+  }
+  __syncthreads();
+  if (threadIdx.x < p.M) {
+    float top = 0.0f;
+    for (int w = 0; w < share; ++w) top = fmaxf(top, s_top[threadIdx.x * share + w]);
+    // 2^up brings the largest below 2^22
+    const int up = min(22 + 126 - static_cast<int>(__float_as_uint(top) >> 23), 120);
+    s_mul[threadIdx.x] = __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
+    s_back[threadIdx.x] = __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
+  }
+  __syncthreads();
+  // then 8 elements per thread and step; a warp takes a pair of blocks: 8 words of 32 columns x 4 quad lanes
+  for (int i = warp; i < p.M * q.Kp; i += kTeamWarps) {
+    const int m = i / q.Kp, kp = i % q.Kp, word = kp * 8 + lane / 4;
+    const float mul = s_mul[m];
+    const uint16_t* src = p.X + m * p.ldx + word * 32 + t * 2;
+    uint32_t v[8];  // columns 2 t, 2 t + 1 of each 8
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const uint32_t x = word * 32 + c * 8 < p.K ? __ldg(reinterpret_cast<const uint32_t*>(src + c * 8)) : 0u;
+      // round to an integer in the low mantissa bits (1.5 * 2^23 added), then bytes with carries:
+      // the three low bytes of v + 0x808080, each less 128, are the signed digits
+      v[2 * c] = __float_as_uint(__fmaf_rn(bf16_lo(x), mul, 12582912.0f)) + (0x00808080u - 0x4B400000u);
+      v[2 * c + 1] = __float_as_uint(__fmaf_rn(bf16_hi(x), mul, 12582912.0f)) + (0x00808080u - 0x4B400000u);
+    }
+#pragma unroll
+    for (int d = 0; d < 3; ++d) {
+      // the order of a word's codes: low nibbles are columns 2t, 16 + 2t, 2t + 1, 17 + 2t, high ones 8 more
+      const uint32_t pick = d == 0 ? 0x0062u : d == 1 ? 0x0051u : 0x0040u;
+      const uint32_t b0 = __byte_perm(__byte_perm(v[0], v[4], pick), __byte_perm(v[1], v[5], pick), 0x5410) ^ 0x80808080u;
+      const uint32_t b1 = __byte_perm(__byte_perm(v[2], v[6], pick), __byte_perm(v[3], v[7], pick), 0x5410) ^ 0x80808080u;
+      const int col = 3 * m + d;
+      *reinterpret_cast<uint2*>(smem + col * q.col_bytes + word / 4 * 128 + t * 32 + word % 4 * 8) = make_uint2(b0, b1);
+      int sum = __dp4a(static_cast<int>(b0), 0x01010101, __dp4a(static_cast<int>(b1), 0x01010101, 0));
+#pragma unroll
+      for (int o = 1; o < G / 8; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      if (lane % (G / 8) == 0) sums[(kp * kGroups + lane / (G / 8)) * kCols + col] = sum;
+    }
+  }
+  __syncthreads();
+
+  // B fragments: column 8 nt + g, this lane's 32 bytes of a block; columns past 3 M repeat the last
+  // one and nothing reads their results
+  const uint8_t* x_col[NT];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) x_col[nt] = smem + min(nt * 8 + g, 3 * p.M - 1) * q.col_bytes + t * 32;
+  float acc[NT][4];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) acc[nt][0] = acc[nt][1] = acc[nt][2] = acc[nt][3] = 0.0f;
+  int side = 0, slot = 0, free_slot = q.ring - 1;
+  for (int rt = rt0; rt < Nt; rt += step) {
+#pragma unroll 1
+    for (int kp = kw; kp < q.Kp; kp += q.kw) {
+      if (q.ring == 4)
+        asm volatile("cp.async.wait_group 2;" ::: "memory");
+      else if (q.ring == 3)
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+      else
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+      __syncwarp();  // every lane's copies are there, and the slot before is read
+      fetch(free_slot);
+      const uint8_t* src = smem + ring_at + warp * q.ring * kSlot + slot * kSlot;
+      const uint16_t* es = reinterpret_cast<const uint16_t*>(src + kScales) + g;
+      const uint8_t* zs = src + kZeros + g;
+      const int* sx = sums + kp * kGroups * kCols + 2 * t;
+      free_slot = slot;
+      slot = slot + 1 == q.ring ? 0 : slot + 1;
+      int d[NT][4];
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        const uint4 u0 = *reinterpret_cast<const uint4*>(src + b * 1024 + lane * 16);
+        const uint4 u1 = *reinterpret_cast<const uint4*>(src + b * 1024 + 512 + lane * 16);
+        const uint32_t lo[4] = {u0.x, u0.y, u0.z, u0.w}, hi[4] = {u1.x, u1.y, u1.z, u1.w};
+        uint32_t x[NT][8];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const uint4 x0 = *reinterpret_cast<const uint4*>(x_col[nt] + (2 * kp + b) * 128);
+          const uint4 x1 = *reinterpret_cast<const uint4*>(x_col[nt] + (2 * kp + b) * 128 + 16);
+          x[nt][0] = x0.x; x[nt][1] = x0.y; x[nt][2] = x0.z; x[nt][3] = x0.w;
+          x[nt][4] = x1.x; x[nt][5] = x1.y; x[nt][6] = x1.z; x[nt][7] = x1.w;
+        }
+#pragma unroll
+        for (int a = 0; a < 4; ++a) {
+          const int gr = (b * 128 + a * 32) / G;
+          if (a * 32 % G == 0) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) d[nt][0] = d[nt][1] = d[nt][2] = d[nt][3] = 0;
+          }
+          const uint32_t a0 = lo[a] & 0x0F0F0F0Fu, a1 = hi[a] & 0x0F0F0F0Fu;
+          const uint32_t a2 = (lo[a] >> 4) & 0x0F0F0F0Fu, a3 = (hi[a] >> 4) & 0x0F0F0F0Fu;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) mma_u8s8(d[nt], a0, a1, a2, a3, x[nt][2 * a], x[nt][2 * a + 1]);
+          if ((a + 1) * 32 % G == 0) {
+            const float e0 = bf16_lo(es[gr * 16]), e1 = bf16_lo(es[gr * 16 + 8]);
+            const int z0 = ASYM ? zs[gr * 16] : 8, z1 = ASYM ? zs[gr * 16 + 8] : 8;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              const int2 sm = *reinterpret_cast<const int2*>(sx + gr * kCols + nt * 8);
+              acc[nt][0] = fmaf(static_cast<float>(d[nt][0] - z0 * sm.x), e0, acc[nt][0]);
+              acc[nt][1] = fmaf(static_cast<float>(d[nt][1] - z0 * sm.y), e0, acc[nt][1]);
+              acc[nt][2] = fmaf(static_cast<float>(d[nt][2] - z1 * sm.x), e1, acc[nt][2]);
+              acc[nt][3] = fmaf(static_cast<float>(d[nt][3] - z1 * sm.y), e1, acc[nt][3]);
+            }
+          }
+        }
+      }
+    }
+    // [team][warp][columns][16] sums; the other side is free once the team has met again
+    float* mine = part + (side * kTeamWarps + warp) * kCols * 16;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        mine[(nt * 8 + 2 * t + (c & 1)) * 16 + g + (c & 2) * 4] = acc[nt][c];
+        acc[nt][c] = 0.0f;
+      }
+    if (q.kw == 1)
+      __syncwarp();
+    else
+      asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "r"(q.kw * 32) : "memory");
+    const float* all = part + (side * kTeamWarps + team * q.kw) * kCols * 16;
+    for (int i = kw * 32 + lane; i < p.M * 8; i += q.kw * 32) {
+      const int m = i / 8, r = i % 8 * 2;
+      const int64_t n = static_cast<int64_t>(rt) * 16 + r;
+      if (n >= p.N) continue;
+      float y0 = 0.0f, y1 = 0.0f;
+      for (int k = 0; k < q.kw; ++k) {
+        const float* c = all + (k * kCols + 3 * m) * 16 + r;
+        const float2 v0 = *reinterpret_cast<const float2*>(c), v1 = *reinterpret_cast<const float2*>(c + 16);
+        const float2 v2 = *reinterpret_cast<const float2*>(c + 32);
+        y0 += fmaf(fmaf(v0.x, 256.0f, v1.x), 256.0f, v2.x);
+        y1 += fmaf(fmaf(v0.y, 256.0f, v1.y), 256.0f, v2.y);
+      }
+      y0 *= s_back[m];
+      y1 *= s_back[m];
+      if (p.bias != nullptr) {
+        const uint32_t b = __ldg(reinterpret_cast<const uint32_t*>(p.bias + n));
+        y0 += bf16_lo(b);
+        y1 += bf16_hi(b);
+      }
+      *reinterpret_cast<__nv_bfloat162*>(p.Y + m * p.N + n) = __floats2bfloat162_rn(y0, y1);
+    }
+    if (q.sides == 2) side ^= 1;
+  }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+}
+
+template <int G, bool ASYM>
+int64_t team_smem(const TeamParams& q, int nt) {
+  const int64_t cols = nt * 8;
+  return 3 * q.p.M * q.col_bytes + static_cast<int64_t>(q.Kp) * (256 / G) * cols * 4 +
+         kTeamWarps * q.ring * team_slot_bytes<G, ASYM>() + q.sides * kTeamWarps * cols * 64;
+}
+
+// Warps of a team. A round of tiles takes an SM the time of its bytes, but a tile never less than
+// its team's warps need for it, about a tenth of the SM's bandwidth each; teams with more than
+// one tile wait for their slowest warp at each. Among equals the larger team, which is done sooner
+// with a small weight (measured, us, kw 1 / 8 / 16: 28672 x 8192 25 / 31 / 33, 4096 x 4096 8.8 / 4.5 / 4.9).
+int team_warps(int64_t Nt, int sms, int Kp) {
+  const int64_t tiles = (Nt + sms - 1) / sms;  // of an SM
+  int best = 1;
+  double least = 1e30;
+  for (int kw = 1; kw <= kTeamWarps && kw <= Kp; ++kw) {
+    const int64_t teams = kTeamWarps / kw, rounds = (tiles + teams - 1) / teams;
+    const double slow = 10.0 / kw;
+    double cost = static_cast<double>(rounds - 1) * std::max<double>(teams, slow) +
+                  std::max<double>(tiles - (rounds - 1) * teams, slow);
+    if (kw > 1 && rounds > 1) cost += 0.3 * rounds;
+    if (cost <= least) least = cost, best = kw;
+  }
+  return best;
+}
+
+template <int NT, int G, bool ASYM>
+cudaError_t launch_team(const TeamParams& q, int sms, cudaStream_t stream) {
+  auto kernel = int4_team_kernel<NT, G, ASYM>;
+  const int smem = static_cast<int>(team_smem<G, ASYM>(q, NT));
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  const int64_t ctas = std::min<int64_t>(sms, (q.p.N + 15) / 16);
+  return launch_kernel(kernel, dim3(static_cast<unsigned>(ctas)), dim3(kTeamWarps * 32), smem, stream, true, q);
+}
+
 template <int NT, int G, bool ASYM, int RW, int PF>
 cudaError_t launch_linear(LinearParams p, cudaStream_t stream) {
   constexpr int kBlocks = kInt4Threads / 32 / RW * PF, kCols = kBlocks * 128, kRows = RW * 16;
@@ -427,7 +733,24 @@ cudaError_t launch_linear(LinearParams p, cudaStream_t stream) {
 
 template <int G, bool ASYM>
 cudaError_t launch_linear_g(const LinearParams& p, cudaStream_t stream) {
-  if (p.M <= 8) return launch_linear<1, G, ASYM, 1, 4>(p, stream);
+  if (p.M <= 8) {
+    TeamParams q;
+    q.p = p;
+    q.Kp = (p.Kb + 1) / 2;
+    q.col_bytes = q.Kp * 256 + 16;  // an odd number of 16-byte units: no bank conflicts
+    int dev = 0, sms = 148;
+    cudaGetDevice(&dev);
+    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    const int64_t Nt = (p.N + 15) / 16;
+    q.kw = team_warps(Nt, sms, q.Kp);
+    q.sides = Nt > static_cast<int64_t>(sms) * (kTeamWarps / q.kw) ? 2 : 1;
+    const int nt = (3 * p.M + 7) / 8;
+    for (q.ring = 4; q.ring >= 2; --q.ring)
+      if (team_smem<G, ASYM>(q, nt) + 1024 <= kSmemMax)
+        return nt == 1 ? launch_team<1, G, ASYM>(q, sms, stream)
+                       : nt == 2 ? launch_team<2, G, ASYM>(q, sms, stream) : launch_team<3, G, ASYM>(q, sms, stream);
+  }
+  if (p.M <= 8) return launch_linear<1, G, ASYM, 8, 4>(p, stream);
   if (p.M <= 16) return launch_linear<2, G, ASYM, 8, 4>(p, stream);
   if (p.M <= 32) return launch_linear<4, G, ASYM, 8, 4>(p, stream);
   return launch_linear<8, G, ASYM, 8, 2>(p, stream);
