@@ -614,6 +614,8 @@ sq_status sq_int4_linear(const void* X_bf16, int64_t M, int64_t K, int64_t ldx, 
   a.group = static_cast<int>(group);
   a.bias = static_cast<const uint16_t*>(bias_bf16);
   a.Y = static_cast<uint16_t*>(Y_bf16);
+  a.status = sq::device_status_word();
+  if (a.status == nullptr) return fail(SQ_ERR_CUDA, "%s: device status word not found", fn);
   cudaError_t e = sq::launch_int4_linear(a, reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? SQ_OK : cuda_fail(e, fn);
 }

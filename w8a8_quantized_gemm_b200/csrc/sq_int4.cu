@@ -222,192 +222,9 @@ struct LinearParams {
   const uint16_t* bias;
   uint16_t* Y;
   int M, K, Kb, groups;
-  int split;   // CTAs of a cluster, which share a row block's columns
-  int stages;  // 1 when a CTA's columns are one chunk
 };
 
-// The tokens' product with the weight streams the codes once: 16x8x16 matrix instructions with
-// the weight rows as the 16 rows and up to 8 NT tokens as columns. A CTA takes RW row tiles, its
-// 8 / RW warps of a tile take the 128-column blocks in turn; each lane's fragments of a block
-// are two 16-byte loads, PF blocks ahead in registers. Activations, scales and zero points of a
-// chunk of columns are staged in shared memory by asynchronous copies, one chunk ahead. Codes
-// become bf16 exactly (128 + code, minus 128 + zero); a group's fp32 sum is scaled and added to
-// the total. Warps of a tile, and the CTAs of a cluster along K, are joined in a fixed order
-// through (distributed) shared memory.
-template <int NT, int G, bool ASYM, int RW, int PF>
-__global__ void __launch_bounds__(kInt4Threads) int4_linear_kernel(const LinearParams p) {
-  constexpr int W = kInt4Threads / 32, KW = W / RW, kBlocks = KW * PF, kCols = kBlocks * 128, kRows = RW * 16;
-  constexpr int kStride = (kCols + 8) * 2, kGroups = kCols / G;
-  extern __shared__ __align__(16) uint8_t smem[];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int rw = warp % RW, kw = warp / RW;
-  const int rank = blockIdx.x % p.split;
-  const int64_t row_block = blockIdx.x / p.split, rt = row_block * RW + rw, n0 = row_block * kRows;
-  const int kb0 = static_cast<int>(static_cast<int64_t>(p.Kb) * rank / p.split);
-  const int kb1 = static_cast<int>(static_cast<int64_t>(p.Kb) * (rank + 1) / p.split);
-  const bool rows_in = rt * 16 < p.N;
-  const uint8_t* tiles = p.Wp + rt * p.Kb * kTileBytes;
-  // the weight does not depend on the kernel before in a decode step: its way into L2 starts
-  // before waiting for that kernel (a hint, safe even if that kernel wrote the weight)
-  if (rows_in && kw == 0 && lane == 0)
-    bulk_prefetch_l2(tiles + static_cast<int64_t>(kb0) * kTileBytes,
-                     static_cast<uint32_t>(min(kb1 - kb0, kBlocks)) * kTileBytes);
-  griddep_wait();
-  griddep_launch_dependents();
-
-  const int x_bytes = (p.M + 1) * kStride, stage_bytes = x_bytes + kGroups * kRows * (ASYM ? 3 : 2);
-  const uint32_t smem32 = smem_u32(smem);
-  auto stage_in = [&](int kb, int stage) {  // the chunk of columns from block kb on
-    const uint32_t dst = smem32 + stage * stage_bytes;
-    const int k0 = kb * 128, k1 = min(p.K, kb1 * 128);
-    for (int i = threadIdx.x; i < p.M * (kCols / 8); i += kInt4Threads) {
-      const int m = i / (kCols / 8), k = i % (kCols / 8) * 8;
-      const bool in = k0 + k < k1;
-      cp_async<16>(dst + m * kStride + k * 2, p.X + (in ? m * p.ldx + k0 + k : 0), in);
-    }
-    for (int i = threadIdx.x; i < kGroups * (kRows / 8); i += kInt4Threads) {
-      const int gr = k0 / G + i / (kRows / 8), r = i % (kRows / 8) * 8;
-      const bool in = gr < p.groups && n0 + r < p.N;
-      const int64_t at = in ? gr * p.N + n0 + r : 0;
-      cp_async<16>(dst + x_bytes + i * 16, p.scale + at, in);
-      if (ASYM) cp_async<8>(dst + x_bytes + kGroups * kRows * 2 + i * 8, p.zero + at, in);
-    }
-    asm volatile("cp.async.commit_group;" ::: "memory");
-  };
-  uint4 w[PF][2];
-  auto fetch = [&](int i, int kb) {
-    if (rows_in && kb < kb1) {
-      const uint4* src = reinterpret_cast<const uint4*>(tiles + static_cast<int64_t>(kb) * kTileBytes) + lane;
-      w[i][0] = __ldcs(src);
-      w[i][1] = __ldcs(src + 32);
-    }
-  };
-#pragma unroll
-  for (int i = 0; i < PF; ++i) {
-    w[i][0] = w[i][1] = make_uint4(0, 0, 0, 0);
-    fetch(i, kb0 + i * KW + kw);
-  }
-  stage_in(kb0, 0);
-  // row M of each stage: zeros, for the tokens that fill up the last 8
-  for (int i = threadIdx.x; i < kStride / 16 * p.stages; i += kInt4Threads)
-    *reinterpret_cast<uint4*>(smem + (i / (kStride / 16)) * stage_bytes + p.M * kStride + i % (kStride / 16) * 16) =
-        make_uint4(0, 0, 0, 0);
-
-  float acc[NT][4];
-  uint32_t x_row[NT];  // this lane's row address for loading the activations' fragments
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) acc[nt][e] = 0.0f;
-    x_row[nt] = smem32 + min(nt * 8 + (lane & 7), p.M) * kStride + (lane >> 3) * 16;
-  }
-  int stage = 0;
-  for (int kb = kb0; kb < kb1; kb += kBlocks) {
-    if (kb + kBlocks < kb1) {
-      stage_in(kb + kBlocks, stage ^ 1);
-      asm volatile("cp.async.wait_group 1;" ::: "memory");
-    } else {
-      asm volatile("cp.async.wait_group 0;" ::: "memory");
-    }
-    __syncthreads();
-    const uint32_t base = stage * stage_bytes;
-    const uint16_t* es = reinterpret_cast<const uint16_t*>(smem + base + x_bytes) + rw * 16 + g;
-    const uint8_t* zs = smem + base + x_bytes + kGroups * kRows * 2 + rw * 16 + g;
-#pragma unroll
-    for (int i = 0; i < PF; ++i) {
-      const int block = i * KW + kw;  // of the chunk
-      if (kb + block < kb1) {
-        const uint32_t lo[4] = {w[i][0].x, w[i][0].y, w[i][0].z, w[i][0].w};
-        const uint32_t hi[4] = {w[i][1].x, w[i][1].y, w[i][1].z, w[i][1].w};
-        float d[NT][4];
-#pragma unroll
-        for (int a = 0; a < 4; ++a) {
-          const int gr = (block * 128 + a * 32) / G * kRows;
-          const uint32_t z0 = ASYM ? zero_pair(zs[gr]) : 0x43084308u, z1 = ASYM ? zero_pair(zs[gr + 8]) : 0x43084308u;
-          if (a * 32 % G == 0) {
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-              for (int e = 0; e < 4; ++e) d[nt][e] = 0.0f;
-          }
-          uint32_t f[2][4];
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            f[j][0] = sub_bf16x2(((lo[a] >> (8 * j)) & 0x000F000Fu) | 0x43004300u, z0);
-            f[j][1] = sub_bf16x2(((hi[a] >> (8 * j)) & 0x000F000Fu) | 0x43004300u, z1);
-            f[j][2] = sub_bf16x2(((lo[a] >> (8 * j + 4)) & 0x000F000Fu) | 0x43004300u, z0);
-            f[j][3] = sub_bf16x2(((hi[a] >> (8 * j + 4)) & 0x000F000Fu) | 0x43004300u, z1);
-          }
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            uint32_t x[4];
-            ldmatrix(x, x_row[nt] + base + block * 256 + a * 64);
-            mma_bf16(d[nt], f[0], x[0], x[1]);
-            mma_bf16(d[nt], f[1], x[2], x[3]);
-          }
-          if ((a + 1) * 32 % G == 0) {
-            const float e0 = bf16_lo(es[gr]), e1 = bf16_lo(es[gr + 8]);
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              acc[nt][0] = fmaf(d[nt][0], e0, acc[nt][0]);
-              acc[nt][1] = fmaf(d[nt][1], e0, acc[nt][1]);
-              acc[nt][2] = fmaf(d[nt][2], e1, acc[nt][2]);
-              acc[nt][3] = fmaf(d[nt][3], e1, acc[nt][3]);
-            }
-          }
-        }
-      }
-      fetch(i, kb + kBlocks + block);
-    }
-    __syncthreads();
-    stage ^= 1;
-  }
-
-  // [KW][M][kRows] partial sums in the staging area
-  float* part = reinterpret_cast<float*>(smem);
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int m = nt * 8 + 2 * t + (e & 1);
-      if (m < p.M) part[(kw * p.M + m) * kRows + rw * 16 + g + (e & 2) * 4] = acc[nt][e];
-    }
-  if (p.split > 1)
-    cluster_sync();
-  else
-    __syncthreads();
-  const int share = kRows / 2 / p.split;  // row pairs that this CTA of the cluster finishes
-  for (int i = threadIdx.x; i < p.M * share; i += kInt4Threads) {
-    const int m = i / share, r = (rank * share + i % share) * 2;
-    const int64_t n = n0 + r;
-    if (n >= p.N) continue;
-    float y0 = 0.0f, y1 = 0.0f;
-    for (int c = 0; c < p.split; ++c) {
-#pragma unroll
-      for (int k = 0; k < KW; ++k) {
-        const float* at = part + (k * p.M + m) * kRows + r;
-        if (p.split > 1) {
-          const uint32_t a = mapa_shared(at, c);
-          y0 += ld_cluster_f32(a);
-          y1 += ld_cluster_f32(a + 4);
-        } else {
-          y0 += at[0];
-          y1 += at[1];
-        }
-      }
-    }
-    if (p.bias != nullptr) {
-      const uint32_t b = __ldg(reinterpret_cast<const uint32_t*>(p.bias + n));
-      y0 += bf16_lo(b);
-      y1 += bf16_hi(b);
-    }
-    const __nv_bfloat162 y = __floats2bfloat162_rn(y0, y1);
-    *reinterpret_cast<__nv_bfloat162*>(p.Y + m * p.N + n) = y;
-  }
-  if (p.split > 1) cluster_sync();  // no CTA leaves while its sums are being read
-}
-
-// ---- up to 8 tokens: int8 matrix instructions.
+// ---- up to 4 tokens: int8 matrix instructions.
 // Making bf16 of 4-bit codes costs a logic operation, most of a shift and a subtraction per pair;
 // for a few tokens that is most of the work, and it bounds the kernel (measured: 230 instructions
 // for a 1024-byte block, 41 us at 1 x 28672 x 8192 whatever the copies do). Bytes are cheaper: a
@@ -425,6 +242,7 @@ __global__ void __launch_bounds__(kInt4Threads) int4_linear_kernel(const LinearP
 // and with nothing to wait for but the copies. The team meets once a tile to add its warps' sums
 // up in order.
 constexpr int kTeamWarps = 16;  // of a CTA, one CTA per SM
+constexpr int kTeamTokens = 4;
 constexpr int64_t kSmemMax = 232448;
 
 struct TeamParams {
@@ -456,7 +274,7 @@ __global__ void __launch_bounds__(kTeamWarps * 32, 1) int4_team_kernel(const Tea
   constexpr int kScales = 2 * kTileBytes, kZeros = kScales + kGroups * 32;
   const LinearParams& p = q.p;
   extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ float s_top[kTeamWarps], s_mul[8], s_back[8];
+  __shared__ float s_top[kTeamWarps], s_mul[kTeamTokens], s_back[kTeamTokens];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int teams = kTeamWarps / q.kw, team = warp / q.kw, kw = warp % q.kw;
   const int Nt = static_cast<int>((p.N + 15) / 16), step = gridDim.x * teams;
@@ -516,7 +334,7 @@ __global__ void __launch_bounds__(kTeamWarps * 32, 1) int4_team_kernel(const Tea
   for (int i = 0; i < q.ring - 1; ++i) fetch(i);
 
   // ---- activations to bytes: the tokens' largest values, each by an equal share of the warps
-  const int share = kTeamWarps / p.M;  // warps of a token, at least 2
+  const int share = kTeamWarps / p.M;  // warps of a token
   if (warp < share * p.M) {
     const uint16_t* x = p.X + warp / share * p.ldx;
     float top = 0.0f;
@@ -713,47 +531,317 @@ cudaError_t launch_team(const TeamParams& q, int sms, cudaStream_t stream) {
   return launch_kernel(kernel, dim3(static_cast<unsigned>(ctas)), dim3(kTeamWarps * 32), smem, stream, true, q);
 }
 
-template <int NT, int G, bool ASYM, int RW, int PF>
-cudaError_t launch_linear(LinearParams p, cudaStream_t stream) {
-  constexpr int kBlocks = kInt4Threads / 32 / RW * PF, kCols = kBlocks * 128, kRows = RW * 16;
-  const int64_t blocks = (p.N + kRows - 1) / kRows;
-  // split along K until two CTAs per SM exist, as long as every CTA keeps a chunk of columns
-  p.split = 1;
-  while (p.split < 8 && blocks * p.split < 2 * 148 && p.Kb >= 2 * p.split * kBlocks) p.split *= 2;
-  const int most = (p.Kb + p.split - 1) / p.split;
-  p.stages = most > kBlocks ? 2 : 1;
-  const size_t stage = (p.M + 1) * (kCols + 8) * 2 + kCols / G * kRows * (ASYM ? 3 : 2);
-  const size_t smem = std::max(stage * p.stages, static_cast<size_t>(p.M) * kRows * (kInt4Threads / 32 / RW) * 4);
-  auto kernel = int4_linear_kernel<NT, G, ASYM, RW, PF>;
+// ---- more tokens, or rows too long for the above: bf16 matrix instructions.
+// The weight rows are the 16 rows of 16x8x16 instructions, 8 NT tokens their columns. Codes become
+// bf16 exactly (128 + code, minus 128 + zero); a group's fp32 sum is scaled and added to the
+// total. Teams and rings as above; the activations come in chunks of `cp` pairs of column blocks
+// for all teams of a CTA, one chunk ahead, and where there are too few row tiles for that the
+// CTAs of a cluster share the columns and add their sums up, in order, through distributed
+// shared memory.
+struct WideParams {
+  LinearParams p;
+  int split;    // CTAs of a cluster
+  int kw;       // warps of a team
+  int ring;     // slots of a warp's ring, 2 to 4
+  int Kp;       // pairs of column blocks
+  int cp;       // of a chunk, a multiple of kw
+  int rounds;   // tiles of a team
+  int buffers;  // of chunks
+  unsigned int* status;
+};
+
+constexpr int wide_warps(int NT) { return NT == 8 ? 8 : 16; }  // 64 tokens' sums need the registers
+
+template <int NT, int G, bool ASYM>
+__global__ void __launch_bounds__(wide_warps(NT) * 32, 1) int4_wide_kernel(const WideParams q) {
+  constexpr int W = wide_warps(NT), kThreads = W * 32, kGroups = 256 / G, kSlot = team_slot_bytes<G, ASYM>();
+  constexpr int kScales = 2 * kTileBytes, kZeros = kScales + kGroups * 32;
+  const LinearParams& p = q.p;
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ __align__(8) uint64_t s_there[2];  // a chunk's copies are there
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int teams = W / q.kw, team = warp / q.kw, kw = warp % q.kw;
+  const int rank = blockIdx.x % q.split, cluster = blockIdx.x / q.split, clusters = gridDim.x / q.split;
+  const int Nt = static_cast<int>((p.N + 15) / 16), step = clusters * teams;
+  const int rt0 = team < teams ? cluster + clusters * team : Nt;
+  const int kp0 = static_cast<int>(static_cast<int64_t>(q.Kp) * rank / q.split);
+  const int kp1 = static_cast<int>(static_cast<int64_t>(q.Kp) * (rank + 1) / q.split);
+  if (kw == 0 && lane == 0 && rt0 < Nt)  // as above
+    bulk_prefetch_l2(p.Wp + (static_cast<int64_t>(rt0) * p.Kb + 2 * kp0) * kTileBytes,
+                     static_cast<uint32_t>(min(p.Kb - 2 * kp0, 2 * q.kw * q.ring)) * kTileBytes);
+  if (threadIdx.x == 0) {
+    mbar_init(&s_there[0], kThreads);
+    mbar_init(&s_there[1], kThreads);
+  }
+  __syncthreads();
+  griddep_wait();
+  griddep_launch_dependents();
+
+  // shared memory: chunks of activations | rings | partial sums
+  const int x_row = q.cp * 512 + 16, x_bytes = p.M * x_row;  // rows of an odd number of 16-byte units
+  const uint32_t smem32 = smem_u32(smem);
+  const int ring_at = q.buffers * x_bytes + warp * q.ring * kSlot;
+  const uint32_t ring32 = smem32 + ring_at;
+  float* part = reinterpret_cast<float*>(smem + q.buffers * x_bytes + W * q.ring * kSlot);  // [warps][M][16]
+
+  int load_rt = kp0 + kw < kp1 ? rt0 : Nt, load_kp = kp0 + kw;
+  const uint8_t* load_src = p.Wp + (static_cast<int64_t>(rt0) * p.Kb + 2 * load_kp) * kTileBytes + lane * 16;
+  const int64_t tile_jump = static_cast<int64_t>(step) * p.Kb * kTileBytes;
+  constexpr int kScaleBytes = G == 32 ? 8 : 4, kLanesPerGroup = 32 / kScaleBytes, kScaleLanes = kGroups * kLanesPerGroup;
+  const int e_group = lane / kLanesPerGroup, e_row = lane % kLanesPerGroup * (kScaleBytes / 2);
+  const int z_group = lane / 4, z_row = lane % 4 * 4;
+  auto fetch = [&](int slot) {
+    if (load_rt < Nt) {
+      const uint32_t dst = ring32 + slot * kSlot;
+      const bool second = 2 * load_kp + 1 < p.Kb;
+      cp_async<16>(dst + lane * 16, load_src, true);
+      cp_async<16>(dst + 512 + lane * 16, load_src + 512, true);
+      cp_async<16>(dst + 1024 + lane * 16, load_src + (second ? 1024 : 0), second);
+      cp_async<16>(dst + 1536 + lane * 16, load_src + (second ? 1536 : 0), second);
+      if (lane < kScaleLanes) {
+        const int gr = load_kp * kGroups + e_group, n = load_rt * 16 + e_row;
+        const bool in = gr < p.groups && n < p.N;
+        cp_async<kScaleBytes>(dst + kScales + lane * kScaleBytes, p.scale + (in ? gr * p.N + n : 0), in);
+      }
+      if (ASYM && lane < 4 * kGroups) {
+        const int gr = load_kp * kGroups + z_group, n = load_rt * 16 + z_row;
+        const bool in = gr < p.groups && n < p.N;
+        cp_async<4>(dst + kZeros + lane * 4, p.zero + (in ? gr * p.N + n : 0), in);
+      }
+      load_kp += q.kw;
+      load_src += 2 * q.kw * kTileBytes;
+      if (load_kp >= kp1) {
+        load_src += tile_jump - static_cast<int64_t>(load_kp - kp0 - kw) * 2 * kTileBytes;
+        load_kp = kp0 + kw;
+        load_rt += step;
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  // chunk c of this CTA's columns into a buffer; each thread's copies report to the buffer's barrier
+  auto bring = [&](int c, int buffer) {
+    const uint32_t dst = smem32 + buffer * x_bytes;
+    const int k0 = (kp0 + c * q.cp) * 256, cols = min(q.cp, kp1 - kp0 - c * q.cp) * 32;  // of 8 columns
+    for (int m = warp; m < p.M; m += W)
+      for (int i = lane; i < cols; i += 32) {
+        const bool in = k0 + i * 8 < p.K;
+        cp_async<16>(dst + m * x_row + i * 16, p.X + m * p.ldx + (in ? k0 + i * 8 : 0), in);
+      }
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(smem_u32(&s_there[buffer])) : "memory");
+  };
+
+  const int chunks = (kp1 - kp0 + q.cp - 1) / q.cp, steps = q.rounds * chunks;
+  const bool resident = chunks <= 2;  // each chunk stays in a buffer of its own
+  bring(0, 0);
+#pragma unroll 1
+  for (int i = 0; i < q.ring - 1; ++i) fetch(i);
+
+  uint32_t x_lane[NT];  // this lane's row for loading fragments; columns past M repeat the last token, unread
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) x_lane[nt] = smem32 + min(nt * 8 + (lane & 7), p.M - 1) * x_row + (lane >> 3) * 16;
+  float acc[NT][4];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) acc[nt][0] = acc[nt][1] = acc[nt][2] = acc[nt][3] = 0.0f;
+  int slot = 0, free_slot = q.ring - 1, chunk = 0, rt = rt0;
+  unsigned phase = 0;  // bit b: parity of buffer b's next chunk
+  for (int s = 0; s < steps; ++s) {
+    __syncthreads();  // the chunk before is read
+    if (s + 1 < steps && (!resident || s + 1 < chunks)) bring(chunk + 1 < chunks ? chunk + 1 : 0, (s + 1) & 1);
+    const int buffer = resident ? chunk : s & 1;
+    if (!resident || s < chunks) {
+      if (!mbar_wait_bounded(&s_there[buffer], (phase >> buffer) & 1, kDefaultWaitLimitNs) && lane == 0)
+        atomicOr(q.status, kErrProducerWait);
+      phase ^= 1u << buffer;
+    }
+    const int here = min(q.cp, kp1 - kp0 - chunk * q.cp);  // pairs of the chunk
+    if (rt < Nt) {
+#pragma unroll 1
+      for (int j = kw; j < here; j += q.kw) {
+        if (q.ring == 4)
+          asm volatile("cp.async.wait_group 2;" ::: "memory");
+        else if (q.ring == 3)
+          asm volatile("cp.async.wait_group 1;" ::: "memory");
+        else
+          asm volatile("cp.async.wait_group 0;" ::: "memory");
+        __syncwarp();  // every lane's copies are there, and the slot before is read
+        fetch(free_slot);
+        const uint8_t* src = smem + ring_at + slot * kSlot;
+        const uint16_t* es = reinterpret_cast<const uint16_t*>(src + kScales) + g;
+        const uint8_t* zs = src + kZeros + g;
+        free_slot = slot;
+        slot = slot + 1 == q.ring ? 0 : slot + 1;
+        const uint32_t x_at = buffer * x_bytes + j * 512;
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          const uint4 u0 = *reinterpret_cast<const uint4*>(src + b * 1024 + lane * 16);
+          const uint4 u1 = *reinterpret_cast<const uint4*>(src + b * 1024 + 512 + lane * 16);
+          const uint32_t lo[4] = {u0.x, u0.y, u0.z, u0.w}, hi[4] = {u1.x, u1.y, u1.z, u1.w};
+          float d[NT][4];
+          uint32_t z0 = 0x43084308u, z1 = 0x43084308u;
+#pragma unroll
+          for (int a = 0; a < 4; ++a) {
+            const int gr = (b * 128 + a * 32) / G * 16;
+            if (a * 32 % G == 0) {
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) d[nt][0] = d[nt][1] = d[nt][2] = d[nt][3] = 0.0f;
+              if (ASYM) {
+                z0 = zero_pair(zs[gr]);
+                z1 = zero_pair(zs[gr + 8]);
+              }
+            }
+            uint32_t f[2][4];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              f[h][0] = sub_bf16x2(((lo[a] >> (8 * h)) & 0x000F000Fu) | 0x43004300u, z0);
+              f[h][1] = sub_bf16x2(((hi[a] >> (8 * h)) & 0x000F000Fu) | 0x43004300u, z1);
+              f[h][2] = sub_bf16x2(((lo[a] >> (8 * h + 4)) & 0x000F000Fu) | 0x43004300u, z0);
+              f[h][3] = sub_bf16x2(((hi[a] >> (8 * h + 4)) & 0x000F000Fu) | 0x43004300u, z1);
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              uint32_t x[4];
+              ldmatrix(x, x_lane[nt] + x_at + b * 256 + a * 64);
+              mma_bf16(d[nt], f[0], x[0], x[1]);
+              mma_bf16(d[nt], f[1], x[2], x[3]);
+            }
+            if ((a + 1) * 32 % G == 0) {
+              const float e0 = bf16_lo(es[gr]), e1 = bf16_lo(es[gr + 8]);
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                acc[nt][0] = fmaf(d[nt][0], e0, acc[nt][0]);
+                acc[nt][1] = fmaf(d[nt][1], e0, acc[nt][1]);
+                acc[nt][2] = fmaf(d[nt][2], e1, acc[nt][2]);
+                acc[nt][3] = fmaf(d[nt][3], e1, acc[nt][3]);
+              }
+            }
+          }
+        }
+      }
+    }
+    if (++chunk < chunks) continue;
+    chunk = 0;
+    // ---- the tiles of this round are done: partial sums of every warp, then each CTA of the
+    // cluster finishes its share of the outputs
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int m = nt * 8 + 2 * t + (e & 1);
+        if (m < p.M) part[(warp * p.M + m) * 16 + g + (e & 2) * 4] = acc[nt][e];
+        acc[nt][e] = 0.0f;
+      }
+    if (q.split > 1)
+      cluster_sync();
+    else
+      __syncthreads();
+    const int64_t tile0 = cluster + static_cast<int64_t>(s / chunks) * step;  // the first team's tile
+    for (int i = threadIdx.x * q.split + rank; i < teams * p.M * 8; i += kThreads * q.split) {
+      const int r = i % 8 * 2, m = i / 8 % p.M, tm = i / 8 / p.M;
+      const int64_t row = (tile0 + clusters * tm) * 16 + r;
+      if (row >= p.N) continue;
+      float y0 = 0.0f, y1 = 0.0f;
+      for (int c = 0; c < q.split; ++c)
+        for (int k = 0; k < q.kw; ++k) {
+          const float* at = part + ((tm * q.kw + k) * p.M + m) * 16 + r;
+          if (q.split > 1) {
+            const uint32_t remote = mapa_shared(at, c);
+            y0 += ld_cluster_f32(remote);
+            y1 += ld_cluster_f32(remote + 4);
+          } else {
+            y0 += at[0];
+            y1 += at[1];
+          }
+        }
+      if (p.bias != nullptr) {
+        const uint32_t b = __ldg(reinterpret_cast<const uint32_t*>(p.bias + row));
+        y0 += bf16_lo(b);
+        y1 += bf16_hi(b);
+      }
+      *reinterpret_cast<__nv_bfloat162*>(p.Y + m * p.N + row) = __floats2bfloat162_rn(y0, y1);
+    }
+    if (q.split > 1) cluster_sync();  // the sums are read: they may be overwritten, or the CTA may end
+    rt += step;
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
+template <int NT, int G, bool ASYM>
+cudaError_t launch_wide(const LinearParams& p, int sms, unsigned int* status, cudaStream_t stream) {
+  constexpr int W = wide_warps(NT), kSlot = team_slot_bytes<G, ASYM>();
+  WideParams q{};
+  q.p = p;
+  q.Kp = (p.Kb + 1) / 2;
+  q.status = status;
+  const int64_t Nt = (p.N + 15) / 16;
+  // Cost in units of one pair of blocks at the SM's share of the bandwidth, or of the matrix
+  // instructions where they take longer; a warp alone reaches about a tenth of that. A round of
+  // tiles has its start and end, a cluster's joins cost as much again.
+  const double unit = std::max(1.0, NT * 64 / 176.0);
+  double least = 1e30;
+  size_t smem = 0;
+  for (int split = 1; split <= 8 && split <= q.Kp; split *= 2) {
+    const int64_t clusters = sms / split, tiles = (Nt + clusters - 1) / clusters;
+    const int pairs = (q.Kp + split - 1) / split;
+    for (int kw = 1; kw <= W && kw <= pairs; ++kw) {
+      const int64_t teams = W / kw, rounds = (tiles + teams - 1) / teams;
+      const double slow = 0.6 * W / kw;
+      const double full = static_cast<double>(rounds - 1) * std::max<double>(teams, slow) +
+                          std::max<double>(tiles - (rounds - 1) * teams, slow);
+      const double cost = full * pairs * unit + rounds * (split > 1 ? 60 : 30);
+      if (cost >= least) continue;
+      // the largest chunks, up to all columns, that leave three slots for every ring
+      const int64_t room = kSmemMax - 1024 - static_cast<int64_t>(W) * p.M * 64;
+      for (int ring = 4; ring >= 2; --ring) {
+        const int64_t left = room - W * ring * kSlot, row = 512;
+        int64_t all = (pairs + kw - 1) / kw * kw;
+        int buffers = 1;
+        if (p.M * (all * row + 16) > left) {
+          buffers = 2;
+          all = (left / 2 / p.M - 16) / row / kw * kw;
+        }
+        if (all < kw || (ring > 2 && buffers == 2 && all * p.M < 64)) continue;
+        least = cost;
+        q.split = split;
+        q.kw = kw;
+        q.ring = ring;
+        q.cp = static_cast<int>(all);
+        q.rounds = static_cast<int>(rounds);
+        q.buffers = buffers;
+        smem = static_cast<size_t>(buffers * p.M * (all * row + 16) + W * ring * kSlot + W * p.M * 64);
+        break;
+      }
+    }
+  }
+  const int64_t clusters = std::min<int64_t>(sms / q.split, Nt);
+  auto kernel = int4_wide_kernel<NT, G, ASYM>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return e;
-  return launch_kernel_clustered(kernel, dim3(static_cast<unsigned>(blocks * p.split)), dim3(kInt4Threads), smem, stream,
-                                 true, static_cast<unsigned>(p.split), p);
+  return launch_kernel_clustered(kernel, dim3(static_cast<unsigned>(clusters * q.split)), dim3(W * 32), smem, stream,
+                                 true, static_cast<unsigned>(q.split), q);
 }
 
 template <int G, bool ASYM>
-cudaError_t launch_linear_g(const LinearParams& p, cudaStream_t stream) {
-  if (p.M <= 8) {
+cudaError_t launch_linear(const LinearParams& p, unsigned int* status, cudaStream_t stream) {
+  int dev = 0, sms = 148;
+  cudaGetDevice(&dev);
+  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (p.M <= kTeamTokens) {
     TeamParams q;
     q.p = p;
     q.Kp = (p.Kb + 1) / 2;
     q.col_bytes = q.Kp * 256 + 16;  // an odd number of 16-byte units: no bank conflicts
-    int dev = 0, sms = 148;
-    cudaGetDevice(&dev);
-    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     const int64_t Nt = (p.N + 15) / 16;
     q.kw = team_warps(Nt, sms, q.Kp);
     q.sides = Nt > static_cast<int64_t>(sms) * (kTeamWarps / q.kw) ? 2 : 1;
     const int nt = (3 * p.M + 7) / 8;
     for (q.ring = 4; q.ring >= 2; --q.ring)
       if (team_smem<G, ASYM>(q, nt) + 1024 <= kSmemMax)
-        return nt == 1 ? launch_team<1, G, ASYM>(q, sms, stream)
-                       : nt == 2 ? launch_team<2, G, ASYM>(q, sms, stream) : launch_team<3, G, ASYM>(q, sms, stream);
+        return nt == 1 ? launch_team<1, G, ASYM>(q, sms, stream) : launch_team<2, G, ASYM>(q, sms, stream);
   }
-  if (p.M <= 8) return launch_linear<1, G, ASYM, 8, 4>(p, stream);
-  if (p.M <= 16) return launch_linear<2, G, ASYM, 8, 4>(p, stream);
-  if (p.M <= 32) return launch_linear<4, G, ASYM, 8, 4>(p, stream);
-  return launch_linear<8, G, ASYM, 8, 2>(p, stream);
+  if (p.M <= 8) return launch_wide<1, G, ASYM>(p, sms, status, stream);
+  if (p.M <= 16) return launch_wide<2, G, ASYM>(p, sms, status, stream);
+  if (p.M <= 32) return launch_wide<4, G, ASYM>(p, sms, status, stream);
+  return launch_wide<8, G, ASYM>(p, sms, status, stream);
 }
 
 // Grid of the two tile kernels: one column block per x, row tiles over y so that about eight
@@ -798,11 +886,11 @@ cudaError_t launch_int4_linear(const Int4LinearArgs& a, cudaStream_t stream) {
   p.Kb = (p.K + 127) / 128;
   p.groups = (p.K + a.group - 1) / a.group;
   if (a.zero != nullptr) {
-    if (a.group == 32) return launch_linear_g<32, true>(p, stream);
-    return a.group == 64 ? launch_linear_g<64, true>(p, stream) : launch_linear_g<128, true>(p, stream);
+    if (a.group == 32) return launch_linear<32, true>(p, a.status, stream);
+    return a.group == 64 ? launch_linear<64, true>(p, a.status, stream) : launch_linear<128, true>(p, a.status, stream);
   }
-  if (a.group == 32) return launch_linear_g<32, false>(p, stream);
-  return a.group == 64 ? launch_linear_g<64, false>(p, stream) : launch_linear_g<128, false>(p, stream);
+  if (a.group == 32) return launch_linear<32, false>(p, a.status, stream);
+  return a.group == 64 ? launch_linear<64, false>(p, a.status, stream) : launch_linear<128, false>(p, a.status, stream);
 }
 
 }  // namespace sq

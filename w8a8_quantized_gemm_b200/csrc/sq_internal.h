@@ -203,6 +203,7 @@ struct Int4LinearArgs {
   int group = 0;
   const uint16_t* bias = nullptr;  // [N] or nullptr
   uint16_t* Y = nullptr;           // [M, N]
+  unsigned int* status = nullptr;
 };
 cudaError_t launch_int4_linear(const Int4LinearArgs& a, cudaStream_t stream);
 
