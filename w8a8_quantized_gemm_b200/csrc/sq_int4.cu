@@ -8,6 +8,7 @@
 // 8-column chunks: the A fragments of two 16x8x16 matrix instructions.
 #include "sq_internal.h"
 #include "sq_ptx.cuh"
+#include "sq_rows.cuh"
 
 #include <cuda_bf16.h>
 
@@ -37,163 +38,6 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
 // bf16 pair of 128 + z: 0x4300 is 128, whose mantissa counts in ones.
 __device__ __forceinline__ uint32_t zero_pair(uint32_t z) { return 0x43004300u | z | (z << 16); }
 
-// ---------------------------------------------------------------- quantization
-// One warp per tile, over the row tiles of one 128-column block. Lane (g, t) reads the
-// columns 32 a + 8 t .. + 7 of rows g and g + 8 (16-byte loads, 64 contiguous bytes per row),
-// so a group of 32 columns belongs to the four lanes of a quad, and two exchanges between
-// them put the codes where the layout wants them.
-template <bool ASYM>
-__global__ void __launch_bounds__(kInt4Threads)
-int4_quant_kernel(const uint16_t* __restrict__ W, int64_t N, int64_t K, int64_t ldw, const float* __restrict__ s,
-                  int group, uint8_t* __restrict__ Wp, uint16_t* __restrict__ scale, uint8_t* __restrict__ zero) {
-  griddep_wait();
-  griddep_launch_dependents();
-  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int64_t Nt = (N + 15) / 16, Kb = (K + 127) / 128;
-  const int64_t kb = blockIdx.x;
-  const int span = group / 32;  // 32-column blocks of a group
-  float sv[4][8];
-#pragma unroll
-  for (int a = 0; a < 4; ++a) {
-    const int64_t k = kb * 128 + a * 32 + t * 8;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) sv[a][i] = 1.0f;
-    if (s != nullptr && k < K) {
-      const float4 x = __ldg(reinterpret_cast<const float4*>(s + k)), y = __ldg(reinterpret_cast<const float4*>(s + k + 4));
-      sv[a][0] = x.x; sv[a][1] = x.y; sv[a][2] = x.z; sv[a][3] = x.w;
-      sv[a][4] = y.x; sv[a][5] = y.y; sv[a][6] = y.z; sv[a][7] = y.w;
-    }
-  }
-  const int64_t rt0 = static_cast<int64_t>(blockIdx.y) * (kInt4Threads / 32) + (threadIdx.x >> 5);
-  for (int64_t rt = rt0; rt < Nt; rt += static_cast<int64_t>(gridDim.y) * (kInt4Threads / 32)) {
-    uint4 raw[2][4];
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int a = 0; a < 4; ++a) {
-        const int64_t n = rt * 16 + h * 8 + g, k = kb * 128 + a * 32 + t * 8;
-        raw[h][a] = (n < N && k < K) ? __ldcs(reinterpret_cast<const uint4*>(W + n * ldw + k)) : make_uint4(0, 0, 0, 0);
-      }
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int64_t n = rt * 16 + h * 8 + g;
-      float hi[4], lo[4];  // per 32-column block: max |w'| (symmetric), or max and min with 0
-#pragma unroll
-      for (int a = 0; a < 4; ++a) {
-        const uint32_t w[4] = {raw[h][a].x, raw[h][a].y, raw[h][a].z, raw[h][a].w};
-        hi[a] = lo[a] = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float v = __fmul_rn(i & 1 ? bf16_hi(w[i / 2]) : bf16_lo(w[i / 2]), sv[a][i]);
-          hi[a] = fmaxf(hi[a], ASYM ? v : fabsf(v));
-          if (ASYM) lo[a] = fminf(lo[a], v);
-        }
-#pragma unroll
-        for (int o = 1; o < 4; o <<= 1) {
-          hi[a] = fmaxf(hi[a], __shfl_xor_sync(0xffffffffu, hi[a], o));
-          if (ASYM) lo[a] = fminf(lo[a], __shfl_xor_sync(0xffffffffu, lo[a], o));
-        }
-      }
-      if (span >= 2) {
-        hi[0] = hi[1] = fmaxf(hi[0], hi[1]);
-        hi[2] = hi[3] = fmaxf(hi[2], hi[3]);
-        lo[0] = lo[1] = fminf(lo[0], lo[1]);
-        lo[2] = lo[3] = fminf(lo[2], lo[3]);
-      }
-      if (span == 4) {
-        hi[0] = hi[1] = hi[2] = hi[3] = fmaxf(hi[0], hi[2]);
-        lo[0] = lo[1] = lo[2] = lo[3] = fminf(lo[0], lo[2]);
-      }
-      uint32_t word[4];
-#pragma unroll
-      for (int a = 0; a < 4; ++a) {
-        const __nv_bfloat16 e = __float2bfloat16_rn(ASYM ? __fdiv_rn(__fsub_rn(hi[a], lo[a]), 15.0f)
-                                                         : __fdiv_rn(hi[a], 7.0f));
-        const float ef = __bfloat162float(e);
-        const float r = ef > 0.0f ? fminf(__fdiv_rn(1.0f, ef), FLT_MAX) : 0.0f;
-        int z = 8;
-        if (ASYM) z = static_cast<int>(fminf(fmaxf(rintf(__fmul_rn(-lo[a], r)), 0.0f), 15.0f));
-        const int64_t k0 = kb * 128 + a * 32;
-        if (t == 0 && (a & (span - 1)) == 0 && k0 < K && n < N && SQ_GUARD(k0 / group < (K + group - 1) / group)) {
-          scale[k0 / group * N + n] = __bfloat16_as_ushort(e);
-          if (ASYM) zero[k0 / group * N + n] = static_cast<uint8_t>(z);
-        }
-        // codes of this lane's 8 columns: clamping w' r to [-z, 15 - z] before the rounding is
-        // the same as clamping the code after it
-        const float down = static_cast<float>(-z), up = static_cast<float>(15 - z);
-        const uint32_t w[4] = {raw[h][a].x, raw[h][a].y, raw[h][a].z, raw[h][a].w};
-        const bool in = n < N && k0 + t * 8 < K;
-        uint32_t pair[4];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const float v0 = __fmul_rn(__fmul_rn(bf16_lo(w[u]), sv[a][2 * u]), r);
-          const float v1 = __fmul_rn(__fmul_rn(bf16_hi(w[u]), sv[a][2 * u + 1]), r);
-          const int q0 = __float2int_rn(fminf(fmaxf(v0, down), up)) + z;
-          const int q1 = __float2int_rn(fminf(fmaxf(v1, down), up)) + z;
-          pair[u] = in ? static_cast<uint32_t>(q0 | (q1 << 16)) << (4 * t) : 0x00080008u << (4 * t);
-        }
-        // lane t keeps pair t of all four lanes
-        const bool b1 = t & 2, b0 = t & 1;
-        uint32_t p0 = b1 ? pair[2] : pair[0], p1 = b1 ? pair[3] : pair[1];
-        p0 |= __shfl_xor_sync(0xffffffffu, b1 ? pair[0] : pair[2], 2);
-        p1 |= __shfl_xor_sync(0xffffffffu, b1 ? pair[1] : pair[3], 2);
-        word[a] = (b0 ? p1 : p0) | __shfl_xor_sync(0xffffffffu, b0 ? p0 : p1, 1);
-      }
-      *reinterpret_cast<uint4*>(Wp + (rt * Kb + kb) * kTileBytes + (h * 32 + lane) * 16) =
-          make_uint4(word[0], word[1], word[2], word[3]);
-    }
-  }
-}
-
-// ---------------------------------------------------------------- values
-// The reverse: each lane collects its 8 columns' nibbles from its quad and writes 16 bytes.
-// code - zero is exact in bf16 (128 + code minus 128 + zero), so the product with the scale
-// is rounded once.
-__global__ void __launch_bounds__(kInt4Threads)
-int4_dequant_kernel(const uint8_t* __restrict__ Wp, const uint16_t* __restrict__ scale,
-                    const uint8_t* __restrict__ zero, int group, int64_t N, int64_t K, uint16_t* __restrict__ out) {
-  griddep_wait();
-  griddep_launch_dependents();
-  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int64_t Nt = (N + 15) / 16, Kb = (K + 127) / 128;
-  const int64_t kb = blockIdx.x;
-  const int64_t rt0 = static_cast<int64_t>(blockIdx.y) * (kInt4Threads / 32) + (threadIdx.x >> 5);
-  for (int64_t rt = rt0; rt < Nt; rt += static_cast<int64_t>(gridDim.y) * (kInt4Threads / 32)) {
-    uint4 unit[2];
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-      unit[h] = __ldcs(reinterpret_cast<const uint4*>(Wp + (rt * Kb + kb) * kTileBytes + (h * 32 + lane) * 16));
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int64_t n = rt * 16 + h * 8 + g;
-      const uint32_t word[4] = {unit[h].x, unit[h].y, unit[h].z, unit[h].w};
-#pragma unroll
-      for (int a = 0; a < 4; ++a) {
-        const int64_t k0 = kb * 128 + a * 32, k = k0 + t * 8;
-        uint32_t w[4];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) w[u] = __shfl_sync(0xffffffffu, word[a], (lane & ~3) | u) >> (4 * t);
-        if (n < N && k < K) {
-          const int64_t at = k0 / group * N + n;
-          const uint32_t e = __ldg(scale + at), zp = zero_pair(zero != nullptr ? __ldg(zero + at) : 8u);
-#pragma unroll
-          for (int u = 0; u < 4; ++u)
-            w[u] = mul_bf16x2(sub_bf16x2((w[u] & 0x000F000Fu) | 0x43004300u, zp), e | (e << 16));
-          *reinterpret_cast<uint4*>(out + n * K + k) = make_uint4(w[0], w[1], w[2], w[3]);
-        }
-      }
-    }
-  }
-}
-
-// ---------------------------------------------------------------- linear layer
-__device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
 __device__ __forceinline__ void ldmatrix(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -207,6 +51,198 @@ __device__ __forceinline__ void cp_async(uint32_t dst, const void* src, bool val
     asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(BYTES), "r"(valid ? BYTES : 0)
                  : "memory");
 }
+
+// ---------------------------------------------------------------- quantization
+// One warp per tile, over the row tiles of one 128-column block. The tile comes as it is into the
+// warp's ring of shared memory (asynchronous 16-byte copies, two tiles ahead); loading it as
+// 8x8 matrices then gives each lane the column pairs of rows g and g + 8 that its 16-byte units
+// hold the codes of, so nothing has to be exchanged: a word of codes is four pairs shifted
+// together. A group of 32 columns belongs to the four lanes of a quad, and lane t of it takes
+// the two divisions for the block a = t. Bound by instructions as much as by HBM (2.6 bytes an
+// element): products are packed pairs, a code's rounding is an addition of 1.5 * 2^23 (the
+// product is below 23 in magnitude, even where a subnormal scale is half a step off), and its
+// zero point and clamp one packed 16-bit operation per pair.
+constexpr int kQuantRing = 3, kQuantRow = 256 + 16, kQuantSlot = 16 * kQuantRow;
+
+template <int G, bool ASYM>
+__global__ void __launch_bounds__(kInt4Threads, 2)
+int4_quant_kernel(const uint16_t* __restrict__ W, int64_t N, int64_t K, int64_t ldw, const float* __restrict__ s,
+                  uint8_t* __restrict__ Wp, uint16_t* __restrict__ scale, uint8_t* __restrict__ zero) {
+  griddep_wait();
+  griddep_launch_dependents();
+  constexpr int kSpan = G / 32;  // 32-column blocks of a group
+  extern __shared__ __align__(16) uint8_t smem[];
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, quad = lane & ~3;
+  const int64_t Nt = (N + 15) / 16, Kb = (K + 127) / 128;
+  const int64_t kb = blockIdx.x;
+  const int cols = static_cast<int>(K - kb * 128 < 128 ? K - kb * 128 : 128);
+  uint64_t sv[16];  // smoothing factors of this lane's column pairs 8 c + 2 t
+#pragma unroll
+  for (int c = 0; c < 16; ++c) {
+    sv[c] = rows::f2_pack(1.0f, 1.0f);
+    if (s != nullptr && c * 8 < cols) sv[c] = __ldg(reinterpret_cast<const unsigned long long*>(s + kb * 128 + c * 8 + 2 * t));
+  }
+  const int64_t step = static_cast<int64_t>(gridDim.y) * (kInt4Threads / 32);
+  int64_t rt = static_cast<int64_t>(blockIdx.y) * (kInt4Threads / 32) + (threadIdx.x >> 5);
+  const uint32_t ring = smem_u32(smem) + (threadIdx.x >> 5) * kQuantRing * kQuantSlot;
+  int64_t next = rt;
+  auto fetch = [&](int slot) {  // lane: 16 bytes of rows lane / 16 + 2 i
+    if (next < Nt) {
+      const int64_t n0 = next * 16 + lane / 16;
+      const uint16_t* src = W + n0 * ldw + kb * 128 + lane % 16 * 8;
+      const uint32_t dst = ring + slot * kQuantSlot + lane / 16 * kQuantRow + lane % 16 * 16;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const bool in = n0 + 2 * i < N && lane % 16 * 8 < cols;
+        cp_async<16>(dst + 2 * i * kQuantRow, in ? src + 2 * i * ldw : W, in);
+      }
+      next += step;
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+#pragma unroll
+  for (int i = 0; i < kQuantRing - 1; ++i) fetch(i);
+  int slot = 0, free_slot = kQuantRing - 1;
+  for (; rt < Nt; rt += step) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kQuantRing - 2) : "memory");
+    __syncwarp();  // every lane's copies are there, and the slot before is read
+    fetch(free_slot);
+    const uint32_t src = ring + slot * kQuantSlot + (lane & 7) * kQuantRow + (lane >> 3) * 16;
+    free_slot = slot;
+    slot = slot + 1 == kQuantRing ? 0 : slot + 1;
+    const bool inside = rt * 16 + 16 <= N && cols == 128;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int64_t n = rt * 16 + h * 8 + g;
+      uint64_t v[16];      // w' of this lane's pairs
+      float hi[4], lo[4];  // per 32-column block: max |w'| (symmetric), or max and min with 0
+#pragma unroll
+      for (int a = 0; a < 4; ++a) {
+        uint32_t w[4];
+        ldmatrix(w, src + h * 8 * kQuantRow + a * 64);
+        hi[a] = lo[a] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          v[4 * a + i] = rows::f2_mul(rows::f2_pack(bf16_lo(w[i]), bf16_hi(w[i])), sv[4 * a + i]);
+          float x, y;
+          rows::f2_unpack(v[4 * a + i], x, y);
+          hi[a] = ASYM ? fmaxf(hi[a], fmaxf(x, y)) : fmaxf(hi[a], fmaxf(fabsf(x), fabsf(y)));
+          if (ASYM) lo[a] = fminf(lo[a], fminf(x, y));
+        }
+      }
+#pragma unroll
+      for (int a = 0; a < 4; a += kSpan) {
+#pragma unroll
+        for (int i = 1; i < kSpan; ++i) {
+          hi[a] = fmaxf(hi[a], hi[a + i]);
+          lo[a] = fminf(lo[a], lo[a + i]);
+        }
+#pragma unroll
+        for (int o = 1; o < 4; o <<= 1) {
+          hi[a] = fmaxf(hi[a], __shfl_xor_sync(0xffffffffu, hi[a], o));
+          if (ASYM) lo[a] = fminf(lo[a], __shfl_xor_sync(0xffffffffu, lo[a], o));
+        }
+#pragma unroll
+        for (int i = 1; i < kSpan; ++i) hi[a + i] = hi[a], lo[a + i] = lo[a];
+      }
+      // this lane's block: t
+      const float top = t & 2 ? (t & 1 ? hi[3] : hi[2]) : (t & 1 ? hi[1] : hi[0]);
+      const float low = t & 2 ? (t & 1 ? lo[3] : lo[2]) : (t & 1 ? lo[1] : lo[0]);
+      const __nv_bfloat16 e = __float2bfloat16_rn(ASYM ? __fdiv_rn(__fsub_rn(top, low), 15.0f) : __fdiv_rn(top, 7.0f));
+      const float ef = __bfloat162float(e);
+      const float my_r = ef > 0.0f ? fminf(__fdiv_rn(1.0f, ef), FLT_MAX) : 0.0f;
+      int my_z = 8;
+      if (ASYM) my_z = static_cast<int>(fminf(fmaxf(rintf(__fmul_rn(-low, my_r)), 0.0f), 15.0f));
+      if (t % kSpan == 0 && t * 32 < cols && n < N) {
+        const int64_t gr = kb * (128 / G) + t / kSpan;
+        if (SQ_GUARD(gr < (K + G - 1) / G)) {
+          scale[gr * N + n] = __bfloat16_as_ushort(e);
+          if (ASYM) zero[gr * N + n] = static_cast<uint8_t>(my_z);
+        }
+      }
+      uint32_t word[4];
+#pragma unroll
+      for (int a = 0; a < 4; ++a) {
+        const float r = __shfl_sync(0xffffffffu, my_r, quad | a);
+        const uint32_t zz = ASYM ? static_cast<uint32_t>(__shfl_sync(0xffffffffu, my_z, quad | a)) * 0x00010001u : 0x00080008u;
+        const uint64_t r2 = rows::f2_pack(r, r);
+        word[a] = 0;
+#pragma unroll
+        for (int i = 3; i >= 0; --i) {
+          float x, y;
+          rows::f2_unpack(rows::f2_mul(v[4 * a + i], r2), x, y);
+          const uint32_t q = __byte_perm(__float_as_uint(x + 12582912.0f), __float_as_uint(y + 12582912.0f), 0x5410);
+          uint32_t code = __viaddmin_s16x2_relu(q, zz, 0x000F000Fu);  // clamp(q + z, 0, 15)
+          if (!inside && (n >= N || a * 32 + i * 8 >= cols)) code = 0x00080008u;
+          word[a] = word[a] * 16 + code;
+        }
+      }
+      __stcs(reinterpret_cast<uint4*>(Wp + (rt * Kb + kb) * kTileBytes + (h * 32 + lane) * 16),
+             make_uint4(word[0], word[1], word[2], word[3]));
+    }
+  }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+}
+
+// ---------------------------------------------------------------- values
+// The reverse: each lane collects its 8 columns' nibbles from its quad and writes 16 bytes.
+// code - zero is exact in bf16 (128 + code minus 128 + zero), so the product with the scale
+// is rounded once.
+template <int G, bool ASYM>
+__global__ void __launch_bounds__(kInt4Threads, 4)
+int4_dequant_kernel(const uint8_t* __restrict__ Wp, const uint16_t* __restrict__ scale,
+                    const uint8_t* __restrict__ zero, int64_t N, int64_t K, uint16_t* __restrict__ out) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int64_t Nt = (N + 15) / 16, Kb = (K + 127) / 128;
+  const int64_t kb = blockIdx.x, step = static_cast<int64_t>(gridDim.y) * (kInt4Threads / 32);
+  for (int64_t rt = static_cast<int64_t>(blockIdx.y) * (kInt4Threads / 32) + (threadIdx.x >> 5); rt < Nt; rt += step) {
+    uint4 unit[2];
+    uint32_t e[2][128 / G], z[2][128 / G];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int64_t n = rt * 16 + h * 8 + g;
+      unit[h] = __ldcs(reinterpret_cast<const uint4*>(Wp + (rt * Kb + kb) * kTileBytes + (h * 32 + lane) * 16));
+#pragma unroll
+      for (int j = 0; j < 128 / G; ++j) {
+        e[h][j] = 0;
+        z[h][j] = 8;
+        if (n < N && kb * 128 + j * G < K) {
+          const int64_t at = (kb * (128 / G) + j) * N + n;
+          e[h][j] = __ldg(scale + at);
+          if (ASYM) z[h][j] = __ldg(zero + at);
+        }
+      }
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int64_t n = rt * 16 + h * 8 + g;
+      const uint32_t word[4] = {unit[h].x, unit[h].y, unit[h].z, unit[h].w};
+#pragma unroll
+      for (int a = 0; a < 4; ++a) {
+        const int64_t k = kb * 128 + a * 32 + t * 8;
+        const uint32_t e2 = e[h][a * 32 / G] * 0x00010001u, zp = ASYM ? zero_pair(z[h][a * 32 / G]) : 0x43084308u;
+        uint32_t w[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          w[u] = __shfl_sync(0xffffffffu, word[a], (lane & ~3) | u) >> (4 * t);
+          w[u] = mul_bf16x2(sub_bf16x2((w[u] & 0x000F000Fu) | 0x43004300u, zp), e2);
+        }
+        if (n < N && k < K) __stcs(reinterpret_cast<uint4*>(out + n * K + k), make_uint4(w[0], w[1], w[2], w[3]));
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------- linear layer
+__device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
 __device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
   float v;
   asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
@@ -844,12 +880,30 @@ cudaError_t launch_linear(const LinearParams& p, unsigned int* status, cudaStrea
   return launch_wide<8, G, ASYM>(p, sms, status, stream);
 }
 
-// Grid of the two tile kernels: one column block per x, row tiles over y so that about eight
+// Grid of the two tile kernels: one column block per x, row tiles over y so that about `per_sm`
 // CTAs per SM exist and each column block's factors are read by few of them.
-dim3 tile_grid(int64_t N, int64_t K) {
+dim3 tile_grid(int64_t N, int64_t K, int per_sm) {
   const int64_t Kb = (K + 127) / 128, rows = ((N + 15) / 16 + kInt4Threads / 32 - 1) / (kInt4Threads / 32);
-  const int64_t y = std::max<int64_t>(1, std::min<int64_t>(rows, (148 * 8 + Kb - 1) / Kb));
+  const int64_t y = std::max<int64_t>(1, std::min<int64_t>(rows, (148 * per_sm + Kb - 1) / Kb));
   return dim3(static_cast<unsigned>(Kb), static_cast<unsigned>(y));
+}
+
+template <int G>
+cudaError_t launch_quant_g(const uint16_t* W, int64_t N, int64_t K, int64_t ldw, const float* s, uint8_t* Wp,
+                           uint16_t* scale, uint8_t* zero, cudaStream_t stream) {
+  auto kernel = zero != nullptr ? int4_quant_kernel<G, true> : int4_quant_kernel<G, false>;
+  constexpr int smem = kInt4Threads / 32 * kQuantRing * kQuantSlot;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  return launch_kernel(kernel, tile_grid(N, K, 4), dim3(kInt4Threads), smem, stream, false, W, N, K, ldw, s, Wp, scale,
+                       zero);
+}
+
+template <int G>
+cudaError_t launch_dequant_g(const uint8_t* Wp, const uint16_t* scale, const uint8_t* zero, int64_t N, int64_t K,
+                             uint16_t* out, cudaStream_t stream) {
+  auto kernel = zero != nullptr ? int4_dequant_kernel<G, true> : int4_dequant_kernel<G, false>;
+  return launch_kernel(kernel, tile_grid(N, K, 8), dim3(kInt4Threads), 0, stream, false, Wp, scale, zero, N, K, out);
 }
 
 }  // namespace
@@ -860,15 +914,16 @@ size_t int4_weight_bytes(int64_t N, int64_t K) {
 
 cudaError_t launch_int4_quant(const uint16_t* W, int64_t N, int64_t K, int64_t ldw, const float* s, int group,
                               uint8_t* Wp, uint16_t* scale, uint8_t* zero, cudaStream_t stream) {
-  auto kernel = zero != nullptr ? int4_quant_kernel<true> : int4_quant_kernel<false>;
-  return launch_kernel(kernel, tile_grid(N, K), dim3(kInt4Threads), 0, stream, false, W, N, K, ldw, s, group, Wp, scale,
-                       zero);
+  if (group == 32) return launch_quant_g<32>(W, N, K, ldw, s, Wp, scale, zero, stream);
+  return group == 64 ? launch_quant_g<64>(W, N, K, ldw, s, Wp, scale, zero, stream)
+                     : launch_quant_g<128>(W, N, K, ldw, s, Wp, scale, zero, stream);
 }
 
 cudaError_t launch_int4_dequant(const uint8_t* Wp, const uint16_t* scale, const uint8_t* zero, int group, int64_t N,
                                 int64_t K, uint16_t* out, cudaStream_t stream) {
-  return launch_kernel(int4_dequant_kernel, tile_grid(N, K), dim3(kInt4Threads), 0, stream, false, Wp, scale, zero,
-                       group, N, K, out);
+  if (group == 32) return launch_dequant_g<32>(Wp, scale, zero, N, K, out, stream);
+  return group == 64 ? launch_dequant_g<64>(Wp, scale, zero, N, K, out, stream)
+                     : launch_dequant_g<128>(Wp, scale, zero, N, K, out, stream);
 }
 
 cudaError_t launch_int4_linear(const Int4LinearArgs& a, cudaStream_t stream) {
