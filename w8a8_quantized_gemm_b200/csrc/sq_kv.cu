@@ -18,7 +18,10 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 }
 
 // ---------------------------------------------------------------- append
-constexpr int kAppendThreads = 256;
+// 128 threads and at most 72 registers: seven CTAs an SM. Measured (us; 8192 tokens of 64 + 16 heads of
+// 128, int8; 2047 tokens of 32 + 64 heads, bf16): 256 threads 88 / 25, 128 threads 69 / 21, held to 72
+// registers 64 / 20.5 (5.1 and 4.9 TB/s), to 64 registers 62 / 21.5.
+constexpr int kAppendThreads = 128;
 
 // head_dim / 16 lanes own a head row (the group of `lanes`, a power of two, has idle ones for
 // head_dim 96): each holds 16 elements, which are 8 pairs when its part of the row is rotated,
@@ -26,7 +29,7 @@ constexpr int kAppendThreads = 256;
 // walks over the token's heads. A CTA takes one token, or several when a token has fewer rows
 // than the CTA has groups.
 template <bool INT8, bool PAIRS>
-__global__ void __launch_bounds__(kAppendThreads)
+__global__ void __launch_bounds__(kAppendThreads, 7)
 rope_kv_append_kernel(const uint16_t* q, int64_t ldq, const uint16_t* __restrict__ k, int64_t ldk,
                       const uint16_t* __restrict__ v, int64_t ldv, int64_t T, int H, const float* __restrict__ cos_t,
                       const float* __restrict__ sin_t, int64_t max_pos, int rot,
@@ -39,6 +42,24 @@ rope_kv_append_kernel(const uint16_t* q, int64_t ldq, const uint16_t* __restrict
   const int64_t tok = static_cast<int64_t>(blockIdx.x) * (groups / groups_per_token) + group / groups_per_token;
   if (tok >= T) return;
   const unsigned quad = lanes == 32 ? 0xffffffffu : ((1u << lanes) - 1u) << (threadIdx.x & 31 & ~(lanes - 1));
+  const bool on = 16 * i < D, turn = 16 * i < rot;
+  // places of the lane's two runs of 8 elements
+  const int p0 = turn && !PAIRS ? 8 * i : 16 * i, p1 = turn && !PAIRS ? rot / 2 + 8 * i : 16 * i + 8;
+  const int rows = H + 2 * c.heads;
+  // a row's elements, loaded one row ahead; the first do not wait for the slot and the angles
+  auto load = [&](int row, uint4 (&r)[2]) {
+    r[0] = r[1] = make_uint4(0, 0, 0, 0);
+    if (on && row < rows) {
+      const uint16_t* src = row < H ? q + tok * ldq + static_cast<int64_t>(row) * D
+                            : row < H + c.heads ? k + tok * ldk + static_cast<int64_t>(row - H) * D
+                                                : v + tok * ldv + static_cast<int64_t>(row - H - c.heads) * D;
+      r[0] = *reinterpret_cast<const uint4*>(src + p0);
+      r[1] = *reinterpret_cast<const uint4*>(src + p1);
+    }
+  };
+  int row = group % groups_per_token;
+  uint4 ahead[2];
+  load(row, ahead);
   const int slot = __ldg(slots + tok);
   if (slot < 0) return;
   const int64_t pos = rot > 0 ? __ldg(positions + tok) : 0;
@@ -47,9 +68,6 @@ rope_kv_append_kernel(const uint16_t* q, int64_t ldq, const uint16_t* __restrict
     if (i == 0 && group % groups_per_token == 0) atomicOr(status, kErrIndex);
     return;
   }
-  const bool on = 16 * i < D, turn = 16 * i < rot;
-  // places of the lane's two runs of 8 elements
-  const int p0 = turn && !PAIRS ? 8 * i : 16 * i, p1 = turn && !PAIRS ? rot / 2 + 8 * i : 16 * i + 8;
   float cs[8], sn[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) cs[j] = 1.0f, sn[j] = 0.0f;
@@ -60,19 +78,12 @@ rope_kv_append_kernel(const uint16_t* q, int64_t ldq, const uint16_t* __restrict
     cs[0] = c0.x; cs[1] = c0.y; cs[2] = c0.z; cs[3] = c0.w; cs[4] = c1.x; cs[5] = c1.y; cs[6] = c1.z; cs[7] = c1.w;
     sn[0] = s0.x; sn[1] = s0.y; sn[2] = s0.z; sn[3] = s0.w; sn[4] = s1.x; sn[5] = s1.y; sn[6] = s1.z; sn[7] = s1.w;
   }
-  const int rows = H + 2 * c.heads;
-  for (int row = group % groups_per_token; row < rows; row += groups_per_token) {
+  for (; row < rows; row += groups_per_token) {
     const bool is_q = row < H, is_v = row >= H + c.heads;
     const int head = is_q ? row : is_v ? row - H - c.heads : row - H;
-    const uint16_t* src = (is_q ? q + tok * ldq : is_v ? v + tok * ldv : k + tok * ldk) + static_cast<int64_t>(head) * D;
     float x[16];
-    if (on) {
-      const uint4 r[2] = {*reinterpret_cast<const uint4*>(src + p0), *reinterpret_cast<const uint4*>(src + p1)};
-      rows::widen16(r, x);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 16; ++j) x[j] = 0.0f;
-    }
+    sq::rows::widen16(ahead, x);
+    load(row + groups_per_token, ahead);
     if (turn && !is_v) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
@@ -107,9 +118,9 @@ rope_kv_append_kernel(const uint16_t* q, int64_t ldq, const uint16_t* __restrict
 #pragma unroll
         for (int j = 0; j < 16; ++j) e[j] = __float2int_rn(fminf(fmaxf(__fmul_rn(x[j], r), -128.0f), 127.0f));
         *reinterpret_cast<uint2*>(dst + p0) =
-            make_uint2(rows::pack4(e[0], e[1], e[2], e[3]), rows::pack4(e[4], e[5], e[6], e[7]));
+            make_uint2(sq::rows::pack4(e[0], e[1], e[2], e[3]), sq::rows::pack4(e[4], e[5], e[6], e[7]));
         *reinterpret_cast<uint2*>(dst + p1) =
-            make_uint2(rows::pack4(e[8], e[9], e[10], e[11]), rows::pack4(e[12], e[13], e[14], e[15]));
+            make_uint2(sq::rows::pack4(e[8], e[9], e[10], e[11]), sq::rows::pack4(e[12], e[13], e[14], e[15]));
       }
       if (i == 0) (is_v ? c.v_scale : c.k_scale)[page * c.scale_page_stride + at] = __fdiv_rn(a, 127.0f);
     }
