@@ -23,7 +23,7 @@ LIB = os.path.join(PKG, "libsq.so")
 LIB_DEBUG = os.path.join(PKG, "libsq_debug.so")
 
 SOURCES = ["sq_api.cu", "sq_reduce.cu", "sq_quant.cu", "sq_outlier.cu", "sq_gemm.cu", "sq_noalloc.cu",
-           "sq_variants.cu", "sq_gemv.cu", "sq_int4.cu", "sq_kv.cu", "sq_attention.cu"]
+           "sq_variants.cu", "sq_gemv.cu", "sq_int4.cu", "sq_int4_tc.cu", "sq_kv.cu", "sq_attention.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
               "--expt-relaxed-constexpr", "-I", INCLUDE, "-I", CSRC]

@@ -1186,6 +1186,12 @@ cudaError_t run(const GemmArgs& a, const Plan& pl, cudaStream_t stream, const ch
 
 }  // namespace
 
+bool make_bf16_operand_map(void* map, const void* base, uint64_t inner, uint64_t outer, uint64_t pitch_bytes,
+                           uint32_t box_rows) {
+  return make_operand_map(static_cast<CUtensorMap*>(map), base, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, inner, outer,
+                          pitch_bytes, box_rows);
+}
+
 size_t gemm_workspace_bytes(int64_t M, int64_t N, int64_t K, bool outliers) {
   if (gemv_applies(M, K, outliers)) return 0;
   const Plan pl = plan_gemm(M, N, K, outliers);

@@ -927,6 +927,7 @@ cudaError_t launch_int4_dequant(const uint8_t* Wp, const uint16_t* scale, const 
 }
 
 cudaError_t launch_int4_linear(const Int4LinearArgs& a, cudaStream_t stream) {
+  if (a.M > 4) return launch_int4_linear_tc(a, stream);
   LinearParams p{};
   p.X = a.X;
   p.ldx = a.ldx;

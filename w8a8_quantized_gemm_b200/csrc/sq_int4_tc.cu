@@ -1,0 +1,492 @@
+// The 4-bit linear layer for more than a few tokens, on the tensor cores (tcgen05).
+//   Y[m,n] = sum_k X[m,k] * (code[n,k] - zero[g,n]) * scale[g,n] + bias[n]
+//
+// The weight rows are the 128 rows of the instructions, the tokens (up to 64) their columns, so
+// that every code is made a bf16 number once for all tokens; the codes' bytes bound the call
+// until about 64 tokens. Two warpgroups take the 128-column blocks of a row block in turn. A thread
+// owns a weight row: its 64 bytes of codes (contiguous in the tiled layout) come by asynchronous
+// copies several blocks ahead, become code - zero exactly (128 + code, minus 128 + zero) in the
+// order of the columns, and go into tensor memory as operand A; the tokens are operand B, streamed
+// by TMA. Products and a group's sums are fp32 in tensor memory, one accumulator per group; the
+// warpgroup reads it back, scales it and adds it to its fp32 totals in registers while the
+// other's block is multiplied. At a row block's end the two add up, in order, and so do, through
+// distributed shared memory, the CTAs of a cluster that share the columns where there are too
+// few row blocks to go round.
+#include "sq_internal.h"
+#include "sq_ptx.cuh"
+
+#include <cuda_bf16.h>
+
+#include <algorithm>
+
+namespace sq {
+namespace {
+
+constexpr int kTileBytes = 1024;
+constexpr int kWorkers = 256;                 // two warpgroups
+constexpr int kThreads = kWorkers + 64;       // a warp for TMA, one for the matrix instructions
+constexpr int kCodeRow = 80;                  // 64 bytes of codes: an odd number of 16-byte units
+constexpr int kCodeSlot = 32 * kCodeRow;      // of a warp and block
+constexpr int64_t kSmemMax = 232448;
+
+struct TcParams {
+  int64_t N;
+  const uint8_t* Wp;
+  const uint16_t* scale;
+  const uint8_t* zero;
+  const uint16_t* bias;
+  uint16_t* Y;
+  int M, K, Kb, groups;
+  int split;      // CTAs of a cluster
+  int row_blocks;
+  unsigned int* status;
+};
+
+template <int TOKENS_, int G_>
+struct Cfg {
+  static constexpr int kTokens = TOKENS_, G = G_;
+  // columns of a unit of work: a block, or half of one where its groups' accumulators need the room
+  static constexpr int kUnit = G == 32 ? 64 : 128;
+  static constexpr int kHalves = 128 / kUnit, kGroups = kUnit / G;
+  static constexpr int kAtom = kTokens * 128;  // 64 columns of the tokens, 128-byte swizzle
+  static constexpr int kXSlot = kAtom * (kUnit / 64), kXStages = 4;
+  static constexpr int kCodeStages = 5;
+  static constexpr int kPart = kTokens * 128 * 4;
+  static constexpr int kX = 0, kCodes = kXStages * kXSlot, kSums = kCodes + 8 * kCodeStages * kCodeSlot;
+  static constexpr int kSmem = kSums + kPart + 1024;  // and the alignment
+  static_assert(kSmem <= kSmemMax - 1024, "shared memory of an SM");
+  // tensor memory: accumulators of the two warpgroups, then two operands each
+  static constexpr int kD = 0, kDStride = 128, kA = 256, kAStride = 128, kABuffer = 64;
+  static_assert(kGroups * kTokens <= kDStride, "accumulators of a unit");
+};
+
+template <int BYTES>
+__device__ __forceinline__ void cp_async(uint32_t dst, const void* src, bool valid) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(BYTES), "r"(valid ? BYTES : 0)
+               : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                       uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ uint32_t sub_bf16x2(uint32_t a, uint32_t b) {
+  const __nv_bfloat162 r =
+      __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+__device__ __forceinline__ void workers_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+
+// Cluster-scope arrival on, and wait for, an mbarrier that orders reads of distributed shared memory.
+__device__ __forceinline__ void arrive_cluster(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+__device__ __forceinline__ bool wait_cluster_bounded(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
+  const uint64_t t0 = global_timer_ns();
+  while (true) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred P;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 P, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, P;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    if (ok) return true;
+    if (global_timer_ns() - t0 > limit_ns) return false;
+  }
+}
+__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+struct Shared {
+  uint64_t x_full[4], x_empty[4], a_full[2][2], d_full[2], d_free[2], done, part_ready, part_free;
+  uint32_t tmem;
+  volatile uint32_t abort;
+};
+
+template <int TOKENS, int G, bool ASYM>
+__global__ void __launch_bounds__(kThreads, 1)
+int4_tc_kernel(const __grid_constant__ CUtensorMap x_map, const TcParams p) {
+  using C = Cfg<TOKENS, G>;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ Shared sh;
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = blockIdx.x % p.split, cluster = blockIdx.x / p.split, clusters = gridDim.x / p.split;
+  const int b0 = static_cast<int>(static_cast<int64_t>(p.Kb) * rank / p.split);
+  const int nb = static_cast<int>(static_cast<int64_t>(p.Kb) * (rank + 1) / p.split) - b0;  // blocks of this CTA
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C::kXStages; ++i) {
+      mbar_init(&sh.x_full[i], 1);
+      mbar_init(&sh.x_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh.a_full[i][0], 128);
+      mbar_init(&sh.a_full[i][1], 128);
+      mbar_init(&sh.d_full[i], 1);
+      mbar_init(&sh.d_free[i], 128);
+    }
+    mbar_init(&sh.done, 1);
+    mbar_init(&sh.part_ready, p.split);
+    mbar_init(&sh.part_free, p.split);
+    sh.abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 9) {
+    tmem_alloc(&sh.tmem, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  if (p.split > 1)
+    cluster_sync();  // the peers' barriers are ready
+  else
+    __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem;
+  griddep_wait();
+  griddep_launch_dependents();
+
+  // A wait that gives up is recorded and makes every later one return at once, so that each role
+  // runs through its loops without waiting.
+  auto wait = [&](uint64_t* bar, uint32_t parity, unsigned code) -> bool {
+    if (sh.abort) return false;
+    if (mbar_wait_bounded(bar, parity, kDefaultWaitLimitNs)) return true;
+    sh.abort = 1;
+    atomicOr(p.status, code);
+    return false;
+  };
+  // units of a row block in order: pairs of blocks; their halves; first and second warpgroup's block
+  if (warp == 8) {
+    if (lane == 0) {
+      tma_prefetch_desc(&x_map);
+      int n = 0, issued = 0;
+      for (int rb = cluster; rb < p.row_blocks; rb += clusters)
+        for (int pair = 0; pair < nb; pair += 2)
+          for (int h = 0; h < C::kHalves; ++h)
+            for (int wg = 0; wg < 2 && pair + wg < nb; ++wg, ++n) {
+              const int s = n % C::kXStages;
+              if (n >= C::kXStages) wait(&sh.x_empty[s], ((n / C::kXStages) - 1) & 1, kErrProducerWait);
+              if (sh.abort) continue;
+              mbar_arrive_expect_tx(&sh.x_full[s], C::kXSlot);
+              const int k0 = (b0 + pair + wg) * 128 + h * C::kUnit;
+#pragma unroll
+              for (int a = 0; a < C::kUnit / 64; ++a)
+                tma_load_2d(smem + C::kX + s * C::kXSlot + a * C::kAtom, &x_map, &sh.x_full[s], k0 + a * 64, 0, kEvictLast);
+              issued = n + 1;
+            }
+      // copies still in flight after a wait gave up end before the CTA does
+      if (sh.abort)
+        for (int i = std::max(0, issued - C::kXStages); i < issued; ++i)
+          mbar_wait_bounded(&sh.x_full[i % C::kXStages], (i / C::kXStages) & 1, kDefaultWaitLimitNs);
+    }
+  } else if (warp == 9) {
+    if (lane == 0) {
+      constexpr uint32_t kIdesc = idesc_bf16_f32(128, C::kTokens);
+      int n = 0, done[2] = {0, 0};
+      for (int rb = cluster; rb < p.row_blocks; rb += clusters)
+        for (int pair = 0; pair < nb; pair += 2)
+          for (int h = 0; h < C::kHalves; ++h)
+            for (int wg = 0; wg < 2 && pair + wg < nb; ++wg, ++n) {
+              const int s = n % C::kXStages, u = wg == 0 ? done[0]++ : done[1]++;
+              wait(&sh.x_full[s], (n / C::kXStages) & 1, kErrMmaWait);
+              wait(&sh.a_full[wg][u & 1], (u >> 1) & 1, kErrMmaWait);
+              if (u > 0) wait(&sh.d_free[wg], (u - 1) & 1, kErrMmaWait);
+              if (sh.abort) continue;
+              tc_fence_after();
+              const uint32_t a0 = tmem + C::kA + wg * C::kAStride + (u & 1) * C::kABuffer;
+              const uint32_t d0 = tmem + C::kD + wg * C::kDStride;
+              const uint32_t x0 = smem_u32(smem + C::kX + s * C::kXSlot);
+#pragma unroll
+              for (int j = 0; j < C::kUnit / 16; ++j) {
+                const uint64_t b = smem_desc_k128(x0 + (j / 4) * C::kAtom + (j % 4) * 32);
+                mma_ts(d0 + j / (G / 16) * C::kTokens, a0 + j * 8, b, kIdesc, j % (G / 16) != 0);
+              }
+              mma_commit(&sh.d_full[wg]);
+              mma_commit(&sh.x_empty[s]);
+            }
+      mma_commit(&sh.done);
+      if (!mbar_wait_bounded(&sh.done, 0, kDefaultWaitLimitNs)) atomicOr(p.status, kErrTeardownWait);
+    }
+  } else {
+    const int wg = warp >> 2, quarter = warp & 3, row = quarter * 32 + lane;
+    const uint32_t tmem_lane = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+    const uint32_t ring = smem_u32(smem + C::kCodes) + warp * C::kCodeStages * kCodeSlot;
+    const uint8_t* ring_p = smem + C::kCodes + warp * C::kCodeStages * kCodeSlot;
+    const int64_t Nt = (p.N + 15) / 16;
+    // ---- this warp's blocks: wg, wg + 2, ... of each row block, codes several ahead
+    int load_rb = wg < nb ? cluster : p.row_blocks, load_b = wg;
+    auto fetch = [&](int slot) {
+      if (load_rb < p.row_blocks) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {  // 16 bytes (i % 2) * 32 + lane of tile i / 2
+          const int64_t rt = static_cast<int64_t>(load_rb) * 8 + quarter * 2 + i / 2;
+          const bool in = rt < Nt;
+          const uint8_t* src = p.Wp + (in ? (rt * p.Kb + b0 + load_b) * kTileBytes + (i % 2) * 512 + lane * 16 : 0);
+          cp_async<16>(ring + slot * kCodeSlot + ((i / 2) * 16 + (i % 2) * 8 + lane / 4) * kCodeRow + lane % 4 * 16, src, in);
+        }
+        load_b += 2;
+        if (load_b >= nb) load_b = wg, load_rb += clusters;
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+#pragma unroll
+    for (int i = 0; i < C::kCodeStages - 1; ++i) fetch(i);
+
+    constexpr int kPer = 128 / G;  // groups of a block
+    uint32_t e_next[kPer], z_next[kPer];
+    auto factors = [&](int rb, int b) {  // this row's, of the block's groups
+      const int64_t n = static_cast<int64_t>(rb) * 128 + row;
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) {
+        const int gr = (b0 + b) * kPer + j;
+        e_next[j] = 0;
+        z_next[j] = 8;
+        if (rb < p.row_blocks && b < nb && n < p.N && gr < p.groups) {
+          e_next[j] = __ldg(p.scale + gr * p.N + n);
+          if (ASYM) z_next[j] = __ldg(p.zero + gr * p.N + n);
+        }
+      }
+    };
+    int slot = 0, free_slot = C::kCodeStages - 1, u = 0;
+    uint4 code[4];
+    float e[kPer], e_old[kPer];
+    uint32_t z[kPer];
+    factors(cluster, wg);
+    // block b of row block rb: codes into registers, its factors, the next block's on their way
+    auto take = [&](int rb, int b) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(C::kCodeStages - 2) : "memory");
+      __syncwarp();
+      fetch(free_slot);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) code[c] = *reinterpret_cast<const uint4*>(ring_p + slot * kCodeSlot + lane * kCodeRow + c * 16);
+      free_slot = slot;
+      slot = slot + 1 == C::kCodeStages ? 0 : slot + 1;
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) {
+        e[j] = bf16_lo(e_next[j]);
+        z[j] = 0x43004300u | z_next[j] | (z_next[j] << 16);
+      }
+      if (b + 2 < nb)
+        factors(rb, b + 2);
+      else
+        factors(rb + clusters, wg);
+    };
+    // half h of the block as operand A of unit `at`
+    auto convert = [&](int h, int at) {
+      const uint32_t dst = tmem_lane + C::kA + wg * C::kAStride + (at & 1) * C::kABuffer;
+#pragma unroll
+      for (int q = 0; q < C::kUnit / 64; ++q) {
+        uint32_t r[32];
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+          const int a = 2 * q + w;  // of the unit: the block's word a + 2 h
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const uint32_t lo = a == 0 ? code[c].x : a == 1 ? code[c].y : a == 2 ? code[c].z : code[c].w;
+            const uint32_t hi = a == 0 ? code[c].z : code[c].w;
+            const uint32_t v = C::kHalves == 2 && h == 1 ? hi : lo;
+            const uint32_t zz = C::kHalves == 2 && h == 1 ? z[(a + 2) * 32 / G % kPer] : z[a * 32 / G];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              r[16 * w + 4 * i + c] = sub_bf16x2(((v >> (4 * i)) & 0x000F000Fu) | 0x43004300u, zz);
+          }
+        }
+        tmem_st_32x32b_x32(dst + q * 32, r);
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive(&sh.a_full[wg][at & 1]);  // (one barrier per operand: a thread may be a unit ahead of another)
+    };
+
+    float acc[C::kTokens];
+#pragma unroll
+    for (int m = 0; m < C::kTokens; ++m) acc[m] = 0.0f;
+    float* part = reinterpret_cast<float*>(smem + C::kSums);  // [tokens][128 rows]
+    int item = 0;
+    // the conversion runs one unit ahead of the accumulation: unit u's product is formed meanwhile
+    int next_rb = wg < nb ? cluster : p.row_blocks, next_b = wg, next_h = 0, ahead = 0;
+    auto step_next = [&]() {
+      if (next_rb >= p.row_blocks) return;
+      if (next_h == 0) {
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) e_old[j] = e[j];
+        take(next_rb, next_b);
+      }
+      convert(next_h, ahead++);
+      if (++next_h == C::kHalves) {
+        next_h = 0;
+        next_b += 2;
+        if (next_b >= nb) next_b = wg, next_rb += clusters;
+      }
+    };
+    step_next();
+    for (int rb = cluster; rb < p.row_blocks; rb += clusters, ++item) {
+      for (int b = wg; b < nb; b += 2)
+        for (int h = 0; h < C::kHalves; ++h, ++u) {
+          // the factors of unit u: those before the block taken ahead, if the step ahead took one
+          const bool took = next_h == 0 && next_rb < p.row_blocks;
+          step_next();
+          const bool ok = wait(&sh.d_full[wg], u & 1, kErrEpilogueWait);
+          if (!__all_sync(0xffffffffu, ok)) continue;
+          tc_fence_after();
+#pragma unroll
+          for (int j = 0; j < C::kGroups; ++j) {
+            const int of = j + (C::kHalves == 2 ? h * C::kGroups : 0);
+            float f = 0.0f;
+#pragma unroll
+            for (int i = 0; i < kPer; ++i)
+              if (i == of) f = took ? e_old[i] : e[i];
+#pragma unroll
+            for (int m = 0; m < C::kTokens; m += 16) {
+              uint32_t d[16];
+              tmem_ld_32x32b_x16(tmem_lane + C::kD + wg * C::kDStride + j * C::kTokens + m, d);
+              tmem_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 16; ++i) acc[m + i] = fmaf(__uint_as_float(d[i]), f, acc[m + i]);
+            }
+          }
+          tc_fence_before();
+          mbar_arrive(&sh.d_free[wg]);
+        }
+      // ---- the row block's sums: second warpgroup, plus first, plus the other CTAs'
+      if (p.split > 1 && item > 0 && !sh.abort &&
+          !wait_cluster_bounded(&sh.part_free, (item - 1) & 1, kDefaultWaitLimitNs)) {
+        sh.abort = 1;
+        atomicOr(p.status, kErrEpilogueWait);
+      }
+      workers_sync();
+      if (wg == 1)
+#pragma unroll
+        for (int m = 0; m < C::kTokens; ++m) part[m * 128 + row] = acc[m];
+      workers_sync();
+      if (wg == 0)
+#pragma unroll
+        for (int m = 0; m < C::kTokens; ++m) part[m * 128 + row] += acc[m];
+#pragma unroll
+      for (int m = 0; m < C::kTokens; ++m) acc[m] = 0.0f;
+      workers_sync();
+      if (p.split > 1) {
+        if (threadIdx.x < p.split) arrive_cluster(mapa_shared(&sh.part_ready, threadIdx.x));
+        if (!sh.abort && !wait_cluster_bounded(&sh.part_ready, item & 1, kDefaultWaitLimitNs)) {
+          sh.abort = 1;
+          atomicOr(p.status, kErrEpilogueWait);
+        }
+      }
+      const int pairs = 64 / p.split;  // row pairs that this CTA finishes
+      for (int i = threadIdx.x; i < p.M * pairs; i += kWorkers) {
+        const int m = i / pairs, r = (rank * pairs + i % pairs) * 2;
+        const int64_t n = static_cast<int64_t>(rb) * 128 + r;
+        if (n >= p.N) continue;
+        float y0 = 0.0f, y1 = 0.0f;
+        if (p.split == 1) {
+          y0 = part[m * 128 + r];
+          y1 = part[m * 128 + r + 1];
+        } else {
+          for (int c = 0; c < p.split; ++c) {
+            const uint32_t at = mapa_shared(part + m * 128 + r, c);
+            y0 += ld_cluster_f32(at);
+            y1 += ld_cluster_f32(at + 4);
+          }
+        }
+        if (p.bias != nullptr) {
+          const uint32_t b = __ldg(reinterpret_cast<const uint32_t*>(p.bias + n));
+          y0 += bf16_lo(b);
+          y1 += bf16_hi(b);
+        }
+        *reinterpret_cast<__nv_bfloat162*>(p.Y + m * p.N + n) = __floats2bfloat162_rn(y0, y1);
+      }
+      if (p.split > 1) {
+        workers_sync();
+        if (threadIdx.x < p.split) arrive_cluster(mapa_shared(&sh.part_free, threadIdx.x));
+      }
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+  }
+  __syncwarp();
+  tc_fence_before();
+  if (p.split > 1)
+    cluster_sync();  // no CTA leaves while its sums are being read
+  else
+    __syncthreads();
+  tc_fence_after();
+  if (warp == 9) tmem_dealloc(tmem, 512);
+}
+
+template <int TOKENS, int G, bool ASYM>
+cudaError_t launch_tc(const Int4LinearArgs& a, cudaStream_t stream) {
+  using C = Cfg<TOKENS, G>;
+  TcParams p{};
+  p.N = a.N;
+  p.Wp = a.Wp;
+  p.scale = a.scale;
+  p.zero = a.zero;
+  p.bias = a.bias;
+  p.Y = a.Y;
+  p.M = static_cast<int>(a.M);
+  p.K = static_cast<int>(a.K);
+  p.Kb = (p.K + 127) / 128;
+  p.groups = (p.K + G - 1) / G;
+  p.status = a.status;
+  p.row_blocks = static_cast<int>((a.N + 127) / 128);
+  int dev = 0, sms = 148;
+  cudaGetDevice(&dev);
+  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  // Rounds of row blocks over the clusters, in blocks of columns per CTA, and what a round costs
+  // besides: its end, and the exchange of a cluster.
+  double least = 1e30;
+  p.split = 1;
+  for (int split = 1; split <= 8 && split <= p.Kb; split *= 2) {
+    const int clusters = sms / split, rounds = (p.row_blocks + clusters - 1) / clusters;
+    const double cost = rounds * ((p.Kb + split - 1) / split + (split > 1 ? 6.0 : 3.0));
+    if (cost < least) least = cost, p.split = split;
+  }
+  CUtensorMap map{};
+  if (!make_bf16_operand_map(&map, a.X, static_cast<uint64_t>(a.K), static_cast<uint64_t>(a.M),
+                     static_cast<uint64_t>(a.ldx) * 2, TOKENS))
+    return cudaErrorInvalidValue;
+  auto kernel = int4_tc_kernel<TOKENS, G, ASYM>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  if (e != cudaSuccess) return e;
+  const int clusters = std::min(sms / p.split, p.row_blocks);
+  return launch_kernel_clustered(kernel, dim3(static_cast<unsigned>(clusters * p.split)), dim3(kThreads), C::kSmem, stream,
+                                 true, static_cast<unsigned>(p.split), map, p);
+}
+
+template <int TOKENS>
+cudaError_t launch_tokens(const Int4LinearArgs& a, cudaStream_t stream) {
+  if (a.zero != nullptr) {
+    if (a.group == 32) return launch_tc<TOKENS, 32, true>(a, stream);
+    return a.group == 64 ? launch_tc<TOKENS, 64, true>(a, stream) : launch_tc<TOKENS, 128, true>(a, stream);
+  }
+  if (a.group == 32) return launch_tc<TOKENS, 32, false>(a, stream);
+  return a.group == 64 ? launch_tc<TOKENS, 64, false>(a, stream) : launch_tc<TOKENS, 128, false>(a, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_int4_linear_tc(const Int4LinearArgs& a, cudaStream_t stream) {
+  if (a.M <= 16) return launch_tokens<16>(a, stream);
+  if (a.M <= 32) return launch_tokens<32>(a, stream);
+  return launch_tokens<64>(a, stream);
+}
+
+}  // namespace sq

@@ -206,6 +206,11 @@ struct Int4LinearArgs {
   unsigned int* status = nullptr;
 };
 cudaError_t launch_int4_linear(const Int4LinearArgs& a, cudaStream_t stream);
+cudaError_t launch_int4_linear_tc(const Int4LinearArgs& a, cudaStream_t stream);  // sq_int4_tc.cu
+// Tensor map (a CUtensorMap) of a K-major bf16 operand: 64 columns x box_rows rows, 128-byte
+// swizzle, zero fill out of range (sq_gemm.cu).
+bool make_bf16_operand_map(void* map, const void* base, uint64_t inner, uint64_t outer, uint64_t pitch_bytes,
+                           uint32_t box_rows);
 
 // ---- paged key-value cache (append in sq_kv.cu, attention in sq_attention.cu)
 struct KvView {  // a checked sq_kv_cache, as the kernels take it
