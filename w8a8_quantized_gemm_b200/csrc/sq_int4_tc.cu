@@ -24,9 +24,9 @@ namespace {
 
 constexpr int kTileBytes = 1024;
 constexpr int kWorkers = 256;                 // two warpgroups
-constexpr int kThreads = kWorkers + 64;       // a warp for TMA, one for the matrix instructions
+constexpr int kThreads = kWorkers + 96;       // a warp for TMA, one per warpgroup for the matrix instructions
 constexpr int kCodeRow = 80;                  // 64 bytes of codes: an odd number of 16-byte units
-constexpr int kCodeSlot = 32 * kCodeRow;      // of a warp and block
+constexpr int kCodeBytes = 32 * kCodeRow;     // of a warp's rows in a block
 constexpr int64_t kSmemMax = 232448;
 
 struct TcParams {
@@ -50,7 +50,9 @@ struct Cfg {
   static constexpr int kHalves = 128 / kUnit, kGroups = kUnit / G;
   static constexpr int kAtom = kTokens * 128;  // 64 columns of the tokens, 128-byte swizzle
   static constexpr int kXSlot = kAtom * (kUnit / 64), kXStages = 4;
-  static constexpr int kCodeStages = 5;
+  // a warp's slot: codes, then the rows' scales and zero points per group
+  static constexpr int kPer = 128 / G, kScales = kCodeBytes, kZeros = kScales + kPer * 64;
+  static constexpr int kCodeSlot = kZeros + kPer * 32, kCodeStages = 5;
   static constexpr int kPart = kTokens * 128 * 4;
   static constexpr int kX = 0, kCodes = kXStages * kXSlot, kSums = kCodes + 8 * kCodeStages * kCodeSlot;
   static constexpr int kSmem = kSums + kPart + 1024;  // and the alignment
@@ -62,8 +64,11 @@ struct Cfg {
 
 template <int BYTES>
 __device__ __forceinline__ void cp_async(uint32_t dst, const void* src, bool valid) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(BYTES), "r"(valid ? BYTES : 0)
-               : "memory");
+  if constexpr (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(BYTES), "r"(valid ? BYTES : 0)
+                 : "memory");
 }
 __device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
                                        uint32_t accumulate) {
@@ -82,6 +87,15 @@ __device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)
         "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(taddr)
       : "memory");
+}
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(one));
+  return one != 0;
 }
 __device__ __forceinline__ uint32_t sub_bf16x2(uint32_t a, uint32_t b) {
   const __nv_bfloat162 r =
@@ -118,7 +132,7 @@ __device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
 }
 
 struct Shared {
-  uint64_t x_full[4], x_empty[4], a_full[2][2], d_full[2], d_free[2], done, part_ready, part_free;
+  uint64_t x_full[4], x_empty[4], a_full[2][2], d_full[2], d_free[2], done[2], part_ready, part_free;
   uint32_t tmem;
   volatile uint32_t abort;
 };
@@ -144,8 +158,8 @@ int4_tc_kernel(const __grid_constant__ CUtensorMap x_map, const TcParams p) {
       mbar_init(&sh.a_full[i][1], 128);
       mbar_init(&sh.d_full[i], 1);
       mbar_init(&sh.d_free[i], 128);
+      mbar_init(&sh.done[i], 1);
     }
-    mbar_init(&sh.done, 1);
     mbar_init(&sh.part_ready, p.split);
     mbar_init(&sh.part_free, p.split);
     sh.abort = 0;
@@ -168,6 +182,7 @@ int4_tc_kernel(const __grid_constant__ CUtensorMap x_map, const TcParams p) {
   // A wait that gives up is recorded and makes every later one return at once, so that each role
   // runs through its loops without waiting.
   auto wait = [&](uint64_t* bar, uint32_t parity, unsigned code) -> bool {
+    if (mbar_try_wait(bar, parity)) return true;
     if (sh.abort) return false;
     if (mbar_wait_bounded(bar, parity, kDefaultWaitLimitNs)) return true;
     sh.abort = 1;
@@ -198,97 +213,123 @@ int4_tc_kernel(const __grid_constant__ CUtensorMap x_map, const TcParams p) {
         for (int i = std::max(0, issued - C::kXStages); i < issued; ++i)
           mbar_wait_bounded(&sh.x_full[i % C::kXStages], (i / C::kXStages) & 1, kDefaultWaitLimitNs);
     }
-  } else if (warp == 9) {
-    if (lane == 0) {
-      constexpr uint32_t kIdesc = idesc_bf16_f32(128, C::kTokens);
-      int n = 0, done[2] = {0, 0};
-      for (int rb = cluster; rb < p.row_blocks; rb += clusters)
-        for (int pair = 0; pair < nb; pair += 2)
-          for (int h = 0; h < C::kHalves; ++h)
-            for (int wg = 0; wg < 2 && pair + wg < nb; ++wg, ++n) {
-              const int s = n % C::kXStages, u = wg == 0 ? done[0]++ : done[1]++;
-              wait(&sh.x_full[s], (n / C::kXStages) & 1, kErrMmaWait);
-              wait(&sh.a_full[wg][u & 1], (u >> 1) & 1, kErrMmaWait);
-              if (u > 0) wait(&sh.d_free[wg], (u - 1) & 1, kErrMmaWait);
-              if (sh.abort) continue;
-              tc_fence_after();
-              const uint32_t a0 = tmem + C::kA + wg * C::kAStride + (u & 1) * C::kABuffer;
-              const uint32_t d0 = tmem + C::kD + wg * C::kDStride;
-              const uint32_t x0 = smem_u32(smem + C::kX + s * C::kXSlot);
+  } else if (warp > 8) {
+    // The whole warp runs the loop (its operands then live in uniform registers, as the instructions
+    // want them) and one lane issues. One warp per warpgroup: a unit costs some hundred cycles here.
+    const int wg = warp - 9;
+    constexpr uint32_t kIdesc = idesc_bf16_f32(128, C::kTokens);
+    const uint64_t x_desc = smem_desc_k128(smem_u32(smem + C::kX));
+    const bool one = elect_one();
+    int n = 0, u = 0;
+    for (int rb = cluster; rb < p.row_blocks; rb += clusters)
+      for (int pair = 0; pair < nb; pair += 2) {
+        const int both = pair + 1 < nb ? 2 : 1;
+        for (int h = 0; h < C::kHalves; ++h, n += both) {
+          if (wg >= both) continue;
+          const int s = (n + wg) % C::kXStages;
+          wait(&sh.x_full[s], ((n + wg) / C::kXStages) & 1, kErrMmaWait);
+          wait(&sh.a_full[wg][u & 1], (u >> 1) & 1, kErrMmaWait);
+          if (u > 0) wait(&sh.d_free[wg], (u - 1) & 1, kErrMmaWait);
+          tc_fence_after();
+          const uint32_t a0 = tmem + C::kA + wg * C::kAStride + (u & 1) * C::kABuffer;
+          const uint32_t d0 = tmem + C::kD + wg * C::kDStride;
+          const uint64_t b0 = x_desc + ((s * C::kXSlot) >> 4);  // addresses count in 16 bytes
+          if (one && !sh.abort) {
 #pragma unroll
-              for (int j = 0; j < C::kUnit / 16; ++j) {
-                const uint64_t b = smem_desc_k128(x0 + (j / 4) * C::kAtom + (j % 4) * 32);
-                mma_ts(d0 + j / (G / 16) * C::kTokens, a0 + j * 8, b, kIdesc, j % (G / 16) != 0);
-              }
-              mma_commit(&sh.d_full[wg]);
-              mma_commit(&sh.x_empty[s]);
-            }
-      mma_commit(&sh.done);
-      if (!mbar_wait_bounded(&sh.done, 0, kDefaultWaitLimitNs)) atomicOr(p.status, kErrTeardownWait);
+            for (int j = 0; j < C::kUnit / 16; ++j)
+              mma_ts(d0 + j / (G / 16) * C::kTokens, a0 + j * 8, b0 + (((j / 4) * C::kAtom + (j % 4) * 32) >> 4), kIdesc,
+                     j % (G / 16) != 0);
+            mma_commit(&sh.d_full[wg]);
+            mma_commit(&sh.x_empty[s]);
+          }
+          __syncwarp();
+          ++u;
+        }
+      }
+    if (one) {
+      mma_commit(&sh.done[wg]);
+      if (!mbar_wait_bounded(&sh.done[wg], 0, kDefaultWaitLimitNs)) atomicOr(p.status, kErrTeardownWait);
     }
   } else {
     const int wg = warp >> 2, quarter = warp & 3, row = quarter * 32 + lane;
     const uint32_t tmem_lane = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
-    const uint32_t ring = smem_u32(smem + C::kCodes) + warp * C::kCodeStages * kCodeSlot;
-    const uint8_t* ring_p = smem + C::kCodes + warp * C::kCodeStages * kCodeSlot;
+    const uint32_t ring = smem_u32(smem + C::kCodes) + warp * C::kCodeStages * C::kCodeSlot;
+    const uint8_t* ring_p = smem + C::kCodes + warp * C::kCodeStages * C::kCodeSlot;
     const int64_t Nt = (p.N + 15) / 16;
-    // ---- this warp's blocks: wg, wg + 2, ... of each row block, codes several ahead
+    constexpr int kPer = C::kPer;  // groups of a block
+    // ---- this warp's blocks: wg, wg + 2, ... of each row block, codes and factors several ahead
     int load_rb = wg < nb ? cluster : p.row_blocks, load_b = wg;
+    const int64_t tile_bytes = static_cast<int64_t>(p.Kb) * kTileBytes;
+    const uint8_t* src = nullptr;  // 16 bytes `lane` of this warp's first tile in the next block
+    const uint16_t* e_src = nullptr;
+    const uint8_t* z_src = nullptr;
+    bool in0 = false, in1 = false;
+    // lane's part of a block's scales: 32 rows per group, kE bytes a lane; and of its zero points, 4 bytes
+    constexpr int kE = G == 32 ? 8 : 4, kELanes = 64 / kE;
+    const int e_group = lane / kELanes, e_row = lane % kELanes * (kE / 2), z_group = lane / 8, z_row = lane % 8 * 4;
+    bool e_in = false, z_in = false;
+    auto locate = [&]() {  // the next row block
+      const int64_t rt = static_cast<int64_t>(load_rb) * 8 + quarter * 2, n = static_cast<int64_t>(load_rb) * 128 + quarter * 32;
+      in0 = rt < Nt;
+      in1 = rt + 1 < Nt;
+      src = p.Wp + rt * tile_bytes + static_cast<int64_t>(b0 + wg) * kTileBytes + lane * 16;
+      e_in = lane < kPer * kELanes && n + e_row < p.N;
+      z_in = lane < kPer * 8 && n + z_row < p.N;
+      e_src = p.scale + ((b0 + wg) * kPer + e_group) * p.N + n + e_row;
+      z_src = p.zero + ((b0 + wg) * kPer + z_group) * p.N + n + z_row;
+    };
+    if (load_rb < p.row_blocks) locate();
     auto fetch = [&](int slot) {
       if (load_rb < p.row_blocks) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {  // 16 bytes (i % 2) * 32 + lane of tile i / 2
-          const int64_t rt = static_cast<int64_t>(load_rb) * 8 + quarter * 2 + i / 2;
-          const bool in = rt < Nt;
-          const uint8_t* src = p.Wp + (in ? (rt * p.Kb + b0 + load_b) * kTileBytes + (i % 2) * 512 + lane * 16 : 0);
-          cp_async<16>(ring + slot * kCodeSlot + ((i / 2) * 16 + (i % 2) * 8 + lane / 4) * kCodeRow + lane % 4 * 16, src, in);
+        const uint32_t dst = ring + slot * C::kCodeSlot + lane / 4 * kCodeRow + lane % 4 * 16;  // row lane / 4, then 8 on
+        cp_async<16>(dst, in0 ? src : p.Wp, in0);
+        cp_async<16>(dst + 8 * kCodeRow, in0 ? src + 512 : p.Wp, in0);
+        cp_async<16>(dst + 16 * kCodeRow, in1 ? src + tile_bytes : p.Wp, in1);
+        cp_async<16>(dst + 24 * kCodeRow, in1 ? src + tile_bytes + 512 : p.Wp, in1);
+        const int gr = (b0 + load_b) * kPer;
+        if (lane < kPer * kELanes) {
+          const bool in = e_in && gr + e_group < p.groups;
+          cp_async<kE>(ring + slot * C::kCodeSlot + C::kScales + lane * kE, in ? e_src : p.scale, in);
         }
+        if (ASYM && lane < kPer * 8) {
+          const bool in = z_in && gr + z_group < p.groups;
+          cp_async<4>(ring + slot * C::kCodeSlot + C::kZeros + lane * 4, in ? z_src : p.zero, in);
+        }
+        src += 2 * kTileBytes;
+        e_src += 2 * kPer * p.N;
+        if (ASYM) z_src += 2 * kPer * p.N;
         load_b += 2;
-        if (load_b >= nb) load_b = wg, load_rb += clusters;
+        if (load_b >= nb) {
+          load_b = wg;
+          load_rb += clusters;
+          if (load_rb < p.row_blocks) locate();
+        }
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
     };
-#pragma unroll
+#pragma unroll 1
     for (int i = 0; i < C::kCodeStages - 1; ++i) fetch(i);
 
-    constexpr int kPer = 128 / G;  // groups of a block
-    uint32_t e_next[kPer], z_next[kPer];
-    auto factors = [&](int rb, int b) {  // this row's, of the block's groups
-      const int64_t n = static_cast<int64_t>(rb) * 128 + row;
-#pragma unroll
-      for (int j = 0; j < kPer; ++j) {
-        const int gr = (b0 + b) * kPer + j;
-        e_next[j] = 0;
-        z_next[j] = 8;
-        if (rb < p.row_blocks && b < nb && n < p.N && gr < p.groups) {
-          e_next[j] = __ldg(p.scale + gr * p.N + n);
-          if (ASYM) z_next[j] = __ldg(p.zero + gr * p.N + n);
-        }
-      }
-    };
     int slot = 0, free_slot = C::kCodeStages - 1, u = 0;
     uint4 code[4];
     float e[kPer], e_old[kPer];
     uint32_t z[kPer];
-    factors(cluster, wg);
-    // block b of row block rb: codes into registers, its factors, the next block's on their way
-    auto take = [&](int rb, int b) {
+    // the next block's codes and this row's factors into registers
+    auto take = [&]() {
       asm volatile("cp.async.wait_group %0;" ::"n"(C::kCodeStages - 2) : "memory");
       __syncwarp();
       fetch(free_slot);
+      const uint8_t* at = ring_p + slot * C::kCodeSlot;
 #pragma unroll
-      for (int c = 0; c < 4; ++c) code[c] = *reinterpret_cast<const uint4*>(ring_p + slot * kCodeSlot + lane * kCodeRow + c * 16);
-      free_slot = slot;
-      slot = slot + 1 == C::kCodeStages ? 0 : slot + 1;
+      for (int c = 0; c < 4; ++c) code[c] = *reinterpret_cast<const uint4*>(at + lane * kCodeRow + c * 16);
 #pragma unroll
       for (int j = 0; j < kPer; ++j) {
-        e[j] = bf16_lo(e_next[j]);
-        z[j] = 0x43004300u | z_next[j] | (z_next[j] << 16);
+        e[j] = bf16_lo(*reinterpret_cast<const uint16_t*>(at + C::kScales + j * 64 + lane * 2));
+        const uint32_t zero = ASYM ? at[C::kZeros + j * 32 + lane] : 8u;
+        z[j] = 0x43004300u | zero | (zero << 16);
       }
-      if (b + 2 < nb)
-        factors(rb, b + 2);
-      else
-        factors(rb + clusters, wg);
+      free_slot = slot;
+      slot = slot + 1 == C::kCodeStages ? 0 : slot + 1;
     };
     // half h of the block as operand A of unit `at`
     auto convert = [&](int h, int at) {
@@ -329,7 +370,7 @@ int4_tc_kernel(const __grid_constant__ CUtensorMap x_map, const TcParams p) {
       if (next_h == 0) {
 #pragma unroll
         for (int j = 0; j < kPer; ++j) e_old[j] = e[j];
-        take(next_rb, next_b);
+        take();
       }
       convert(next_h, ahead++);
       if (++next_h == C::kHalves) {
