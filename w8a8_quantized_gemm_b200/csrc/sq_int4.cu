@@ -567,7 +567,7 @@ cudaError_t launch_team(const TeamParams& q, int sms, cudaStream_t stream) {
   return launch_kernel(kernel, dim3(static_cast<unsigned>(ctas)), dim3(kTeamWarps * 32), smem, stream, true, q);
 }
 
-// ---- more tokens, or rows too long for the above: bf16 matrix instructions.
+// ---- 5 to 16 tokens, or rows too long for the above: bf16 matrix instructions.
 // The weight rows are the 16 rows of 16x8x16 instructions, 8 NT tokens their columns. Codes become
 // bf16 exactly (128 + code, minus 128 + zero); a group's fp32 sum is scaled and added to the
 // total. Teams and rings as above; the activations come in chunks of `cp` pairs of column blocks
@@ -586,11 +586,9 @@ struct WideParams {
   unsigned int* status;
 };
 
-constexpr int wide_warps(int NT) { return NT == 8 ? 8 : 16; }  // 64 tokens' sums need the registers
-
 template <int NT, int G, bool ASYM>
-__global__ void __launch_bounds__(wide_warps(NT) * 32, 1) int4_wide_kernel(const WideParams q) {
-  constexpr int W = wide_warps(NT), kThreads = W * 32, kGroups = 256 / G, kSlot = team_slot_bytes<G, ASYM>();
+__global__ void __launch_bounds__(kTeamWarps * 32, 1) int4_wide_kernel(const WideParams q) {
+  constexpr int W = kTeamWarps, kThreads = W * 32, kGroups = 256 / G, kSlot = team_slot_bytes<G, ASYM>();
   constexpr int kScales = 2 * kTileBytes, kZeros = kScales + kGroups * 32;
   const LinearParams& p = q.p;
   extern __shared__ __align__(16) uint8_t smem[];
@@ -803,16 +801,14 @@ __global__ void __launch_bounds__(wide_warps(NT) * 32, 1) int4_wide_kernel(const
 
 template <int NT, int G, bool ASYM>
 cudaError_t launch_wide(const LinearParams& p, int sms, unsigned int* status, cudaStream_t stream) {
-  constexpr int W = wide_warps(NT), kSlot = team_slot_bytes<G, ASYM>();
+  constexpr int W = kTeamWarps, kSlot = team_slot_bytes<G, ASYM>();
   WideParams q{};
   q.p = p;
   q.Kp = (p.Kb + 1) / 2;
   q.status = status;
   const int64_t Nt = (p.N + 15) / 16;
-  // Cost in units of one pair of blocks at the SM's share of the bandwidth, or of the matrix
-  // instructions where they take longer; a warp alone reaches about a tenth of that. A round of
-  // tiles has its start and end, a cluster's joins cost as much again.
-  const double unit = std::max(1.0, NT * 64 / 176.0);
+  // Cost in units of one pair of blocks at the SM's share of the bandwidth; a warp alone reaches
+  // about a tenth of that. A round of tiles has its start and end, a cluster's joins cost as much again.
   double least = 1e30;
   size_t smem = 0;
   for (int split = 1; split <= 8 && split <= q.Kp; split *= 2) {
@@ -823,7 +819,7 @@ cudaError_t launch_wide(const LinearParams& p, int sms, unsigned int* status, cu
       const double slow = 0.6 * W / kw;
       const double full = static_cast<double>(rounds - 1) * std::max<double>(teams, slow) +
                           std::max<double>(tiles - (rounds - 1) * teams, slow);
-      const double cost = full * pairs * unit + rounds * (split > 1 ? 60 : 30);
+      const double cost = full * pairs + rounds * (split > 1 ? 60 : 30);
       if (cost >= least) continue;
       // the largest chunks, up to all columns, that leave three slots for every ring
       const int64_t room = kSmemMax - 1024 - static_cast<int64_t>(W) * p.M * 64;
@@ -875,9 +871,7 @@ cudaError_t launch_linear(const LinearParams& p, unsigned int* status, cudaStrea
         return nt == 1 ? launch_team<1, G, ASYM>(q, sms, stream) : launch_team<2, G, ASYM>(q, sms, stream);
   }
   if (p.M <= 8) return launch_wide<1, G, ASYM>(p, sms, status, stream);
-  if (p.M <= 16) return launch_wide<2, G, ASYM>(p, sms, status, stream);
-  if (p.M <= 32) return launch_wide<4, G, ASYM>(p, sms, status, stream);
-  return launch_wide<8, G, ASYM>(p, sms, status, stream);
+  return launch_wide<2, G, ASYM>(p, sms, status, stream);
 }
 
 // Grid of the two tile kernels: one column block per x, row tiles over y so that about `per_sm`
@@ -927,7 +921,9 @@ cudaError_t launch_int4_dequant(const uint8_t* Wp, const uint16_t* scale, const 
 }
 
 cudaError_t launch_int4_linear(const Int4LinearArgs& a, cudaStream_t stream) {
-  if (a.M > 4) return launch_int4_linear_tc(a, stream);
+  // Measured (us; these kernels / tcgen05): 8 x 28672 x 8192 44 / 58, 16 x 28672 x 8192 57 / 58,
+  // 16 x 11008 x 4096 15 / 17, 32 x 28672 x 8192 79 / 63, 64 x 4096 x 4096 45 / 12
+  if (a.M > 16) return launch_int4_linear_tc(a, stream);
   LinearParams p{};
   p.X = a.X;
   p.ldx = a.ldx;

@@ -1,15 +1,15 @@
-// The 4-bit linear layer for more than a few tokens, on the tensor cores (tcgen05).
+// The 4-bit linear layer for 17 to 64 tokens, on the tensor cores (tcgen05).
 //   Y[m,n] = sum_k X[m,k] * (code[n,k] - zero[g,n]) * scale[g,n] + bias[n]
 //
 // The weight rows are the 128 rows of the instructions, the tokens (up to 64) their columns, so
 // that every code is made a bf16 number once for all tokens; the codes' bytes bound the call
-// until about 64 tokens. Two warpgroups take the 128-column blocks of a row block in turn. A thread
+// until about 64 tokens. Warpgroups take the 128-column blocks of a row block in turn. A thread
 // owns a weight row: its 64 bytes of codes (contiguous in the tiled layout) come by asynchronous
 // copies several blocks ahead, become code - zero exactly (128 + code, minus 128 + zero) in the
 // order of the columns, and go into tensor memory as operand A; the tokens are operand B, streamed
 // by TMA. Products and a group's sums are fp32 in tensor memory, one accumulator per group; the
 // warpgroup reads it back, scales it and adds it to its fp32 totals in registers while the
-// other's block is multiplied. At a row block's end the two add up, in order, and so do, through
+// others' blocks are converted and multiplied. At a row block's end they add up, in order, and so do, through
 // distributed shared memory, the CTAs of a cluster that share the columns where there are too
 // few row blocks to go round.
 #include "sq_internal.h"
@@ -23,11 +23,10 @@ namespace sq {
 namespace {
 
 constexpr int kTileBytes = 1024;
-constexpr int kWorkers = 256;                 // two warpgroups
-constexpr int kThreads = kWorkers + 96;       // a warp for TMA, one per warpgroup for the matrix instructions
 constexpr int kCodeRow = 80;                  // 64 bytes of codes: an odd number of 16-byte units
 constexpr int kCodeBytes = 32 * kCodeRow;     // of a warp's rows in a block
 constexpr int64_t kSmemMax = 232448;
+constexpr uint64_t kAbortWaitNs = 10000000;  // 10 ms: far more than a copy takes
 
 struct TcParams {
   int64_t N;
@@ -45,30 +44,34 @@ struct TcParams {
 template <int TOKENS_, int G_>
 struct Cfg {
   static constexpr int kTokens = TOKENS_, G = G_;
+  // Two warpgroups, a warp for TMA and one per warpgroup for the matrix instructions. (Three of them,
+  // with registers handed over by the other warps, were measured no faster: 55 against 56 us at
+  // 16 x 28672 x 8192, 28 against 25 us at 64 x 8192 x 8192; the conversions' logic operations bound both.)
+  static constexpr int kWg = 2, kWorkers = kWg * 128, kThreads = kWorkers + 32 + 32 * kWg;
   // columns of a unit of work: a block, or half of one where its groups' accumulators need the room
-  static constexpr int kUnit = G == 32 ? 64 : 128;
+  static constexpr int kUnit = 128 + (128 / G) * kTokens <= 256 ? 128 : 64;
   static constexpr int kHalves = 128 / kUnit, kGroups = kUnit / G;
   static constexpr int kAtom = kTokens * 128;  // 64 columns of the tokens, 128-byte swizzle
-  static constexpr int kXSlot = kAtom * (kUnit / 64), kXStages = 4;
+  static constexpr int kXSlot = kAtom * (kUnit / 64), kXStages = kTokens == 64 ? 4 : 8;
   // a warp's slot: codes, then the rows' scales and zero points per group
   static constexpr int kPer = 128 / G, kScales = kCodeBytes, kZeros = kScales + kPer * 64;
   static constexpr int kCodeSlot = kZeros + kPer * 32, kCodeStages = 5;
+  static_assert((kXStages & (kXStages - 1)) == 0, "stages are counted with shifts");
   static constexpr int kPart = kTokens * 128 * 4;
-  static constexpr int kX = 0, kCodes = kXStages * kXSlot, kSums = kCodes + 8 * kCodeStages * kCodeSlot;
+  static constexpr int kX = 0, kCodes = kXStages * kXSlot, kSums = kCodes + 4 * kWg * kCodeStages * kCodeSlot;
   static constexpr int kSmem = kSums + kPart + 1024;  // and the alignment
   static_assert(kSmem <= kSmemMax - 1024, "shared memory of an SM");
-  // tensor memory: accumulators of the two warpgroups, then two operands each
-  static constexpr int kD = 0, kDStride = 128, kA = 256, kAStride = 128, kABuffer = 64;
-  static_assert(kGroups * kTokens <= kDStride, "accumulators of a unit");
+  // tensor memory of a warpgroup: accumulators, then two operands
+  static constexpr int kA = kGroups * kTokens, kStride = 256;
+  static_assert(kA + kUnit <= kStride && kWg * kStride <= 512, "tensor memory");
 };
 
 template <int BYTES>
-__device__ __forceinline__ void cp_async(uint32_t dst, const void* src, bool valid) {
+__device__ __forceinline__ void cp_async(uint32_t dst, const void* src) {
   if constexpr (BYTES == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
   else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(BYTES), "r"(valid ? BYTES : 0)
-                 : "memory");
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(BYTES) : "memory");
 }
 __device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
                                        uint32_t accumulate) {
@@ -104,7 +107,10 @@ __device__ __forceinline__ uint32_t sub_bf16x2(uint32_t a, uint32_t b) {
 }
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
-__device__ __forceinline__ void workers_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+template <int THREADS>
+__device__ __forceinline__ void workers_sync() {
+  asm volatile("bar.sync 1, %0;" ::"n"(THREADS) : "memory");
+}
 
 // Cluster-scope arrival on, and wait for, an mbarrier that orders reads of distributed shared memory.
 __device__ __forceinline__ void arrive_cluster(uint32_t cluster_addr) {
@@ -132,18 +138,19 @@ __device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
 }
 
 struct Shared {
-  uint64_t x_full[4], x_empty[4], a_full[2][2], d_full[2], d_free[2], done[2], part_ready, part_free;
+  uint64_t x_full[8], x_empty[8], a_full[2][2], d_full[2], d_free[2], done[2], part_ready, part_free;
   uint32_t tmem;
   volatile uint32_t abort;
 };
 
 template <int TOKENS, int G, bool ASYM>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Cfg<TOKENS, G>::kThreads, 1)
 int4_tc_kernel(const __grid_constant__ CUtensorMap x_map, const TcParams p) {
   using C = Cfg<TOKENS, G>;
   extern __shared__ uint8_t smem_raw[];
   __shared__ Shared sh;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  constexpr int kTmaWarp = 4 * C::kWg;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = blockIdx.x % p.split, cluster = blockIdx.x / p.split, clusters = gridDim.x / p.split;
   const int b0 = static_cast<int>(static_cast<int64_t>(p.Kb) * rank / p.split);
@@ -153,7 +160,7 @@ int4_tc_kernel(const __grid_constant__ CUtensorMap x_map, const TcParams p) {
       mbar_init(&sh.x_full[i], 1);
       mbar_init(&sh.x_empty[i], 1);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < C::kWg; ++i) {
       mbar_init(&sh.a_full[i][0], 128);
       mbar_init(&sh.a_full[i][1], 128);
       mbar_init(&sh.d_full[i], 1);
@@ -165,7 +172,7 @@ int4_tc_kernel(const __grid_constant__ CUtensorMap x_map, const TcParams p) {
     sh.abort = 0;
     fence_mbar_init();
   }
-  if (warp == 9) {
+  if (warp == kTmaWarp) {
     tmem_alloc(&sh.tmem, 512);
     tmem_relinquish();
   }
@@ -189,50 +196,56 @@ int4_tc_kernel(const __grid_constant__ CUtensorMap x_map, const TcParams p) {
     atomicOr(p.status, code);
     return false;
   };
-  // units of a row block in order: pairs of blocks; their halves; first and second warpgroup's block
-  if (warp == 8) {
-    if (lane == 0) {
-      tma_prefetch_desc(&x_map);
-      int n = 0, issued = 0;
+  // Units of a row block in order: kWg blocks at a time, one per warpgroup; their halves; the warpgroups.
+  if (warp >= kTmaWarp) {
+    // A whole warp runs each of these loops, so that addresses and descriptors live in uniform
+    // registers as the instructions want them (one lane alone took 90 cycles an instruction), and one
+    // lane issues.
+    const bool one = elect_one();
+    if (warp == kTmaWarp) {
+      if (one) tma_prefetch_desc(&x_map);
+      unsigned n = 0;
       for (int rb = cluster; rb < p.row_blocks; rb += clusters)
-        for (int pair = 0; pair < nb; pair += 2)
+        for (int base = 0; base < nb; base += C::kWg)
           for (int h = 0; h < C::kHalves; ++h)
-            for (int wg = 0; wg < 2 && pair + wg < nb; ++wg, ++n) {
-              const int s = n % C::kXStages;
-              if (n >= C::kXStages) wait(&sh.x_empty[s], ((n / C::kXStages) - 1) & 1, kErrProducerWait);
-              if (sh.abort) continue;
-              mbar_arrive_expect_tx(&sh.x_full[s], C::kXSlot);
-              const int k0 = (b0 + pair + wg) * 128 + h * C::kUnit;
+            for (int wg = 0; wg < C::kWg && base + wg < nb; ++wg, ++n) {
+              const unsigned s = n % C::kXStages;
+              // slot s has been read; where that gives up, nothing more is brought
+              if (n >= C::kXStages && !wait(&sh.x_empty[s], (n / C::kXStages - 1) & 1, kErrProducerWait)) continue;
+              if (one) {
+                const int k0 = (b0 + base + wg) * 128 + h * C::kUnit;
+                mbar_arrive_expect_tx(&sh.x_full[s], C::kXSlot);
 #pragma unroll
-              for (int a = 0; a < C::kUnit / 64; ++a)
-                tma_load_2d(smem + C::kX + s * C::kXSlot + a * C::kAtom, &x_map, &sh.x_full[s], k0 + a * 64, 0, kEvictLast);
-              issued = n + 1;
+                for (int a = 0; a < C::kUnit / 64; ++a)
+                  tma_load_2d(smem + C::kX + s * C::kXSlot + a * C::kAtom, &x_map, &sh.x_full[s], k0 + a * 64, 0, kEvictLast);
+              }
+              __syncwarp();
             }
       // copies still in flight after a wait gave up end before the CTA does
       if (sh.abort)
-        for (int i = std::max(0, issued - C::kXStages); i < issued; ++i)
-          mbar_wait_bounded(&sh.x_full[i % C::kXStages], (i / C::kXStages) & 1, kDefaultWaitLimitNs);
-    }
-  } else if (warp > 8) {
-    // The whole warp runs the loop (its operands then live in uniform registers, as the instructions
-    // want them) and one lane issues. One warp per warpgroup: a unit costs some hundred cycles here.
-    const int wg = warp - 9;
+        for (int i = 0; i < C::kXStages; ++i) {
+          mbar_wait_bounded(&sh.x_full[i], 0, kAbortWaitNs);
+          mbar_wait_bounded(&sh.x_full[i], 1, kAbortWaitNs);
+        }
+    } else {
+    // One issuing warp per warpgroup: a unit costs some hundred cycles here, which one warp for all
+    // could not keep up with.
+    const int wg = warp - kTmaWarp - 1;
     constexpr uint32_t kIdesc = idesc_bf16_f32(128, C::kTokens);
     const uint64_t x_desc = smem_desc_k128(smem_u32(smem + C::kX));
-    const bool one = elect_one();
-    int n = 0, u = 0;
+    const uint32_t d0 = tmem + wg * C::kStride;
+    unsigned n = 0, u = 0;
     for (int rb = cluster; rb < p.row_blocks; rb += clusters)
-      for (int pair = 0; pair < nb; pair += 2) {
-        const int both = pair + 1 < nb ? 2 : 1;
-        for (int h = 0; h < C::kHalves; ++h, n += both) {
-          if (wg >= both) continue;
-          const int s = (n + wg) % C::kXStages;
+      for (int base = 0; base < nb; base += C::kWg) {
+        const int all = min(C::kWg, nb - base);
+        for (int h = 0; h < C::kHalves; ++h, n += all) {
+          if (wg >= all) continue;
+          const unsigned s = (n + wg) % C::kXStages;
           wait(&sh.x_full[s], ((n + wg) / C::kXStages) & 1, kErrMmaWait);
           wait(&sh.a_full[wg][u & 1], (u >> 1) & 1, kErrMmaWait);
           if (u > 0) wait(&sh.d_free[wg], (u - 1) & 1, kErrMmaWait);
           tc_fence_after();
-          const uint32_t a0 = tmem + C::kA + wg * C::kAStride + (u & 1) * C::kABuffer;
-          const uint32_t d0 = tmem + C::kD + wg * C::kDStride;
+          const uint32_t a0 = d0 + C::kA + (u & 1) * (C::kUnit / 2);
           const uint64_t b0 = x_desc + ((s * C::kXSlot) >> 4);  // addresses count in 16 bytes
           if (one && !sh.abort) {
 #pragma unroll
@@ -250,55 +263,49 @@ int4_tc_kernel(const __grid_constant__ CUtensorMap x_map, const TcParams p) {
       mma_commit(&sh.done[wg]);
       if (!mbar_wait_bounded(&sh.done[wg], 0, kDefaultWaitLimitNs)) atomicOr(p.status, kErrTeardownWait);
     }
+    }
   } else {
     const int wg = warp >> 2, quarter = warp & 3, row = quarter * 32 + lane;
-    const uint32_t tmem_lane = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+    const uint32_t tmem_lane = tmem + wg * C::kStride + (static_cast<uint32_t>(quarter * 32) << 16);
     const uint32_t ring = smem_u32(smem + C::kCodes) + warp * C::kCodeStages * C::kCodeSlot;
     const uint8_t* ring_p = smem + C::kCodes + warp * C::kCodeStages * C::kCodeSlot;
     const int64_t Nt = (p.N + 15) / 16;
     constexpr int kPer = C::kPer;  // groups of a block
-    // ---- this warp's blocks: wg, wg + 2, ... of each row block, codes and factors several ahead
+    // ---- this warp's blocks: wg, wg + kWg, ... of each row block, codes and factors several ahead.
+    // Rows past N take a valid row's bytes and groups past K the last group's: neither is ever used
+    // (the tokens are zero there).
     int load_rb = wg < nb ? cluster : p.row_blocks, load_b = wg;
     const int64_t tile_bytes = static_cast<int64_t>(p.Kb) * kTileBytes;
-    const uint8_t* src = nullptr;  // 16 bytes `lane` of this warp's first tile in the next block
+    const uint8_t *src = nullptr, *z_src = nullptr;  // 16 bytes `lane` of this warp's first tile in the next block
     const uint16_t* e_src = nullptr;
-    const uint8_t* z_src = nullptr;
-    bool in0 = false, in1 = false;
+    int64_t second = 0;  // from the first tile to the second
     // lane's part of a block's scales: 32 rows per group, kE bytes a lane; and of its zero points, 4 bytes
     constexpr int kE = G == 32 ? 8 : 4, kELanes = 64 / kE;
-    const int e_group = lane / kELanes, e_row = lane % kELanes * (kE / 2), z_group = lane / 8, z_row = lane % 8 * 4;
-    bool e_in = false, z_in = false;
+    const int e_group = lane / kELanes % kPer, z_group = lane / 8 % kPer;
     auto locate = [&]() {  // the next row block
-      const int64_t rt = static_cast<int64_t>(load_rb) * 8 + quarter * 2, n = static_cast<int64_t>(load_rb) * 128 + quarter * 32;
-      in0 = rt < Nt;
-      in1 = rt + 1 < Nt;
-      src = p.Wp + rt * tile_bytes + static_cast<int64_t>(b0 + wg) * kTileBytes + lane * 16;
-      e_in = lane < kPer * kELanes && n + e_row < p.N;
-      z_in = lane < kPer * 8 && n + z_row < p.N;
-      e_src = p.scale + ((b0 + wg) * kPer + e_group) * p.N + n + e_row;
-      z_src = p.zero + ((b0 + wg) * kPer + z_group) * p.N + n + z_row;
+      const int64_t rt = static_cast<int64_t>(load_rb) * 8 + quarter * 2, last = Nt - 1;
+      src = p.Wp + (rt < last ? rt : last) * tile_bytes + static_cast<int64_t>(b0 + wg) * kTileBytes + lane * 16;
+      second = rt + 1 < Nt ? tile_bytes : 0;
+      const int64_t n = static_cast<int64_t>(load_rb) * 128 + quarter * 32, e_row = n + lane % kELanes * (kE / 2),
+                    z_row = n + lane % 8 * 4;
+      e_src = p.scale + (e_row < p.N ? e_row : 0);
+      if (ASYM) z_src = p.zero + (z_row < p.N ? z_row : 0);
     };
     if (load_rb < p.row_blocks) locate();
     auto fetch = [&](int slot) {
       if (load_rb < p.row_blocks) {
-        const uint32_t dst = ring + slot * C::kCodeSlot + lane / 4 * kCodeRow + lane % 4 * 16;  // row lane / 4, then 8 on
-        cp_async<16>(dst, in0 ? src : p.Wp, in0);
-        cp_async<16>(dst + 8 * kCodeRow, in0 ? src + 512 : p.Wp, in0);
-        cp_async<16>(dst + 16 * kCodeRow, in1 ? src + tile_bytes : p.Wp, in1);
-        cp_async<16>(dst + 24 * kCodeRow, in1 ? src + tile_bytes + 512 : p.Wp, in1);
+        const uint32_t at = ring + slot * C::kCodeSlot, dst = at + lane / 4 * kCodeRow + lane % 4 * 16;  // row lane / 4, then 8 on
+        cp_async<16>(dst, src);
+        cp_async<16>(dst + 8 * kCodeRow, src + 512);
+        cp_async<16>(dst + 16 * kCodeRow, src + second);
+        cp_async<16>(dst + 24 * kCodeRow, src + second + 512);
         const int gr = (b0 + load_b) * kPer;
-        if (lane < kPer * kELanes) {
-          const bool in = e_in && gr + e_group < p.groups;
-          cp_async<kE>(ring + slot * C::kCodeSlot + C::kScales + lane * kE, in ? e_src : p.scale, in);
-        }
-        if (ASYM && lane < kPer * 8) {
-          const bool in = z_in && gr + z_group < p.groups;
-          cp_async<4>(ring + slot * C::kCodeSlot + C::kZeros + lane * 4, in ? z_src : p.zero, in);
-        }
-        src += 2 * kTileBytes;
-        e_src += 2 * kPer * p.N;
-        if (ASYM) z_src += 2 * kPer * p.N;
-        load_b += 2;
+        if (lane < kPer * kELanes)
+          cp_async<kE>(at + C::kScales + lane * kE, e_src + min(gr + e_group, p.groups - 1) * p.N);
+        if (ASYM && lane < kPer * 8)
+          cp_async<4>(at + C::kZeros + lane * 4, z_src + min(gr + z_group, p.groups - 1) * p.N);
+        src += C::kWg * kTileBytes;
+        load_b += C::kWg;
         if (load_b >= nb) {
           load_b = wg;
           load_rb += clusters;
@@ -312,7 +319,7 @@ int4_tc_kernel(const __grid_constant__ CUtensorMap x_map, const TcParams p) {
 
     int slot = 0, free_slot = C::kCodeStages - 1, u = 0;
     uint4 code[4];
-    float e[kPer], e_old[kPer];
+    float e[kPer];
     uint32_t z[kPer];
     // the next block's codes and this row's factors into registers
     auto take = [&]() {
@@ -333,7 +340,7 @@ int4_tc_kernel(const __grid_constant__ CUtensorMap x_map, const TcParams p) {
     };
     // half h of the block as operand A of unit `at`
     auto convert = [&](int h, int at) {
-      const uint32_t dst = tmem_lane + C::kA + wg * C::kAStride + (at & 1) * C::kABuffer;
+      const uint32_t dst = tmem_lane + C::kA + (at & 1) * (C::kUnit / 2);
 #pragma unroll
       for (int q = 0; q < C::kUnit / 64; ++q) {
         uint32_t r[32];
@@ -363,68 +370,67 @@ int4_tc_kernel(const __grid_constant__ CUtensorMap x_map, const TcParams p) {
     for (int m = 0; m < C::kTokens; ++m) acc[m] = 0.0f;
     float* part = reinterpret_cast<float*>(smem + C::kSums);  // [tokens][128 rows]
     int item = 0;
-    // the conversion runs one unit ahead of the accumulation: unit u's product is formed meanwhile
-    int next_rb = wg < nb ? cluster : p.row_blocks, next_b = wg, next_h = 0, ahead = 0;
-    auto step_next = [&]() {
-      if (next_rb >= p.row_blocks) return;
-      if (next_h == 0) {
-#pragma unroll
-        for (int j = 0; j < kPer; ++j) e_old[j] = e[j];
-        take();
-      }
-      convert(next_h, ahead++);
-      if (++next_h == C::kHalves) {
-        next_h = 0;
-        next_b += 2;
-        if (next_b >= nb) next_b = wg, next_rb += clusters;
-      }
+    // The conversion runs one unit ahead of the accumulation: unit u is multiplied meanwhile.
+    int left = 0;  // units not converted yet
+    for (int rb = cluster; rb < p.row_blocks; rb += clusters) left += (nb - wg + C::kWg - 1) / C::kWg * C::kHalves;
+    int next_h = 0, ahead = 0;
+    float f[kPer];  // the factors of the block being accumulated
+    auto step_ahead = [&]() {
+      if (ahead == left) return;
+      if (next_h == 0) take();
+      if (C::kHalves == 1 || next_h == 0)
+        convert(0, ahead);
+      else
+        convert(1, ahead);
+      ++ahead;
+      next_h = next_h + 1 == C::kHalves ? 0 : next_h + 1;
     };
-    step_next();
+    step_ahead();
     for (int rb = cluster; rb < p.row_blocks; rb += clusters, ++item) {
-      for (int b = wg; b < nb; b += 2)
+      for (int b = wg; b < nb; b += C::kWg)
+#pragma unroll
         for (int h = 0; h < C::kHalves; ++h, ++u) {
-          // the factors of unit u: those before the block taken ahead, if the step ahead took one
-          const bool took = next_h == 0 && next_rb < p.row_blocks;
-          step_next();
+          if (h == 0) {
+#pragma unroll
+            for (int j = 0; j < kPer; ++j) f[j] = e[j];
+          }
+          step_ahead();
           const bool ok = wait(&sh.d_full[wg], u & 1, kErrEpilogueWait);
           if (!__all_sync(0xffffffffu, ok)) continue;
           tc_fence_after();
 #pragma unroll
           for (int j = 0; j < C::kGroups; ++j) {
-            const int of = j + (C::kHalves == 2 ? h * C::kGroups : 0);
-            float f = 0.0f;
-#pragma unroll
-            for (int i = 0; i < kPer; ++i)
-              if (i == of) f = took ? e_old[i] : e[i];
 #pragma unroll
             for (int m = 0; m < C::kTokens; m += 16) {
               uint32_t d[16];
-              tmem_ld_32x32b_x16(tmem_lane + C::kD + wg * C::kDStride + j * C::kTokens + m, d);
+              tmem_ld_32x32b_x16(tmem_lane + j * C::kTokens + m, d);
               tmem_wait_ld();
 #pragma unroll
-              for (int i = 0; i < 16; ++i) acc[m + i] = fmaf(__uint_as_float(d[i]), f, acc[m + i]);
+              for (int i = 0; i < 16; ++i) acc[m + i] = fmaf(__uint_as_float(d[i]), f[h * C::kGroups + j], acc[m + i]);
             }
           }
           tc_fence_before();
           mbar_arrive(&sh.d_free[wg]);
         }
-      // ---- the row block's sums: second warpgroup, plus first, plus the other CTAs'
+      // ---- the row block's sums: the warpgroups' in order, then the other CTAs'
       if (p.split > 1 && item > 0 && !sh.abort &&
           !wait_cluster_bounded(&sh.part_free, (item - 1) & 1, kDefaultWaitLimitNs)) {
         sh.abort = 1;
         atomicOr(p.status, kErrEpilogueWait);
       }
-      workers_sync();
-      if (wg == 1)
+      workers_sync<C::kWorkers>();
+      if (wg == 1) {
 #pragma unroll
         for (int m = 0; m < C::kTokens; ++m) part[m * 128 + row] = acc[m];
-      workers_sync();
-      if (wg == 0)
+      }
+      workers_sync<C::kWorkers>();
+      if (wg == 0) {
 #pragma unroll
         for (int m = 0; m < C::kTokens; ++m) part[m * 128 + row] += acc[m];
+      }
+      workers_sync<C::kWorkers>();
 #pragma unroll
       for (int m = 0; m < C::kTokens; ++m) acc[m] = 0.0f;
-      workers_sync();
       if (p.split > 1) {
         if (threadIdx.x < p.split) arrive_cluster(mapa_shared(&sh.part_ready, threadIdx.x));
         if (!sh.abort && !wait_cluster_bounded(&sh.part_ready, item & 1, kDefaultWaitLimitNs)) {
@@ -433,7 +439,7 @@ int4_tc_kernel(const __grid_constant__ CUtensorMap x_map, const TcParams p) {
         }
       }
       const int pairs = 64 / p.split;  // row pairs that this CTA finishes
-      for (int i = threadIdx.x; i < p.M * pairs; i += kWorkers) {
+      for (int i = threadIdx.x; i < p.M * pairs; i += C::kWorkers) {
         const int m = i / pairs, r = (rank * pairs + i % pairs) * 2;
         const int64_t n = static_cast<int64_t>(rb) * 128 + r;
         if (n >= p.N) continue;
@@ -456,7 +462,7 @@ int4_tc_kernel(const __grid_constant__ CUtensorMap x_map, const TcParams p) {
         *reinterpret_cast<__nv_bfloat162*>(p.Y + m * p.N + n) = __floats2bfloat162_rn(y0, y1);
       }
       if (p.split > 1) {
-        workers_sync();
+        workers_sync<C::kWorkers>();
         if (threadIdx.x < p.split) arrive_cluster(mapa_shared(&sh.part_free, threadIdx.x));
       }
     }
@@ -469,7 +475,7 @@ int4_tc_kernel(const __grid_constant__ CUtensorMap x_map, const TcParams p) {
   else
     __syncthreads();
   tc_fence_after();
-  if (warp == 9) tmem_dealloc(tmem, 512);
+  if (warp == kTmaWarp) tmem_dealloc(tmem, 512);
 }
 
 template <int TOKENS, int G, bool ASYM>
@@ -508,7 +514,7 @@ cudaError_t launch_tc(const Int4LinearArgs& a, cudaStream_t stream) {
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
   const int clusters = std::min(sms / p.split, p.row_blocks);
-  return launch_kernel_clustered(kernel, dim3(static_cast<unsigned>(clusters * p.split)), dim3(kThreads), C::kSmem, stream,
+  return launch_kernel_clustered(kernel, dim3(static_cast<unsigned>(clusters * p.split)), dim3(C::kThreads), C::kSmem, stream,
                                  true, static_cast<unsigned>(p.split), map, p);
 }
 
@@ -525,9 +531,7 @@ cudaError_t launch_tokens(const Int4LinearArgs& a, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_int4_linear_tc(const Int4LinearArgs& a, cudaStream_t stream) {
-  if (a.M <= 16) return launch_tokens<16>(a, stream);
-  if (a.M <= 32) return launch_tokens<32>(a, stream);
-  return launch_tokens<64>(a, stream);
+  return a.M <= 32 ? launch_tokens<32>(a, stream) : launch_tokens<64>(a, stream);
 }
 
 }  // namespace sq
