@@ -272,6 +272,9 @@ struct LinearParams {
 //   sum_k x_k (code - zero) = sum_k x_k code - zero * sum_k x_k,
 // with the group's sums of x taken beforehand. A group's result is scaled and added in fp32.
 //
+// Rows too long for shared memory come in chunks of columns, if every team has one tile only (its
+// sums stay in registers meanwhile).
+//
 // Teams of `kw` warps: each team on a row tile of its own, then on the next that is due (all
 // teams of the grid in turn); within a tile the warps take pairs of 128-column blocks in turn.
 // Every lane brings its own fragments into its warp's ring with asynchronous copies, across tiles
@@ -284,10 +287,11 @@ constexpr int64_t kSmemMax = 232448;
 struct TeamParams {
   LinearParams p;
   int kw;         // warps of a team
-  int sides;      // buffers of partial sums: 2 if a team has more than one tile
+  int rounds;     // tiles of a team
   int ring;       // slots of a warp's ring, 2 to 4
   int Kp;         // pairs of column blocks, the second of the last one may lie past K
-  int col_bytes;  // of a column of activation bytes
+  int cp;         // pairs whose activations are in shared memory at a time: all, or a multiple of kw
+  int col_bytes;  // of a column of them
 };
 
 template <int G, bool ASYM>
@@ -325,10 +329,11 @@ __global__ void __launch_bounds__(kTeamWarps * 32, 1) int4_team_kernel(const Tea
   griddep_launch_dependents();
 
   // shared memory: columns of bytes | [groups][kCols] sums of a group's bytes | rings | partial sums
-  const int sums_at = 3 * p.M * q.col_bytes, ring_at = sums_at + q.Kp * kGroups * kCols * 4;
+  // (with one tile per team, partial sums where the columns were)
+  const int sums_at = 3 * p.M * q.col_bytes, ring_at = sums_at + q.cp * kGroups * kCols * 4;
   const uint32_t ring32 = smem_u32(smem) + ring_at + warp * q.ring * kSlot;
   int* sums = reinterpret_cast<int*>(smem + sums_at);
-  float* part = reinterpret_cast<float*>(smem + ring_at + kTeamWarps * q.ring * kSlot);  // [sides][warps][kCols][16]
+  float* part = reinterpret_cast<float*>(smem + (q.rounds == 1 ? 0 : ring_at + kTeamWarps * q.ring * kSlot));  // [2][warps][kCols][16]
 
   // ---- the next pair to bring
   int load_rt = kw < q.Kp ? rt0 : Nt, load_kp = kw;
@@ -396,34 +401,35 @@ __global__ void __launch_bounds__(kTeamWarps * 32, 1) int4_team_kernel(const Tea
   }
   __syncthreads();
   // then 8 elements per thread and step; a warp takes a pair of blocks: 8 words of 32 columns x 4 quad lanes
-  for (int i = warp; i < p.M * q.Kp; i += kTeamWarps) {
-    const int m = i / q.Kp, kp = i % q.Kp, word = kp * 8 + lane / 4;
-    const float mul = s_mul[m];
-    const uint16_t* src = p.X + m * p.ldx + word * 32 + t * 2;
-    uint32_t v[8];  // columns 2 t, 2 t + 1 of each 8
+  auto to_bytes = [&](int first, int pairs) {
+    for (int i = warp; i < p.M * pairs; i += kTeamWarps) {
+      const int m = i / pairs, kp = i % pairs, word = (first + kp) * 8 + lane / 4;
+      const float mul = s_mul[m];
+      const uint16_t* src = p.X + m * p.ldx + word * 32 + t * 2;
+      uint32_t v[8];  // columns 2 t, 2 t + 1 of each 8
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      const uint32_t x = word * 32 + c * 8 < p.K ? __ldg(reinterpret_cast<const uint32_t*>(src + c * 8)) : 0u;
-      // round to an integer in the low mantissa bits (1.5 * 2^23 added), then bytes with carries:
-      // the three low bytes of v + 0x808080, each less 128, are the signed digits
-      v[2 * c] = __float_as_uint(__fmaf_rn(bf16_lo(x), mul, 12582912.0f)) + (0x00808080u - 0x4B400000u);
-      v[2 * c + 1] = __float_as_uint(__fmaf_rn(bf16_hi(x), mul, 12582912.0f)) + (0x00808080u - 0x4B400000u);
+      for (int c = 0; c < 4; ++c) {
+        const uint32_t x = word * 32 + c * 8 < p.K ? __ldg(reinterpret_cast<const uint32_t*>(src + c * 8)) : 0u;
+        // round to an integer in the low mantissa bits (1.5 * 2^23 added), then bytes with carries:
+        // the three low bytes of v + 0x808080, each less 128, are the signed digits
+        v[2 * c] = __float_as_uint(__fmaf_rn(bf16_lo(x), mul, 12582912.0f)) + (0x00808080u - 0x4B400000u);
+        v[2 * c + 1] = __float_as_uint(__fmaf_rn(bf16_hi(x), mul, 12582912.0f)) + (0x00808080u - 0x4B400000u);
+      }
+#pragma unroll
+      for (int d = 0; d < 3; ++d) {
+        // the order of a word's codes: low nibbles are columns 2t, 16 + 2t, 2t + 1, 17 + 2t, high ones 8 more
+        const uint32_t pick = d == 0 ? 0x0062u : d == 1 ? 0x0051u : 0x0040u;
+        const uint32_t b0 = __byte_perm(__byte_perm(v[0], v[4], pick), __byte_perm(v[1], v[5], pick), 0x5410) ^ 0x80808080u;
+        const uint32_t b1 = __byte_perm(__byte_perm(v[2], v[6], pick), __byte_perm(v[3], v[7], pick), 0x5410) ^ 0x80808080u;
+        const int col = 3 * m + d;
+        *reinterpret_cast<uint2*>(smem + col * q.col_bytes + (2 * kp + lane / 16) * 128 + t * 32 + lane / 4 % 4 * 8) = make_uint2(b0, b1);
+        int sum = __dp4a(static_cast<int>(b0), 0x01010101, __dp4a(static_cast<int>(b1), 0x01010101, 0));
+#pragma unroll
+        for (int o = 1; o < G / 8; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        if (lane % (G / 8) == 0) sums[(kp * kGroups + lane / (G / 8)) * kCols + col] = sum;
+      }
     }
-#pragma unroll
-    for (int d = 0; d < 3; ++d) {
-      // the order of a word's codes: low nibbles are columns 2t, 16 + 2t, 2t + 1, 17 + 2t, high ones 8 more
-      const uint32_t pick = d == 0 ? 0x0062u : d == 1 ? 0x0051u : 0x0040u;
-      const uint32_t b0 = __byte_perm(__byte_perm(v[0], v[4], pick), __byte_perm(v[1], v[5], pick), 0x5410) ^ 0x80808080u;
-      const uint32_t b1 = __byte_perm(__byte_perm(v[2], v[6], pick), __byte_perm(v[3], v[7], pick), 0x5410) ^ 0x80808080u;
-      const int col = 3 * m + d;
-      *reinterpret_cast<uint2*>(smem + col * q.col_bytes + word / 4 * 128 + t * 32 + word % 4 * 8) = make_uint2(b0, b1);
-      int sum = __dp4a(static_cast<int>(b0), 0x01010101, __dp4a(static_cast<int>(b1), 0x01010101, 0));
-#pragma unroll
-      for (int o = 1; o < G / 8; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      if (lane % (G / 8) == 0) sums[(kp * kGroups + lane / (G / 8)) * kCols + col] = sum;
-    }
-  }
-  __syncthreads();
+  };
 
   // B fragments: column 8 nt + g, this lane's 32 bytes of a block; columns past 3 M repeat the last
   // one and nothing reads their results
@@ -434,63 +440,74 @@ __global__ void __launch_bounds__(kTeamWarps * 32, 1) int4_team_kernel(const Tea
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) acc[nt][0] = acc[nt][1] = acc[nt][2] = acc[nt][3] = 0.0f;
   int side = 0, slot = 0, free_slot = q.ring - 1;
-  for (int rt = rt0; rt < Nt; rt += step) {
+  int rt = rt0;
+  for (int round = 0; round < q.rounds; ++round, rt += step) {
+    for (int first = 0; first < q.Kp; first += q.cp) {
+      const int pairs = min(q.cp, q.Kp - first);
+      if (round == 0) {  // (more than one chunk: there is one round)
+        if (first > 0) __syncthreads();  // the chunk before is read
+        to_bytes(first, pairs);
+        __syncthreads();
+      }
 #pragma unroll 1
-    for (int kp = kw; kp < q.Kp; kp += q.kw) {
-      if (q.ring == 4)
-        asm volatile("cp.async.wait_group 2;" ::: "memory");
-      else if (q.ring == 3)
-        asm volatile("cp.async.wait_group 1;" ::: "memory");
-      else
-        asm volatile("cp.async.wait_group 0;" ::: "memory");
-      __syncwarp();  // every lane's copies are there, and the slot before is read
-      fetch(free_slot);
-      const uint8_t* src = smem + ring_at + warp * q.ring * kSlot + slot * kSlot;
-      const uint16_t* es = reinterpret_cast<const uint16_t*>(src + kScales) + g;
-      const uint8_t* zs = src + kZeros + g;
-      const int* sx = sums + kp * kGroups * kCols + 2 * t;
-      free_slot = slot;
-      slot = slot + 1 == q.ring ? 0 : slot + 1;
-      int d[NT][4];
+      for (int kp = rt < Nt ? kw : pairs; kp < pairs; kp += q.kw) {
+        if (q.ring == 4)
+          asm volatile("cp.async.wait_group 2;" ::: "memory");
+        else if (q.ring == 3)
+          asm volatile("cp.async.wait_group 1;" ::: "memory");
+        else
+          asm volatile("cp.async.wait_group 0;" ::: "memory");
+        __syncwarp();  // every lane's copies are there, and the slot before is read
+        fetch(free_slot);
+        const uint8_t* src = smem + ring_at + warp * q.ring * kSlot + slot * kSlot;
+        const uint16_t* es = reinterpret_cast<const uint16_t*>(src + kScales) + g;
+        const uint8_t* zs = src + kZeros + g;
+        const int* sx = sums + kp * kGroups * kCols + 2 * t;
+        free_slot = slot;
+        slot = slot + 1 == q.ring ? 0 : slot + 1;
+        int d[NT][4];
 #pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        const uint4 u0 = *reinterpret_cast<const uint4*>(src + b * 1024 + lane * 16);
-        const uint4 u1 = *reinterpret_cast<const uint4*>(src + b * 1024 + 512 + lane * 16);
-        const uint32_t lo[4] = {u0.x, u0.y, u0.z, u0.w}, hi[4] = {u1.x, u1.y, u1.z, u1.w};
-        uint32_t x[NT][8];
+        for (int b = 0; b < 2; ++b) {
+          const uint4 u0 = *reinterpret_cast<const uint4*>(src + b * 1024 + lane * 16);
+          const uint4 u1 = *reinterpret_cast<const uint4*>(src + b * 1024 + 512 + lane * 16);
+          const uint32_t lo[4] = {u0.x, u0.y, u0.z, u0.w}, hi[4] = {u1.x, u1.y, u1.z, u1.w};
+          uint32_t x[NT][4];  // of two words
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          const uint4 x0 = *reinterpret_cast<const uint4*>(x_col[nt] + (2 * kp + b) * 128);
-          const uint4 x1 = *reinterpret_cast<const uint4*>(x_col[nt] + (2 * kp + b) * 128 + 16);
-          x[nt][0] = x0.x; x[nt][1] = x0.y; x[nt][2] = x0.z; x[nt][3] = x0.w;
-          x[nt][4] = x1.x; x[nt][5] = x1.y; x[nt][6] = x1.z; x[nt][7] = x1.w;
-        }
+          for (int a = 0; a < 4; ++a) {
+            const int gr = (b * 128 + a * 32) / G;
+            if (a % 2 == 0) {
 #pragma unroll
-        for (int a = 0; a < 4; ++a) {
-          const int gr = (b * 128 + a * 32) / G;
-          if (a * 32 % G == 0) {
+              for (int nt = 0; nt < NT; ++nt) {
+                const uint4 v = *reinterpret_cast<const uint4*>(x_col[nt] + (2 * kp + b) * 128 + a * 8);
+                x[nt][0] = v.x; x[nt][1] = v.y; x[nt][2] = v.z; x[nt][3] = v.w;
+              }
+            }
+            if (a * 32 % G == 0) {
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) d[nt][0] = d[nt][1] = d[nt][2] = d[nt][3] = 0;
-          }
-          const uint32_t a0 = lo[a] & 0x0F0F0F0Fu, a1 = hi[a] & 0x0F0F0F0Fu;
-          const uint32_t a2 = (lo[a] >> 4) & 0x0F0F0F0Fu, a3 = (hi[a] >> 4) & 0x0F0F0F0Fu;
+              for (int nt = 0; nt < NT; ++nt) d[nt][0] = d[nt][1] = d[nt][2] = d[nt][3] = 0;
+            }
+            const uint32_t a0 = lo[a] & 0x0F0F0F0Fu, a1 = hi[a] & 0x0F0F0F0Fu;
+            const uint32_t a2 = (lo[a] >> 4) & 0x0F0F0F0Fu, a3 = (hi[a] >> 4) & 0x0F0F0F0Fu;
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) mma_u8s8(d[nt], a0, a1, a2, a3, x[nt][2 * a], x[nt][2 * a + 1]);
-          if ((a + 1) * 32 % G == 0) {
-            const float e0 = bf16_lo(es[gr * 16]), e1 = bf16_lo(es[gr * 16 + 8]);
-            const int z0 = ASYM ? zs[gr * 16] : 8, z1 = ASYM ? zs[gr * 16 + 8] : 8;
+            for (int nt = 0; nt < NT; ++nt) mma_u8s8(d[nt], a0, a1, a2, a3, x[nt][a % 2 * 2], x[nt][a % 2 * 2 + 1]);
+            if ((a + 1) * 32 % G == 0) {
+              const float e0 = bf16_lo(es[gr * 16]), e1 = bf16_lo(es[gr * 16 + 8]);
+              const int z0 = ASYM ? zs[gr * 16] : 8, z1 = ASYM ? zs[gr * 16 + 8] : 8;
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              const int2 sm = *reinterpret_cast<const int2*>(sx + gr * kCols + nt * 8);
-              acc[nt][0] = fmaf(static_cast<float>(d[nt][0] - z0 * sm.x), e0, acc[nt][0]);
-              acc[nt][1] = fmaf(static_cast<float>(d[nt][1] - z0 * sm.y), e0, acc[nt][1]);
-              acc[nt][2] = fmaf(static_cast<float>(d[nt][2] - z1 * sm.x), e1, acc[nt][2]);
-              acc[nt][3] = fmaf(static_cast<float>(d[nt][3] - z1 * sm.y), e1, acc[nt][3]);
+              for (int nt = 0; nt < NT; ++nt) {
+                const int2 sm = *reinterpret_cast<const int2*>(sx + gr * kCols + nt * 8);
+                acc[nt][0] = fmaf(static_cast<float>(d[nt][0] - z0 * sm.x), e0, acc[nt][0]);
+                acc[nt][1] = fmaf(static_cast<float>(d[nt][1] - z0 * sm.y), e0, acc[nt][1]);
+                acc[nt][2] = fmaf(static_cast<float>(d[nt][2] - z1 * sm.x), e1, acc[nt][2]);
+                acc[nt][3] = fmaf(static_cast<float>(d[nt][3] - z1 * sm.y), e1, acc[nt][3]);
+              }
             }
           }
         }
       }
     }
+    if (q.rounds == 1) __syncthreads();  // the columns are read, the sums may take their place
+    if (rt >= Nt) continue;
     // [team][warp][columns][16] sums; the other side is free once the team has met again
     float* mine = part + (side * kTeamWarps + warp) * kCols * 16;
 #pragma unroll
@@ -526,16 +543,37 @@ __global__ void __launch_bounds__(kTeamWarps * 32, 1) int4_team_kernel(const Tea
       }
       *reinterpret_cast<__nv_bfloat162*>(p.Y + m * p.N + n) = __floats2bfloat162_rn(y0, y1);
     }
-    if (q.sides == 2) side ^= 1;
+    side ^= q.rounds > 1;
   }
   asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
+// Shared memory of a team launch; see the kernel's layout.
 template <int G, bool ASYM>
 int64_t team_smem(const TeamParams& q, int nt) {
-  const int64_t cols = nt * 8;
-  return 3 * q.p.M * q.col_bytes + static_cast<int64_t>(q.Kp) * (256 / G) * cols * 4 +
-         kTeamWarps * q.ring * team_slot_bytes<G, ASYM>() + q.sides * kTeamWarps * cols * 64;
+  const int64_t cols = nt * 8, sums = kTeamWarps * cols * 64;
+  const int64_t rest = 3 * q.p.M * q.col_bytes + static_cast<int64_t>(q.cp) * (256 / G) * cols * 4 +
+                       kTeamWarps * q.ring * team_slot_bytes<G, ASYM>();
+  return q.rounds == 1 ? std::max(rest, sums) : rest + 2 * sums;
+}
+
+// Slots and chunks: all columns at once with as many slots as fit, or, with one tile per team, the
+// largest chunks beside three slots (at least 8 pairs, else the other kernel is as fast).
+template <int G, bool ASYM>
+bool team_fits(TeamParams* q, int nt) {
+  const int64_t most = kSmemMax - 1024;
+  auto fits = [&](int ring, int cp) {
+    q->ring = ring;
+    q->cp = cp;
+    q->col_bytes = cp * 256 + 16;  // an odd number of 16-byte units: no bank conflicts
+    return team_smem<G, ASYM>(*q, nt) <= most;
+  };
+  for (int ring = 4; ring >= 2; --ring)
+    if (fits(ring, q->Kp)) return true;
+  if (q->rounds > 1) return false;
+  for (int cp = q->Kp / q->kw * q->kw; cp >= 8; cp -= q->kw)
+    if (fits(3, cp)) return true;
+  return false;
 }
 
 // Warps of a team. A round of tiles takes an SM the time of its bytes, but a tile never less than
@@ -861,14 +899,14 @@ cudaError_t launch_linear(const LinearParams& p, unsigned int* status, cudaStrea
     TeamParams q;
     q.p = p;
     q.Kp = (p.Kb + 1) / 2;
-    q.col_bytes = q.Kp * 256 + 16;  // an odd number of 16-byte units: no bank conflicts
-    const int64_t Nt = (p.N + 15) / 16;
+    const int64_t Nt = (p.N + 15) / 16, ctas = std::min<int64_t>(sms, Nt);
     q.kw = team_warps(Nt, sms, q.Kp);
-    q.sides = Nt > static_cast<int64_t>(sms) * (kTeamWarps / q.kw) ? 2 : 1;
+    const int64_t teams = ctas * (kTeamWarps / q.kw);
+    q.rounds = static_cast<int>((Nt + teams - 1) / teams);
     const int nt = (3 * p.M + 7) / 8;
-    for (q.ring = 4; q.ring >= 2; --q.ring)
-      if (team_smem<G, ASYM>(q, nt) + 1024 <= kSmemMax)
-        return nt == 1 ? launch_team<1, G, ASYM>(q, sms, stream) : launch_team<2, G, ASYM>(q, sms, stream);
+    if (team_fits<G, ASYM>(&q, nt)) {
+      return nt == 1 ? launch_team<1, G, ASYM>(q, sms, stream) : launch_team<2, G, ASYM>(q, sms, stream);
+    }
   }
   if (p.M <= 8) return launch_wide<1, G, ASYM>(p, sms, status, stream);
   return launch_wide<2, G, ASYM>(p, sms, status, stream);
