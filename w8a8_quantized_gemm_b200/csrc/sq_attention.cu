@@ -207,27 +207,39 @@ __device__ __forceinline__ int64_t warp_sum(int64_t v) {
   return v;
 }
 
-// The place `at` (< the number of tiles) as a cursor: prefix sums over 32 sequences at a time.
+// 32 sequences, one a lane: their ranges, tiles (of all units) and the tiles up to each's end.
 template <typename S>
-__device__ __forceinline__ Cursor<S> cursor_at(const AttnParams& p, int units, int64_t at, int lane) {
-  Cursor<S> c;
-  int64_t base = 0;
-  for (int b0 = 0;; b0 += 32) {
-    Range r{};
+struct Scan {
+  Range r;
+  int64_t n, upto;
+  __device__ __forceinline__ Scan(const AttnParams& p, int units, int b0, int lane) : r{} {
     if (b0 + lane < p.B) r = range_of<S>(p, b0 + lane);
-    const int64_t n = static_cast<int64_t>(r.last - r.first) * units;
-    int64_t incl = n;
+    n = static_cast<int64_t>(r.last - r.first) * units;
+    upto = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += v;
+      const int64_t v = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += v;
     }
-    const unsigned past = __ballot_sync(0xffffffffu, at < base + incl);
+  }
+};
+
+// The place `at` (< the number of tiles) as a cursor: prefix sums over 32 sequences at a time,
+// the first of which the caller has.
+template <typename S>
+__device__ __forceinline__ Cursor<S> cursor_at(const AttnParams& p, int units, Scan<S> s, int64_t at, int lane) {
+  Cursor<S> c;
+  int64_t base = 0;
+  for (int b0 = 0;;) {
+    const unsigned past = __ballot_sync(0xffffffffu, at < base + s.upto);
     if (past != 0) {
       const int src = __ffs(past) - 1;
-      const int64_t start = base + __shfl_sync(0xffffffffu, incl - n, src);
+      const int64_t start = base + __shfl_sync(0xffffffffu, s.upto - s.n, src);
       c.b = b0 + src;
-      c.r = range_of<S>(p, c.b);
+      c.r.lo = __shfl_sync(0xffffffffu, s.r.lo, src);
+      c.r.len = __shfl_sync(0xffffffffu, s.r.len, src);
+      c.r.first = __shfl_sync(0xffffffffu, s.r.first, src);
+      c.r.last = __shfl_sync(0xffffffffu, s.r.last, src);
       const int per = c.r.last - c.r.first;
       const int unit = static_cast<int>(divide(at - start, per));
       c.kvh = unit / p.blocks;
@@ -236,7 +248,9 @@ __device__ __forceinline__ Cursor<S> cursor_at(const AttnParams& p, int units, i
       c.tile = c.r.first + static_cast<int>(at - c.unit_pos);
       return c;
     }
-    base += __shfl_sync(0xffffffffu, incl, 31);
+    base += __shfl_sync(0xffffffffu, s.upto, 31);
+    b0 += 32;
+    s = Scan<S>(p, units, b0, lane);
   }
 }
 
@@ -253,9 +267,9 @@ __global__ void __launch_bounds__(S::WARPS * 32, 1) paged_attention_kernel(const
   __shared__ int4 s_unit[2 * W];
   __shared__ int64_t s_span[2 * W][2];
   __shared__ float s_factor[2 * W][S::kHeads], s_sum[2 * W][S::kHeads], s_top[2 * W][S::kHeads];
-  __shared__ int64_t s_from;
-  __shared__ int s_count;
-  __shared__ bool s_last;
+  __shared__ int64_t s_from[2];
+  __shared__ int s_count[2];
+  __shared__ bool s_last[2];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int units = p.c.heads * p.blocks;
   uint8_t* ring = smem + warp * S::kRing;
@@ -263,13 +277,16 @@ __global__ void __launch_bounds__(S::WARPS * 32, 1) paged_attention_kernel(const
   const uint32_t ring32 = smem_u32(ring);
 
   // this CTA's and this warp's piece of the line
-  int64_t total = 0;
-  for (int b = lane; b < p.B; b += 32) {
-    const Range r = range_of<S>(p, b);
-    if (blockIdx.x == 0 && warp == 0 && r.len != __ldg(p.seq_lens + b)) atomicOr(p.status, kErrIndex);
-    total += static_cast<int64_t>(r.last - r.first) * units;
+  const Scan<S> scan(p, units, 0, lane);
+  int64_t total = __shfl_sync(0xffffffffu, scan.upto, 31);
+  if (p.B > 32) {
+    int64_t rest = 0;
+    for (int b = lane + 32; b < p.B; b += 32) {
+      const Range r = range_of<S>(p, b);
+      rest += static_cast<int64_t>(r.last - r.first) * units;
+    }
+    total += warp_sum(rest);
   }
-  total = warp_sum(total);
   const int64_t ctas = min(static_cast<int64_t>(gridDim.x), divide(total + W - 1, W));
   const bool works = blockIdx.x < ctas;
   const int64_t cta0 = works ? divide(total * blockIdx.x, ctas) : 0;
@@ -279,7 +296,7 @@ __global__ void __launch_bounds__(S::WARPS * 32, 1) paged_attention_kernel(const
   __syncwarp();
 
   if (p0 < p1) {
-    Cursor<S> load = cursor_at<S>(p, units, p0, lane), cur = load;
+    Cursor<S> load = cursor_at<S>(p, units, scan, p0, lane), cur = load;
     const int n = static_cast<int>(p1 - p0);
     const int shift = p.c.page_shift;
     // page table entries win .. win + 63 of sequence win_b, one of each half per lane
@@ -680,23 +697,31 @@ __global__ void __launch_bounds__(S::WARPS * 32, 1) paged_attention_kernel(const
   const unsigned parts = __ballot_sync(0xffffffffu, my_unit >= 0), below = parts & ((1u << lane) - 1u);
   const int before = __shfl_sync(0xffffffffu, my_unit, below != 0 ? 31 - __clz(below) : 0);
   const unsigned heads_of_groups = __ballot_sync(0xffffffffu, my_unit >= 0 && (below == 0 || before != my_unit));
-  // every part's factor exp2(its maximum - its unit's), a thread per part and head
-  for (int i = threadIdx.x; i < 2 * W * S::kHeads; i += W * 32) {
-    const int k = i / S::kHeads, hi = i % S::kHeads;
-    if (!((parts >> k) & 1)) continue;
-    const unsigned upto = heads_of_groups & (0xffffffffu >> (31 - k));
-    const int k0 = 31 - __clz(upto);
-    const unsigned after = k == 31 ? 0u : heads_of_groups >> (k + 1);
-    const int k1 = after != 0 ? k + __ffs(after) : 2 * W;
-    float top = -INFINITY, sum = 0.0f;
-    for (int j = k0; j < k1; ++j)
-      if ((parts >> j) & 1) top = fmaxf(top, part_of(j)[S::kHeads * D + hi]);
-    for (int j = k0; j < k1; ++j)
-      if ((parts >> j) & 1)
-        sum = fmaf(shrink(part_of(j)[S::kHeads * D + hi], top), part_of(j)[S::kHeads * (D + 1) + hi], sum);
-    s_factor[k][hi] = shrink(part_of(k)[S::kHeads * D + hi], top);
-    s_top[k][hi] = top;
-    s_sum[k][hi] = sum;
+  // every part's factor exp2(its maximum - its unit's): a warp per head, a lane per part, and
+  // scans that stop at a unit's first part (seg0), whose last one (seg1) then has the whole
+  const int seg0 = 31 - __clz(heads_of_groups & (0xffffffffu >> (31 - lane)));
+  const unsigned later = heads_of_groups & ~(0xffffffffu >> (31 - lane));
+  const int seg1 = later != 0 ? __ffs(later) - 2 : 31;
+  for (int hi = warp; hi < S::kHeads; hi += W) {
+    const bool mine = my_unit >= 0;
+    const float m = mine ? part_of(lane)[S::kHeads * D + hi] : -INFINITY;
+    const float l = mine ? part_of(lane)[S::kHeads * (D + 1) + hi] : 0.0f;
+    float top = m;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const float v = __shfl_up_sync(0xffffffffu, top, o);
+      if (lane - o >= seg0) top = fmaxf(top, v);
+    }
+    top = __shfl_sync(0xffffffffu, top, seg1);
+    const float f = shrink(m, top);
+    float sum = f * l;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const float v = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane - o >= seg0) sum += v;
+    }
+    sum = __shfl_sync(0xffffffffu, sum, seg1);
+    if (mine) s_factor[lane][hi] = f, s_top[lane][hi] = top, s_sum[lane][hi] = sum;
   }
   __syncthreads();
   int open[2] = {-1, -1};  // the part that starts the unit left open
@@ -721,52 +746,79 @@ __global__ void __launch_bounds__(S::WARPS * 32, 1) paged_attention_kernel(const
   }
 
   // ---- joining across CTAs: the last one to bring its part adds them all up in order.
-#pragma unroll 1
-  for (int side = 0; side < 2; ++side) {
-    const int mine = side == 0 ? open[0] : open[1];
-    if (mine < 0) continue;  // uniform over the CTA
-    const int4 unit = s_unit[mine];
+  if (open[0] >= 0 || open[1] >= 0) {  // uniform over the CTA
     __threadfence();
     __syncthreads();
-    if (threadIdx.x == 0) {
-      const int64_t c0 = divide((s_span[mine][0] + 1) * ctas - 1, total);
-      const int count = static_cast<int>(divide(s_span[mine][1] * ctas - 1, total) - c0) + 1;
-      const bool last = atomicAdd(p.counters + unit.x, 1u) == static_cast<unsigned>(count - 1);
-      if (last) p.counters[unit.x] = 0;  // as the next call needs it
-      s_from = c0;
-      s_count = count;
-      s_last = last;
+    if (lane == 0 && warp < 2) {
+      const int at = warp == 0 ? open[0] : open[1];
+      bool last = false;
+      if (at >= 0) {
+        const int64_t c0 = divide((s_span[at][0] + 1) * ctas - 1, total);
+        const int count = static_cast<int>(divide(s_span[at][1] * ctas - 1, total) - c0) + 1;
+        unsigned* counter = p.counters + s_unit[at].x;
+        last = atomicAdd(counter, 1u) == static_cast<unsigned>(count - 1);
+        if (last) *counter = 0;  // as the next call needs it
+        s_from[warp] = c0;
+        s_count[warp] = count;
+      }
+      s_last[warp] = last;
     }
     __syncthreads();
-    if (!s_last) continue;
     __threadfence();
-    const int count = s_count;
+  } else if (threadIdx.x < 2) {
+    s_last[threadIdx.x] = false;
+  }
+  __syncthreads();
+#pragma unroll 1
+  for (int side = 0; side < 2; ++side) {
+    if (!s_last[side]) continue;  // uniform over the CTA
+    if (side == 1 && s_last[0]) __syncthreads();  // side 0 is done with the factors
+    const int4 unit = s_unit[side == 0 ? open[0] : open[1]];
+    const int count = s_count[side];
     // part of the k-th CTA: side 1 in the one where the unit starts, side 0 in the others
-    const float* parts0 = p.parts + s_from * 2 * S::kPart;
+    const float* parts0 = p.parts + s_from[side] * 2 * S::kPart;
     auto part = [&](int k) { return parts0 + (2 * k + (k == 0 ? 1 : 0)) * S::kPart; };
+    auto load4 = [&](int k, int i) { return __ldcg(reinterpret_cast<const float4*>(part(k) + i)); };
+    // the first parts' states are on the way while the factors are found
+    constexpr int kEarly = 8;
+    float4 early[kEarly];
+    if (threadIdx.x * 4 < S::kHeads * D) {
+#pragma unroll
+      for (int k = 0; k < kEarly; ++k)
+        if (k < count) early[k] = load4(k, threadIdx.x * 4);
+    }
     float* factor = reinterpret_cast<float*>(smem);  // [heads][count]; the rings are done with
     for (int hi = warp; hi < S::kHeads; hi += W) {
-      float top = -INFINITY, sum = 0.0f;
-      for (int k = lane; k < count; k += 32) top = fmaxf(top, __ldcg(part(k) + S::kHeads * D + hi));
+      auto top_of = [&](int k) { return k < count ? __ldcg(part(k) + S::kHeads * D + hi) : -INFINITY; };
+      auto sum_of = [&](int k) { return k < count ? __ldcg(part(k) + S::kHeads * (D + 1) + hi) : 0.0f; };
+      const float m = top_of(lane), l = sum_of(lane);
+      float top = m;
+      for (int k = lane + 32; k < count; k += 32) top = fmaxf(top, top_of(k));
 #pragma unroll
       for (int w = 16; w > 0; w >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
+      float sum = 0.0f;
       for (int k = lane; k < count; k += 32) {
-        const float f = shrink(__ldcg(part(k) + S::kHeads * D + hi), top);
+        const float f = shrink(k == lane ? m : top_of(k), top);
         factor[hi * count + k] = f;
-        sum = fmaf(f, __ldcg(part(k) + S::kHeads * (D + 1) + hi), sum);
+        sum = fmaf(f, k == lane ? l : sum_of(k), sum);
       }
 #pragma unroll
       for (int w = 16; w > 0; w >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
-      if (lane == 0) s_sum[0][hi] = sum, s_top[0][hi] = top;
+      if (lane == 0) s_sum[side][hi] = sum, s_top[side][hi] = top;
     }
     __syncthreads();
     for (int i = threadIdx.x * 4; i < S::kHeads * D; i += W * 32 * 4) {
       const int hi = i / D;
       float4 acc = make_float4(0, 0, 0, 0);
+      int k = 0;
+      if (i == threadIdx.x * 4) {
+#pragma unroll
+        for (; k < kEarly; ++k)
+          if (k < count) add(acc, factor[hi * count + k], early[k]);
+      }
 #pragma unroll 8
-      for (int k = 0; k < count; ++k)
-        add(acc, factor[hi * count + k], __ldcg(reinterpret_cast<const float4*>(part(k) + i)));
-      write_out(unit, hi, i % D, acc, s_top[0][hi], s_sum[0][hi]);
+      for (; k < count; ++k) add(acc, factor[hi * count + k], load4(k, i));
+      write_out(unit, hi, i % D, acc, s_top[side][hi], s_sum[side][hi]);
     }
   }
 
@@ -776,6 +828,7 @@ __global__ void __launch_bounds__(S::WARPS * 32, 1) paged_attention_kernel(const
     if (b0 + lane < p.B) {
       const Range r = range_of<S>(p, b0 + lane);
       none = r.first == r.last;
+      if (r.len != __ldg(p.seq_lens + b0 + lane)) atomicOr(p.status, kErrIndex);
     }
     for (unsigned left = __ballot_sync(0xffffffffu, none); left != 0; left &= left - 1) {
       const int64_t b = b0 + __ffs(left) - 1;
