@@ -157,6 +157,8 @@ __device__ __forceinline__ void split_bf16(float a, float b, uint32_t& hi, uint3
 // exp2(a - b) of two running maxima; nothing came before a maximum of -inf.
 __device__ __forceinline__ float shrink(float a, float b) { return a == -INFINITY ? 0.0f : exp2_approx(a - b); }
 
+constexpr int kMaxCtas = 160;  // one per SM
+
 // The tokens lo <= t < len that sequence b attends to, and its tiles first <= i < last.
 struct Range {
   int lo, len, first, last;
@@ -769,10 +771,13 @@ __global__ void __launch_bounds__(S::WARPS * 32, 1) paged_attention_kernel(const
     s_last[threadIdx.x] = false;
   }
   __syncthreads();
-#pragma unroll 1
-  for (int side = 0; side < 2; ++side) {
-    if (!s_last[side]) continue;  // uniform over the CTA
-    if (side == 1 && s_last[0]) __syncthreads();  // side 0 is done with the factors
+  if (s_last[0] || s_last[1]) {  // uniform over the CTA
+    // all warps for the one side, or half of them for each
+    const bool both = s_last[0] && s_last[1];
+    const int side = both ? static_cast<int>(warp >= W / 2) : static_cast<int>(s_last[1]);
+    const int warp0 = both && side == 1 ? W / 2 : 0;
+    const int warps = !both ? W : side == 0 ? W / 2 : W - W / 2;
+    const int first = ((warp - warp0) * 32 + lane) * 4, step = warps * 128;
     const int4 unit = s_unit[side == 0 ? open[0] : open[1]];
     const int count = s_count[side];
     // part of the k-th CTA: side 1 in the one where the unit starts, side 0 in the others
@@ -782,13 +787,15 @@ __global__ void __launch_bounds__(S::WARPS * 32, 1) paged_attention_kernel(const
     // the first parts' states are on the way while the factors are found
     constexpr int kEarly = 8;
     float4 early[kEarly];
-    if (threadIdx.x * 4 < S::kHeads * D) {
+    if (first < S::kHeads * D) {
 #pragma unroll
       for (int k = 0; k < kEarly; ++k)
-        if (k < count) early[k] = load4(k, threadIdx.x * 4);
+        if (k < count) early[k] = load4(k, first);
     }
-    float* factor = reinterpret_cast<float*>(smem);  // [heads][count]; the rings are done with
-    for (int hi = warp; hi < S::kHeads; hi += W) {
+    // factors [heads][count], where the rings were
+    static_assert(S::kSmem >= 2 * S::kHeads * kMaxCtas * 4, "both sides' factors");
+    float* factor = reinterpret_cast<float*>(smem) + side * (S::kHeads * kMaxCtas);
+    for (int hi = warp - warp0; hi < S::kHeads; hi += warps) {
       auto top_of = [&](int k) { return k < count ? __ldcg(part(k) + S::kHeads * D + hi) : -INFINITY; };
       auto sum_of = [&](int k) { return k < count ? __ldcg(part(k) + S::kHeads * (D + 1) + hi) : 0.0f; };
       const float m = top_of(lane), l = sum_of(lane);
@@ -807,11 +814,11 @@ __global__ void __launch_bounds__(S::WARPS * 32, 1) paged_attention_kernel(const
       if (lane == 0) s_sum[side][hi] = sum, s_top[side][hi] = top;
     }
     __syncthreads();
-    for (int i = threadIdx.x * 4; i < S::kHeads * D; i += W * 32 * 4) {
+    for (int i = first; i < S::kHeads * D; i += step) {
       const int hi = i / D;
       float4 acc = make_float4(0, 0, 0, 0);
       int k = 0;
-      if (i == threadIdx.x * 4) {
+      if (i == first) {
 #pragma unroll
         for (; k < kEarly; ++k)
           if (k < count) add(acc, factor[hi * count + k], early[k]);
@@ -841,7 +848,6 @@ __global__ void __launch_bounds__(S::WARPS * 32, 1) paged_attention_kernel(const
 }
 
 // ---------------------------------------------------------------- launch
-constexpr int kMaxCtas = 160;  // one per SM
 
 int cta_count() {
   int dev = 0, sms = 148;
