@@ -133,6 +133,26 @@ def test_linear_many_rows(M, N, K):
     assert torch.equal(Y, Y2)
 
 
+@pytest.mark.parametrize("M", [3, 4, 9, 16, 17, 40])
+def test_linear_nonfinite_tokens_stay_to_themselves(M):
+    """A token with a NaN gives NaN, one with an infinity nothing finite that its weight does not
+    hide (a code equal to its zero point makes NaN); the other tokens' results are as ever."""
+    N, K, group = 48, 400, 64
+    codes, scale, zero = _codes(N, K, group, True, M)
+    x = np.random.default_rng(M).normal(0, 1, (M, K)).astype(np.float32)
+    x[1, 7], x[M - 1, K - 1] = np.nan, -np.inf
+    X = wl.f32_to_bf16_bits(x)
+    X[1, 7], X[M - 1, K - 1] = 0x7FC0, 0xFF80
+    Wp, e, z = _up(codes, scale, zero, True)
+    Y = empty((M, N), torch.bfloat16)
+    sq.sq_int4_linear(dev_bf16(X), Wp, e, z, group, None, Y)
+    sq.sq_sync_status()
+    rest = [m for m in range(M) if m not in (1, M - 1)]
+    y, absum = osv.int4_linear(X[rest], osv.int4_values(codes, scale, zero, group), None)
+    _check_linear(Y[rest], y, absum, K)
+    assert bool(torch.isnan(Y[1]).all()) and not bool(torch.isfinite(Y[M - 1]).any())
+
+
 def test_linear_strided_tokens_neighbours_untouched():
     """Tokens read through a wider leading dimension; rows around Y stay as they were."""
     codes, scale, zero = _codes(48, 272, 128, False, 4)

@@ -252,6 +252,28 @@ def test_attention_large_scores(int8):
 
 
 @pytest.mark.parametrize("int8", [False, True])
+@pytest.mark.parametrize("lens,H", [([40], 4), ([700, 33], 4), ([2000], 24)])
+def test_attention_nonfinite_query_stays_in_its_head(lens, H, int8):
+    rng = np.random.default_rng(H)
+    B, D, P = len(lens), 64, 16
+    table = np.arange(B * 125, dtype=np.int32).reshape(B, 125)
+    cache, (k, v) = _filled(rng, B * 125, 2, P, D, int8)
+    q = _bits(rng, B, H, D)
+    clean = wl.bf16_bits_to_f32(q).astype(np.float64)
+    q[0, 1, 5], q[B - 1, H - 1, 63] = 0x7FC0, 0x7F80  # NaN, infinity
+    out, lse = _attend(dev_bf16(q), cache, torch.from_numpy(table).cuda(),
+                       torch.tensor(lens, dtype=torch.int32).cuda(), D ** -0.5)
+    sq.sq_sync_status()
+    for b, h in ((0, 1), (B - 1, H - 1)):
+        assert bool(torch.isnan(out[b, h]).all()) and bool(torch.isnan(lse[b, h]))
+    keep = np.ones((B, H), bool)
+    keep[0, 1] = keep[B - 1, H - 1] = False
+    o, l, most, absv = osv.paged_attention(clean, k, v, table, lens, D ** -0.5)
+    mask = torch.from_numpy(keep).cuda()
+    _check_attention(out[mask], lse[mask], (o[keep], l[keep], most[keep], absv[keep]), D, max(lens))
+
+
+@pytest.mark.parametrize("int8", [False, True])
 def test_attention_bad_pages_and_lengths(int8):
     """A page out of range hides its tokens, lengths are cut to the table; both are reported."""
     rng = np.random.default_rng(2)

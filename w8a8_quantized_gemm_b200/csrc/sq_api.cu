@@ -101,7 +101,8 @@ sq_status check_heads(const char* fn, const char* what, const void* p, int64_t r
                       int64_t ld) {
   if (rows < 1 || rows > kMaxRows)
     return fail(SQ_ERR_INVALID, "%s: %lld rows of %s out of [1, 2^31-1]", fn, static_cast<long long>(rows), what);
-  if (ld < heads * D) return fail(SQ_ERR_INVALID, "%s: stride %lld of %s below a row", fn, static_cast<long long>(ld), what);
+  if (ld < heads * D)
+    return fail(SQ_ERR_INVALID, "%s: stride %lld of %s below a row", fn, static_cast<long long>(ld), what);
   if (ld % 8 != 0) return fail(SQ_ERR_ALIGN, "%s: stride of %s must be a multiple of 8", fn, what);
   return check_vec(fn, what, p, true);
 }
@@ -125,7 +126,8 @@ sq_status check_cache(const char* fn, const sq_kv_cache* c, sq::KvView* out) {
   if (!int8 && (c->k_scale != nullptr || c->v_scale != nullptr))
     return fail(SQ_ERR_INVALID, "%s: a bf16 cache has no scales", fn);
   if (c->head_dim != 64 && c->head_dim != 96 && c->head_dim != 128 && c->head_dim != 256)
-    return fail(SQ_ERR_INVALID, "%s: head_dim=%lld must be 64, 96, 128 or 256", fn, static_cast<long long>(c->head_dim));
+    return fail(SQ_ERR_INVALID, "%s: head_dim=%lld must be 64, 96, 128 or 256", fn,
+                static_cast<long long>(c->head_dim));
   if (c->heads < 1 || c->heads > kMaxHeads)
     return fail(SQ_ERR_INVALID, "%s: cache heads=%lld out of [1, %lld]", fn, static_cast<long long>(c->heads),
                 static_cast<long long>(kMaxHeads));

@@ -3,7 +3,7 @@
 // "SmoothQuant量化实战" §5.2 (KV-cache INT8 with per-token, per-head scales).
 //
 // Every key and value is read once for all query heads of its key head: at 4 to 16 flops a
-// byte the call is bound by the bytes of the cache. The work is cut into tiles of 16 tokens of
+// byte the call is bound by the bytes of the cache. The work is cut into tiles of 16 or 32 tokens of
 // one key head; all tiles, in the order (sequence, key head, token), form one line that is
 // dealt out evenly: each CTA (one per SM) gets a contiguous piece of it and each of its warps a
 // contiguous piece of that, whatever the sequences' lengths. A warp works by itself: it brings
@@ -369,7 +369,8 @@ __global__ void __launch_bounds__(S::WARPS * 32, 1) paged_attention_kernel(const
         }
         if (INT8) {
           const int64_t sat = valid ? page * p.c.scale_page_stride + row : 0;
-          if (kTile == 32 || lane < 16) cp_async4(dst + 2 * S::kHalf + (lane & (kTile - 1)) * 4, p.c.k_scale + sat, valid);
+          if (kTile == 32 || lane < 16)
+            cp_async4(dst + 2 * S::kHalf + (lane & (kTile - 1)) * 4, p.c.k_scale + sat, valid);
           if (kTile == 32 || lane >= 16)
             cp_async4(dst + 2 * S::kHalf + (kTile + (lane & (kTile - 1))) * 4, p.c.v_scale + sat, valid);
         }
@@ -396,7 +397,7 @@ __global__ void __launch_bounds__(S::WARPS * 32, 1) paged_attention_kernel(const
           const uint16_t* qr = p.q + cur.b * p.ldq + (static_cast<int64_t>(kvh) * p.group + hl) * D;
           if (INT8) {
             uint2 w[kWords][2];
-            float top = 0.0f;
+            uint32_t top = 0;  // bf16 without their signs are in the order of their bits, infinity and NaN last
 #pragma unroll
             for (int j = 0; j < kWords; ++j)
 #pragma unroll
@@ -408,12 +409,13 @@ __global__ void __launch_bounds__(S::WARPS * 32, 1) paged_attention_kernel(const
             for (int j = 0; j < kWords; ++j)
 #pragma unroll
               for (int h = 0; h < 2; ++h)
-                top = fmaxf(fmaxf(top, fmaxf(fabsf(bf16_lo(w[j][h].x)), fabsf(bf16_hi(w[j][h].x)))),
-                            fmaxf(fabsf(bf16_lo(w[j][h].y)), fabsf(bf16_hi(w[j][h].y))));
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            // 2^up brings the largest below 2^22
-            const int up = min(22 + 126 - static_cast<int>(__float_as_uint(top) >> 23), 120);
+                top = __vmaxu2(__vmaxu2(top, w[j][h].x & 0x7FFF7FFFu), w[j][h].y & 0x7FFF7FFFu);
+            top = max(top >> 16, top & 0xFFFFu);
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            // 2^up brings the largest below 2^22; integers cannot carry infinity or NaN, so the
+            // head's scores become NaN
+            const int up = min(22 + 126 - static_cast<int>(top >> 7), 120);
             const float mul = __uint_as_float(static_cast<uint32_t>(up + 127) << 23);
 #pragma unroll
             for (int j = 0; j < kWords; ++j)
@@ -431,7 +433,8 @@ __global__ void __launch_bounds__(S::WARPS * 32, 1) paged_attention_kernel(const
                 qf[nt][kParts / 2][j][h] = rows::pack4(b[0], b[1], b[2], b[3]);
                 qf[nt][kParts - 1][j][h] = rows::pack4(v[0], v[1], v[2], v[3]);
               }
-            const float back = p.scale * __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
+            const float back =
+                top < 0x7F80u ? p.scale * __uint_as_float(static_cast<uint32_t>(127 - up) << 23) : NAN;
             factor[nt][0] = __shfl_sync(0xffffffffu, back, 8 * t);
             factor[nt][1] = __shfl_sync(0xffffffffu, back, 8 * t + 4);
           } else {
@@ -439,7 +442,8 @@ __global__ void __launch_bounds__(S::WARPS * 32, 1) paged_attention_kernel(const
             for (int j = 0; j < kWords; ++j)
 #pragma unroll
               for (int h = 0; h < 2; ++h)
-                qf[nt][0][j][h] = hl < p.group ? __ldg(reinterpret_cast<const uint32_t*>(qr + 16 * j + 8 * h + 2 * t)) : 0u;
+                qf[nt][0][j][h] =
+                    hl < p.group ? __ldg(reinterpret_cast<const uint32_t*>(qr + 16 * j + 8 * h + 2 * t)) : 0u;
             factor[nt][0] = factor[nt][1] = p.scale;
           }
 #pragma unroll
@@ -859,12 +863,13 @@ int cta_count() {
 size_t round256(size_t v) { return (v + 255) & ~size_t(255); }
 
 template <typename S>
-cudaError_t launch_shape(AttnParams p, const PagedAttentionArgs& a, cudaStream_t stream) {
+cudaError_t launch_shape(AttnParams p, cudaStream_t stream) {
   p.blocks = (p.group + S::kHeads - 1) / S::kHeads;
   auto kernel = paged_attention_kernel<S>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(S::kSmem));
   if (e != cudaSuccess) return e;
-  return launch_kernel(kernel, dim3(static_cast<unsigned>(cta_count())), dim3(S::WARPS * 32), S::kSmem, stream, true, p);
+  return launch_kernel(kernel, dim3(static_cast<unsigned>(cta_count())), dim3(S::WARPS * 32), S::kSmem, stream, true,
+                       p);
 }
 
 }  // namespace
@@ -898,17 +903,23 @@ cudaError_t launch_paged_attention(const PagedAttentionArgs& a, cudaStream_t str
   const bool wide = p.group > 8;  // 16 query heads at a time: keys and values are read half as often
   if (a.cache.int8) {
     switch (a.cache.head_dim) {
-      case 64: return wide ? launch_shape<Shape<64, true, 2, 2, 8, 4>>(p, a, stream) : launch_shape<Shape<64, true, 1, 2, 8, 4>>(p, a, stream);
-      case 96: return wide ? launch_shape<Shape<96, true, 2, 2, 8, 2>>(p, a, stream) : launch_shape<Shape<96, true, 1, 2, 8, 3>>(p, a, stream);
-      case 128: return wide ? launch_shape<Shape<128, true, 2, 2, 8, 2>>(p, a, stream) : launch_shape<Shape<128, true, 1, 2, 8, 2>>(p, a, stream);
-      default: return launch_shape<Shape<256, true, 1, 1, 4, 5>>(p, a, stream);
+      case 64: return wide ? launch_shape<Shape<64, true, 2, 2, 8, 4>>(p, stream)
+                           : launch_shape<Shape<64, true, 1, 2, 8, 4>>(p, stream);
+      case 96: return wide ? launch_shape<Shape<96, true, 2, 2, 8, 2>>(p, stream)
+                           : launch_shape<Shape<96, true, 1, 2, 8, 3>>(p, stream);
+      case 128: return wide ? launch_shape<Shape<128, true, 2, 2, 8, 2>>(p, stream)
+                            : launch_shape<Shape<128, true, 1, 2, 8, 2>>(p, stream);
+      default: return launch_shape<Shape<256, true, 1, 1, 4, 5>>(p, stream);
     }
   }
   switch (a.cache.head_dim) {
-    case 64: return wide ? launch_shape<Shape<64, false, 2, 2, 8, 2>>(p, a, stream) : launch_shape<Shape<64, false, 1, 2, 8, 2>>(p, a, stream);
-    case 96: return wide ? launch_shape<Shape<96, false, 2, 1, 8, 3>>(p, a, stream) : launch_shape<Shape<96, false, 1, 1, 8, 3>>(p, a, stream);
-    case 128: return wide ? launch_shape<Shape<128, false, 2, 1, 4, 5>>(p, a, stream) : launch_shape<Shape<128, false, 1, 1, 4, 5>>(p, a, stream);
-    default: return launch_shape<Shape<256, false, 1, 1, 3, 4>>(p, a, stream);
+    case 64: return wide ? launch_shape<Shape<64, false, 2, 2, 8, 2>>(p, stream)
+                         : launch_shape<Shape<64, false, 1, 2, 8, 2>>(p, stream);
+    case 96: return wide ? launch_shape<Shape<96, false, 2, 1, 8, 3>>(p, stream)
+                         : launch_shape<Shape<96, false, 1, 1, 8, 3>>(p, stream);
+    case 128: return wide ? launch_shape<Shape<128, false, 2, 1, 4, 5>>(p, stream)
+                          : launch_shape<Shape<128, false, 1, 1, 4, 5>>(p, stream);
+    default: return launch_shape<Shape<256, false, 1, 1, 3, 4>>(p, stream);
   }
 }
 

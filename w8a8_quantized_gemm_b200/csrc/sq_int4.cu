@@ -48,7 +48,8 @@ __device__ __forceinline__ void cp_async(uint32_t dst, const void* src, bool val
   if constexpr (BYTES == 16)
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
   else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(BYTES), "r"(valid ? BYTES : 0)
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(BYTES),
+                 "r"(valid ? BYTES : 0)
                  : "memory");
 }
 
@@ -80,7 +81,8 @@ int4_quant_kernel(const uint16_t* __restrict__ W, int64_t N, int64_t K, int64_t 
 #pragma unroll
   for (int c = 0; c < 16; ++c) {
     sv[c] = rows::f2_pack(1.0f, 1.0f);
-    if (s != nullptr && c * 8 < cols) sv[c] = __ldg(reinterpret_cast<const unsigned long long*>(s + kb * 128 + c * 8 + 2 * t));
+    if (s != nullptr && c * 8 < cols)
+      sv[c] = __ldg(reinterpret_cast<const unsigned long long*>(s + kb * 128 + c * 8 + 2 * t));
   }
   const int64_t step = static_cast<int64_t>(gridDim.y) * (kInt4Threads / 32);
   int64_t rt = static_cast<int64_t>(blockIdx.y) * (kInt4Threads / 32) + (threadIdx.x >> 5);
@@ -164,7 +166,8 @@ int4_quant_kernel(const uint16_t* __restrict__ W, int64_t N, int64_t K, int64_t 
 #pragma unroll
       for (int a = 0; a < 4; ++a) {
         const float r = __shfl_sync(0xffffffffu, my_r, quad | a);
-        const uint32_t zz = ASYM ? static_cast<uint32_t>(__shfl_sync(0xffffffffu, my_z, quad | a)) * 0x00010001u : 0x00080008u;
+        const uint32_t zz =
+            ASYM ? static_cast<uint32_t>(__shfl_sync(0xffffffffu, my_z, quad | a)) * 0x00010001u : 0x00080008u;
         const uint64_t r2 = rows::f2_pack(r, r);
         word[a] = 0;
 #pragma unroll
@@ -314,7 +317,8 @@ __global__ void __launch_bounds__(kTeamWarps * 32, 1) int4_team_kernel(const Tea
   constexpr int kScales = 2 * kTileBytes, kZeros = kScales + kGroups * 32;
   const LinearParams& p = q.p;
   extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ float s_top[kTeamWarps], s_mul[kTeamTokens], s_back[kTeamTokens];
+  __shared__ uint32_t s_top[kTeamWarps];
+  __shared__ float s_mul[kTeamTokens], s_back[kTeamTokens];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int teams = kTeamWarps / q.kw, team = warp / q.kw, kw = warp % q.kw;
   const int Nt = static_cast<int>((p.N + 15) / 16), step = gridDim.x * teams;
@@ -333,14 +337,16 @@ __global__ void __launch_bounds__(kTeamWarps * 32, 1) int4_team_kernel(const Tea
   const int sums_at = 3 * p.M * q.col_bytes, ring_at = sums_at + q.cp * kGroups * kCols * 4;
   const uint32_t ring32 = smem_u32(smem) + ring_at + warp * q.ring * kSlot;
   int* sums = reinterpret_cast<int*>(smem + sums_at);
-  float* part = reinterpret_cast<float*>(smem + (q.rounds == 1 ? 0 : ring_at + kTeamWarps * q.ring * kSlot));  // [2][warps][kCols][16]
+  float* part =  // [2][warps][kCols][16]
+      reinterpret_cast<float*>(smem + (q.rounds == 1 ? 0 : ring_at + kTeamWarps * q.ring * kSlot));
 
   // ---- the next pair to bring
   int load_rt = kw < q.Kp ? rt0 : Nt, load_kp = kw;
   const uint8_t* load_src = p.Wp + (static_cast<int64_t>(rt0) * p.Kb + 2 * kw) * kTileBytes + lane * 16;
   const int64_t tile_jump = static_cast<int64_t>(step) * p.Kb * kTileBytes;
   // this lane's part of a pair's scales: kScaleLanes lanes of kScaleBytes; of its zero points: 4 bytes
-  constexpr int kScaleBytes = G == 32 ? 8 : 4, kLanesPerGroup = 32 / kScaleBytes, kScaleLanes = kGroups * kLanesPerGroup;
+  constexpr int kScaleBytes = G == 32 ? 8 : 4, kLanesPerGroup = 32 / kScaleBytes;
+  constexpr int kScaleLanes = kGroups * kLanesPerGroup;
   const int e_group = lane / kLanesPerGroup, e_row = lane % kLanesPerGroup * (kScaleBytes / 2);
   const int z_group = lane / 4, z_row = lane % 4 * 4;
   auto fetch = [&](int slot) {
@@ -378,26 +384,27 @@ __global__ void __launch_bounds__(kTeamWarps * 32, 1) int4_team_kernel(const Tea
   const int share = kTeamWarps / p.M;  // warps of a token
   if (warp < share * p.M) {
     const uint16_t* x = p.X + warp / share * p.ldx;
-    float top = 0.0f;
+    uint32_t top = 0;  // bf16 without their signs are in the order of their bits, infinity and NaN last
 #pragma unroll 4
     for (int k = (warp % share * 32 + lane) * 8; k < p.K; k += share * 256) {
       const uint4 v = __ldg(reinterpret_cast<const uint4*>(x + k));
-      const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) top = fmaxf(top, fmaxf(fabsf(bf16_lo(u[i])), fabsf(bf16_hi(u[i]))));
+      top = __vmaxu2(__vmaxu2(top, v.x & 0x7FFF7FFFu), __vmaxu2(v.y & 0x7FFF7FFFu, v.z & 0x7FFF7FFFu));
+      top = __vmaxu2(top, v.w & 0x7FFF7FFFu);
     }
+    top = max(top >> 16, top & 0xFFFFu);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    for (int o = 16; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
     if (lane == 0) s_top[warp] = top;
   }
   __syncthreads();
   if (threadIdx.x < p.M) {
-    float top = 0.0f;
-    for (int w = 0; w < share; ++w) top = fmaxf(top, s_top[threadIdx.x * share + w]);
-    // 2^up brings the largest below 2^22
-    const int up = min(22 + 126 - static_cast<int>(__float_as_uint(top) >> 23), 120);
+    uint32_t top = 0;
+    for (int w = 0; w < share; ++w) top = max(top, s_top[threadIdx.x * share + w]);
+    // 2^up brings the largest below 2^22; integers cannot carry infinity or NaN, so the token's
+    // results become NaN
+    const int up = min(22 + 126 - static_cast<int>(top >> 7), 120);
     s_mul[threadIdx.x] = __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
-    s_back[threadIdx.x] = __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
+    s_back[threadIdx.x] = __uint_as_float(top < 0x7F80u ? static_cast<uint32_t>(127 - up) << 23 : 0x7FC00000u);
   }
   __syncthreads();
   // then 8 elements per thread and step; a warp takes a pair of blocks: 8 words of 32 columns x 4 quad lanes
@@ -419,10 +426,12 @@ __global__ void __launch_bounds__(kTeamWarps * 32, 1) int4_team_kernel(const Tea
       for (int d = 0; d < 3; ++d) {
         // the order of a word's codes: low nibbles are columns 2t, 16 + 2t, 2t + 1, 17 + 2t, high ones 8 more
         const uint32_t pick = d == 0 ? 0x0062u : d == 1 ? 0x0051u : 0x0040u;
-        const uint32_t b0 = __byte_perm(__byte_perm(v[0], v[4], pick), __byte_perm(v[1], v[5], pick), 0x5410) ^ 0x80808080u;
-        const uint32_t b1 = __byte_perm(__byte_perm(v[2], v[6], pick), __byte_perm(v[3], v[7], pick), 0x5410) ^ 0x80808080u;
-        const int col = 3 * m + d;
-        *reinterpret_cast<uint2*>(smem + col * q.col_bytes + (2 * kp + lane / 16) * 128 + t * 32 + lane / 4 % 4 * 8) = make_uint2(b0, b1);
+        uint32_t b0 = __byte_perm(__byte_perm(v[0], v[4], pick), __byte_perm(v[1], v[5], pick), 0x5410);
+        uint32_t b1 = __byte_perm(__byte_perm(v[2], v[6], pick), __byte_perm(v[3], v[7], pick), 0x5410);
+        b0 ^= 0x80808080u;
+        b1 ^= 0x80808080u;
+        const int col = 3 * m + d, at = col * q.col_bytes + (2 * kp + lane / 16) * 128 + t * 32 + lane / 4 % 4 * 8;
+        *reinterpret_cast<uint2*>(smem + at) = make_uint2(b0, b1);
         int sum = __dp4a(static_cast<int>(b0), 0x01010101, __dp4a(static_cast<int>(b1), 0x01010101, 0));
 #pragma unroll
         for (int o = 1; o < G / 8; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
@@ -579,7 +588,9 @@ bool team_fits(TeamParams* q, int nt) {
 // Warps of a team. A round of tiles takes an SM the time of its bytes, but a tile never less than
 // its team's warps need for it, about a tenth of the SM's bandwidth each; teams with more than
 // one tile wait for their slowest warp at each. Among equals the larger team, which is done sooner
-// with a small weight (measured, us, kw 1 / 8 / 16: 28672 x 8192 25 / 31 / 33, 4096 x 4096 8.8 / 4.5 / 4.9).
+// with a small weight. Measured, us, one token, teams of 2 / 4 / 8 / 16 warps: 4096 x 4096
+// 5.3 / 5.0 / 5.1 / 5.7 (8 taken), 11008 x 4096 7.7 / 8.4 / 8.6 / 10.4 (3 taken, 7.8),
+// 28672 x 8192 28.3 / 27.6 / 27.9 / 33.6 (1 taken, 29.5: 6% off the best).
 int team_warps(int64_t Nt, int sms, int Kp) {
   const int64_t tiles = (Nt + sms - 1) / sms;  // of an SM
   int best = 1;
@@ -659,7 +670,8 @@ __global__ void __launch_bounds__(kTeamWarps * 32, 1) int4_wide_kernel(const Wid
   int load_rt = kp0 + kw < kp1 ? rt0 : Nt, load_kp = kp0 + kw;
   const uint8_t* load_src = p.Wp + (static_cast<int64_t>(rt0) * p.Kb + 2 * load_kp) * kTileBytes + lane * 16;
   const int64_t tile_jump = static_cast<int64_t>(step) * p.Kb * kTileBytes;
-  constexpr int kScaleBytes = G == 32 ? 8 : 4, kLanesPerGroup = 32 / kScaleBytes, kScaleLanes = kGroups * kLanesPerGroup;
+  constexpr int kScaleBytes = G == 32 ? 8 : 4, kLanesPerGroup = 32 / kScaleBytes;
+  constexpr int kScaleLanes = kGroups * kLanesPerGroup;
   const int e_group = lane / kLanesPerGroup, e_row = lane % kLanesPerGroup * (kScaleBytes / 2);
   const int z_group = lane / 4, z_row = lane % 4 * 4;
   auto fetch = [&](int slot) {

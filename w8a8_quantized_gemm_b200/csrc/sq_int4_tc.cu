@@ -217,7 +217,8 @@ int4_tc_kernel(const __grid_constant__ CUtensorMap x_map, const TcParams p) {
                 mbar_arrive_expect_tx(&sh.x_full[s], C::kXSlot);
 #pragma unroll
                 for (int a = 0; a < C::kUnit / 64; ++a)
-                  tma_load_2d(smem + C::kX + s * C::kXSlot + a * C::kAtom, &x_map, &sh.x_full[s], k0 + a * 64, 0, kEvictLast);
+                  tma_load_2d(smem + C::kX + s * C::kXSlot + a * C::kAtom, &x_map, &sh.x_full[s], k0 + a * 64, 0,
+                              kEvictLast);
               }
               __syncwarp();
             }
@@ -294,7 +295,8 @@ int4_tc_kernel(const __grid_constant__ CUtensorMap x_map, const TcParams p) {
     if (load_rb < p.row_blocks) locate();
     auto fetch = [&](int slot) {
       if (load_rb < p.row_blocks) {
-        const uint32_t at = ring + slot * C::kCodeSlot, dst = at + lane / 4 * kCodeRow + lane % 4 * 16;  // row lane / 4, then 8 on
+        const uint32_t at = ring + slot * C::kCodeSlot;
+        const uint32_t dst = at + lane / 4 * kCodeRow + lane % 4 * 16;  // row lane / 4, then 8 on
         cp_async<16>(dst, src);
         cp_async<16>(dst + 8 * kCodeRow, src + 512);
         cp_async<16>(dst + 16 * kCodeRow, src + second);
