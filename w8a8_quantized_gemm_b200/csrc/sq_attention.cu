@@ -3,10 +3,14 @@
 // "SmoothQuant量化实战" §5.2 (KV-cache INT8 with per-token, per-head scales).
 //
 // Every key and value is read once for all query heads of its key head: at 4 to 16 flops a
-// byte the call is bound by the bytes of the cache. The work is cut into tiles of 16 or 32 tokens of
-// one key head; all tiles, in the order (sequence, key head, token), form one line that is
-// dealt out evenly: each CTA (one per SM) gets a contiguous piece of it and each of its warps a
-// contiguous piece of that, whatever the sequences' lengths. A warp works by itself: it brings
+// byte the call is bound by the bytes of the cache where it is long (64 sequences of up to 8192,
+// 8 key heads of 128, 64 query heads: 128 us, 5.4 TB/s of int8 cache) and by the chain of
+// dependent steps where it is short (one such sequence, 32 query heads: 16.7 us: page table,
+// tile and queries 4, scores and values of two tiles 3, the two joins 5). The work is cut into
+// tiles of 16 or 32 tokens of one key head; all tiles, in the order (sequence, key head, token),
+// form one line that is dealt out evenly: each CTA (one per SM) gets a contiguous piece of it and
+// each of its warps a contiguous piece of that, whatever the sequences' lengths. A warp works by
+// itself: it brings
 // its tiles into its own ring of shared memory with asynchronous copies, several tiles ahead,
 // and keeps the running maximum m, the sum l and the unnormalised output of the 8 (or 16) query
 // heads in registers. Only where a piece ends inside a key head's tiles is the state joined with
@@ -900,26 +904,32 @@ cudaError_t launch_paged_attention(const PagedAttentionArgs& a, cudaStream_t str
   p.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(a.ws) + round256(static_cast<size_t>(a.B) * a.H * 4));
   p.status = a.status;
   p.group = static_cast<int>(a.H) / a.cache.heads;
-  const bool wide = p.group > 8;  // 16 query heads at a time: keys and values are read half as often
+  // 16 query heads at a time where a key head has more than 8: keys and values are read half as
+  // often (32 sequences of up to 8192, 4 key heads of 128, int8, 16 query heads each: 62 us, by
+  // eights 74). Warps rather than stages, since a warp's instructions wait for one another: us at
+  // 32 sequences of up to 4096 and 8 key heads, 8 warps of 2 tiles each against 4 of 5: 128 bf16
+  // 64 / 77, 256 int8 74 / 98. Tiles of 32 tokens for int8, whose part per tile is the larger: 64
+  // sequences of up to 8192, 8 key heads of 128: 128 us, of 16 tokens 163.
+  const bool wide = p.group > 8;
   if (a.cache.int8) {
     switch (a.cache.head_dim) {
       case 64: return wide ? launch_shape<Shape<64, true, 2, 2, 8, 4>>(p, stream)
-                           : launch_shape<Shape<64, true, 1, 2, 8, 4>>(p, stream);
+                           : launch_shape<Shape<64, true, 1, 2, 12, 3>>(p, stream);
       case 96: return wide ? launch_shape<Shape<96, true, 2, 2, 8, 2>>(p, stream)
-                           : launch_shape<Shape<96, true, 1, 2, 8, 3>>(p, stream);
+                           : launch_shape<Shape<96, true, 1, 2, 10, 2>>(p, stream);
       case 128: return wide ? launch_shape<Shape<128, true, 2, 2, 8, 2>>(p, stream)
                             : launch_shape<Shape<128, true, 1, 2, 8, 2>>(p, stream);
-      default: return launch_shape<Shape<256, true, 1, 1, 4, 5>>(p, stream);
+      default: return launch_shape<Shape<256, true, 1, 1, 8, 2>>(p, stream);
     }
   }
   switch (a.cache.head_dim) {
     case 64: return wide ? launch_shape<Shape<64, false, 2, 2, 8, 2>>(p, stream)
                          : launch_shape<Shape<64, false, 1, 2, 8, 2>>(p, stream);
-    case 96: return wide ? launch_shape<Shape<96, false, 2, 1, 8, 3>>(p, stream)
-                         : launch_shape<Shape<96, false, 1, 1, 8, 3>>(p, stream);
-    case 128: return wide ? launch_shape<Shape<128, false, 2, 1, 4, 5>>(p, stream)
-                          : launch_shape<Shape<128, false, 1, 1, 4, 5>>(p, stream);
-    default: return launch_shape<Shape<256, false, 1, 1, 3, 4>>(p, stream);
+    case 96: return wide ? launch_shape<Shape<96, false, 2, 1, 10, 2>>(p, stream)
+                         : launch_shape<Shape<96, false, 1, 1, 12, 2>>(p, stream);
+    case 128: return wide ? launch_shape<Shape<128, false, 2, 1, 8, 2>>(p, stream)
+                          : launch_shape<Shape<128, false, 1, 1, 8, 2>>(p, stream);
+    default: return launch_shape<Shape<256, false, 1, 1, 4, 2>>(p, stream);
   }
 }
 
