@@ -36,7 +36,7 @@ struct TcParams {
   const uint16_t* bias;
   uint16_t* Y;
   int M, K, Kb, groups;
-  int split;      // CTAs of a cluster
+  int split, log_split;  // CTAs of a cluster
   int row_blocks;
   unsigned int* status;
 };
@@ -131,9 +131,9 @@ __device__ __forceinline__ bool wait_cluster_bounded(uint64_t* bar, uint32_t par
     if (global_timer_ns() - t0 > limit_ns) return false;
   }
 }
-__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+__device__ __forceinline__ float2 ld_cluster_f32x2(uint32_t addr) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
   return v;
 }
 
@@ -421,15 +421,14 @@ int4_tc_kernel(const __grid_constant__ CUtensorMap x_map, const TcParams p) {
         atomicOr(p.status, kErrEpilogueWait);
       }
       workers_sync<C::kWorkers>();
-      if (wg == 1) {
+      // each warpgroup leaves half of its tokens' sums to the other and takes the other's half of its own
+      constexpr int kHalf = C::kTokens / 2;
+      const bool second = wg == 1;
 #pragma unroll
-        for (int m = 0; m < C::kTokens; ++m) part[m * 128 + row] = acc[m];
-      }
+      for (int m = 0; m < kHalf; ++m) part[((second ? 0 : kHalf) + m) * 128 + row] = second ? acc[m] : acc[kHalf + m];
       workers_sync<C::kWorkers>();
-      if (wg == 0) {
 #pragma unroll
-        for (int m = 0; m < C::kTokens; ++m) part[m * 128 + row] += acc[m];
-      }
+      for (int m = 0; m < kHalf; ++m) part[((second ? kHalf : 0) + m) * 128 + row] += second ? acc[kHalf + m] : acc[m];
       workers_sync<C::kWorkers>();
 #pragma unroll
       for (int m = 0; m < C::kTokens; ++m) acc[m] = 0.0f;
@@ -440,28 +439,40 @@ int4_tc_kernel(const __grid_constant__ CUtensorMap x_map, const TcParams p) {
           atomicOr(p.status, kErrEpilogueWait);
         }
       }
-      const int pairs = 64 / p.split;  // row pairs that this CTA finishes
-      for (int i = threadIdx.x; i < p.M * pairs; i += C::kWorkers) {
-        const int m = i / pairs, r = (rank * pairs + i % pairs) * 2;
-        const int64_t n = static_cast<int64_t>(rb) * 128 + r;
-        if (n >= p.N) continue;
-        float y0 = 0.0f, y1 = 0.0f;
-        if (p.split == 1) {
-          y0 = part[m * 128 + r];
-          y1 = part[m * 128 + r + 1];
-        } else {
-          for (int c = 0; c < p.split; ++c) {
-            const uint32_t at = mapa_shared(part + m * 128 + r, c);
-            y0 += ld_cluster_f32(at);
-            y1 += ld_cluster_f32(at + 4);
+      // row pairs that this CTA finishes: 64 / split of every token, eight a thread at a time, so that
+      // the loads from the other CTAs are under way together
+      const int log_pairs = 6 - p.log_split, items = p.M << log_pairs;
+      for (int i0 = threadIdx.x; i0 < items; i0 += 8 * C::kWorkers) {
+        float2 y[8];
+        uint32_t at[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int i = min(i0 + j * C::kWorkers, items - 1);
+          const int m = i >> log_pairs, r = ((rank << log_pairs) + (i & ((1 << log_pairs) - 1))) * 2;
+          at[j] = (m * 128 + r) * 4;
+          y[j] = make_float2(0.0f, 0.0f);
+        }
+        for (int c = 0; c < p.split; ++c) {
+          const uint32_t from = mapa_shared(part, c);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float2 v = ld_cluster_f32x2(from + at[j]);
+            y[j].x += v.x;
+            y[j].y += v.y;
           }
         }
-        if (p.bias != nullptr) {
-          const uint32_t b = __ldg(reinterpret_cast<const uint32_t*>(p.bias + n));
-          y0 += bf16_lo(b);
-          y1 += bf16_hi(b);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int m = at[j] >> 9;
+          const int64_t n = static_cast<int64_t>(rb) * 128 + (at[j] & 511) / 4;
+          if (i0 + j * C::kWorkers >= items || n >= p.N) continue;
+          if (p.bias != nullptr) {
+            const uint32_t b = __ldg(reinterpret_cast<const uint32_t*>(p.bias + n));
+            y[j].x += bf16_lo(b);
+            y[j].y += bf16_hi(b);
+          }
+          *reinterpret_cast<__nv_bfloat162*>(p.Y + m * p.N + n) = __floats2bfloat162_rn(y[j].x, y[j].y);
         }
-        *reinterpret_cast<__nv_bfloat162*>(p.Y + m * p.N + n) = __floats2bfloat162_rn(y0, y1);
       }
       if (p.split > 1) {
         workers_sync<C::kWorkers>();
@@ -508,6 +519,7 @@ cudaError_t launch_tc(const Int4LinearArgs& a, cudaStream_t stream) {
     const double cost = rounds * ((p.Kb + split - 1) / split + (split > 1 ? 6.0 : 3.0));
     if (cost < least) least = cost, p.split = split;
   }
+  while ((1 << p.log_split) < p.split) ++p.log_split;
   CUtensorMap map{};
   if (!make_bf16_operand_map(&map, a.X, static_cast<uint64_t>(a.K), static_cast<uint64_t>(a.M),
                      static_cast<uint64_t>(a.ldx) * 2, TOKENS))
