@@ -388,7 +388,11 @@ SQ_API sq_status sq_dequant_weight_int4(const uint8_t* Wp, const void* w_scale_b
  * Linear layer of a few tokens with a 4-bit weight:
  *   Y[m,n] = bf16_rne( sum_k X[m,k] * (code[n,k] - zero[g,n]) * scale[g,n] + bias[n] ),  g = k / group
  * Products are exact in fp32, sums are fp32 (group by group, then over the groups, in an
- * order that depends on the shapes only: the same inputs give the same bits).
+ * order that depends on the shapes only: the same inputs give the same bits). Up to 4 tokens
+ * may be taken as integers of 23 bits and a power of two instead, with exact group sums:
+ * elements down to 2^-14 of their token's largest are exact, smaller ones off by at most 2^-23
+ * of it, and a token with an infinity or NaN gives NaN. With more tokens those give what the
+ * formula does. Other tokens' results do not depend on them.
  * X: bf16 [M, K], ldx, 1 <= M <= 64 (more tokens: sq_dequant_weight_int4 or the int8 GEMM).
  * For a weight quantized with smoothing factors s, X must already be divided by s (folded
  * into what produces it, [SQ] §4.2). bias: bf16 [N] or NULL. Y: bf16 [M, N].
@@ -456,7 +460,10 @@ SQ_API sq_status sq_rope_kv_append(const void* q_bf16, int64_t ldq, const void* 
  *   out[b,h] = sum_t p_t v_t,  p = softmax_t( scale * (q[b,h] . k_t) ),
  *   over max(0, seq_lens[b] - window) <= t < seq_lens[b]   (window == 0: the whole sequence)
  *   lse[b,h] = log sum_t exp( scale * (q[b,h] . k_t) )
- * with fp32 scores, softmax statistics and sums, one rounding of out to bf16. A sequence of
+ * with fp32 scores, softmax statistics and sums, one rounding of out to bf16. For an int8 cache
+ * the queries are integers of 23 bits and a power of two (exact down to 2^-14 of a head's
+ * largest element, off by at most 2^-23 of it below), so that the scores' sums are exact;
+ * a query head with an infinity or NaN gives NaN. Value scales are not negative. A sequence of
  * length 0 gives out 0 and lse -inf. Cache contents behind a sequence's last token (NaN
  * included) are never used. The work is split over the sequences' lengths and joined in a
  * fixed order: the same inputs give the same bits.
@@ -486,9 +493,9 @@ SQ_API const char* sq_last_error(void);
 /* Synchronises `stream`, then reads and clears the current device's error word, which
  * kernels set when a bounded wait gives up (a device-side stall or lost arrival) instead
  * of spinning forever, when an index that a paged-cache call read from device memory was out
- * of range (its access was skipped), and, in the debug build libsq_debug.so (same ABI, kernels compiled
- * with device-side bounds guards that skip and record an out-of-range access), when a guard
- * fires. Returns SQ_OK, SQ_ERR_TIMEOUT, SQ_ERR_BOUNDS or SQ_ERR_CUDA. */
+ * of range (its access was skipped), and, in the debug build libsq_debug.so (same ABI, kernels
+ * compiled with device-side bounds guards that skip and record an out-of-range access), when a
+ * guard fires. Returns SQ_OK, SQ_ERR_TIMEOUT, SQ_ERR_BOUNDS or SQ_ERR_CUDA. */
 SQ_API sq_status sq_sync_status(sq_stream_t stream);
 
 /* Library version string and the compute capability it was built for ("sm_100a"). */

@@ -27,15 +27,22 @@ def _f64(bits):
 def test_decode_block(B, int8):
     H, heads, D, P, hidden, group, steps = 4, 2, 64, 16, 272, 64, 19
     rng = np.random.default_rng(B)
-    bits = lambda *shape, scale=1.0: wl.f32_to_bf16_bits((rng.normal(0, 1, shape) * scale).astype(np.float32))  # noqa: E731
-    up = lambda a: torch.from_numpy(np.ascontiguousarray(a)).cuda()  # noqa: E731
+
+    def bits(*shape, scale=1.0):
+        return wl.f32_to_bf16_bits((rng.normal(0, 1, shape) * scale).astype(np.float32))
+
+    def up(a):
+        return torch.from_numpy(np.ascontiguousarray(a)).cuda()
+
     # weights, quantized once
-    w_qkv, w_out, bias = bits((H + 2 * heads) * D, hidden, scale=0.06), bits(hidden, H * D, scale=0.06), bits((H + 2 * heads) * D)
+    w_qkv, w_out = bits((H + 2 * heads) * D, hidden, scale=0.06), bits(hidden, H * D, scale=0.06)
+    bias = bits((H + 2 * heads) * D)
     packed = []
     for w in (w_qkv, w_out):
         N, K = w.shape
         G = -(-K // group)
-        p = (empty(sq.sq_int4_weight_bytes(N, K), torch.uint8), empty((G, N), torch.bfloat16), empty((G, N), torch.uint8))
+        p = (empty(sq.sq_int4_weight_bytes(N, K), torch.uint8), empty((G, N), torch.bfloat16),
+             empty((G, N), torch.uint8))
         sq.sq_quant_weight_int4(dev_bf16(w), None, group, *p)
         packed.append(p)
     values = [osv.int4_values(osv.int4_unpack(host(p[0]), *w.shape), host_bits(p[1]), host(p[2]), group)
@@ -49,8 +56,8 @@ def test_decode_block(B, int8):
     table = rng.permutation(2 * B).reshape(B, 2).astype(np.int32)
     cache = _new_cache(2 * B, heads, P, D, int8)
     cos, sin = (up(t) for t in _tables(32, D))
-    x, pos, slots, lens = empty((B, hidden), torch.bfloat16), *(torch.zeros(B, dtype=torch.int32, device="cuda") for _ in range(3))
-    x.zero_()
+    x = torch.zeros((B, hidden), dtype=torch.bfloat16, device="cuda")
+    pos, slots, lens = (torch.zeros(B, dtype=torch.int32, device="cuda") for _ in range(3))
     dt, ws = up(table), sq.workspace(sq.SQ_OP_PAGED_ATTENTION, B, H, D)
     gws = sq.workspace(sq.SQ_OP_INT8_GEMM_DEQUANT, B, hidden, H * D)
     qkv, att = empty((B, H + 2 * heads, D), torch.bfloat16), empty((B, H, D), torch.bfloat16)
@@ -109,6 +116,6 @@ def test_decode_block(B, int8):
     _check_linear(y4, y, absum, H * D)
     codes, d = oracle.quant_act_per_token(a_bits, np.ones(H * D, np.float32))
     assert np.array_equal(host(a8), codes) and np.array_equal(host(d8), d)
-    y = oracle.int8_gemm(codes, host(w8)).astype(np.float64) * d.astype(np.float64)[:, None] * host(e8).astype(np.float64)
+    y = oracle.int8_gemm(codes, host(w8)) * d.astype(np.float64)[:, None] * host(e8).astype(np.float64)
     # two fp32 products, then half a step of bf16
     assert np.all(np.abs(_f64(host_bits(y8)) - y) <= (2.0 ** -8 + 2.0 ** -22) * np.abs(y) + 2.0 ** -133)

@@ -600,7 +600,8 @@ sq_status sq_int4_linear(const void* X_bf16, int64_t M, int64_t K, int64_t ldx, 
   sq_status st = check_rows(fn, "X", X_bf16, M, K, ldx);
   if (st != SQ_OK) return st;
   if (M > 64) return fail(SQ_ERR_INVALID, "%s: M=%lld above 64", fn, static_cast<long long>(M));
-  if (N < 1 || N > kMaxRows) return fail(SQ_ERR_INVALID, "%s: N=%lld out of [1, 2^31-1]", fn, static_cast<long long>(N));
+  if (N < 1 || N > kMaxRows)
+    return fail(SQ_ERR_INVALID, "%s: N=%lld out of [1, 2^31-1]", fn, static_cast<long long>(N));
   if ((st = check_int4(fn, Wp, w_scale_bf16, w_zero, group, N)) != SQ_OK) return st;
   if ((st = check_vec(fn, "bias", bias_bf16, false)) != SQ_OK) return st;
   if ((st = check_vec(fn, "Y", Y_bf16, true)) != SQ_OK) return st;

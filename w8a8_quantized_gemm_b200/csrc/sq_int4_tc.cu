@@ -2,16 +2,18 @@
 //   Y[m,n] = sum_k X[m,k] * (code[n,k] - zero[g,n]) * scale[g,n] + bias[n]
 //
 // The weight rows are the 128 rows of the instructions, the tokens (up to 64) their columns, so
-// that every code is made a bf16 number once for all tokens; the codes' bytes bound the call
-// until about 64 tokens. Warpgroups take the 128-column blocks of a row block in turn. A thread
+// that every code is made a bf16 number once for all tokens. That bounds the call (half of the
+// time a block takes; 64 x 28672 x 8192 68 us, 64 x 8192 x 8192 23.1, of which 4 are the row
+// block's end: the bytes alone would take 19 and 6, the products 19 and 5). Warpgroups take the
+// 128-column blocks of a row block in turn. A thread
 // owns a weight row: its 64 bytes of codes (contiguous in the tiled layout) come by asynchronous
 // copies several blocks ahead, become code - zero exactly (128 + code, minus 128 + zero) in the
 // order of the columns, and go into tensor memory as operand A; the tokens are operand B, streamed
 // by TMA. Products and a group's sums are fp32 in tensor memory, one accumulator per group; the
 // warpgroup reads it back, scales it and adds it to its fp32 totals in registers while the
-// others' blocks are converted and multiplied. At a row block's end they add up, in order, and so do, through
-// distributed shared memory, the CTAs of a cluster that share the columns where there are too
-// few row blocks to go round.
+// others' blocks are converted and multiplied. At a row block's end they add up, in order, and so
+// do, through distributed shared memory, the CTAs of a cluster that share the columns where there
+// are too few row blocks to go round.
 #include "sq_internal.h"
 #include "sq_ptx.cuh"
 
@@ -45,8 +47,8 @@ template <int TOKENS_, int G_>
 struct Cfg {
   static constexpr int kTokens = TOKENS_, G = G_;
   // Two warpgroups, a warp for TMA and one per warpgroup for the matrix instructions. (Three of them,
-  // with registers handed over by the other warps, were measured no faster: 55 against 56 us at
-  // 16 x 28672 x 8192, 28 against 25 us at 64 x 8192 x 8192; the conversions' logic operations bound both.)
+  // with registers handed over by the other warps, were measured no faster: 55 against 58 us at
+  // 16 x 28672 x 8192, 28 against 25 us at 64 x 8192 x 8192.)
   static constexpr int kWg = 2, kWorkers = kWg * 128, kThreads = kWorkers + 32 + 32 * kWg;
   // columns of a unit of work: a block, or half of one where its groups' accumulators need the room
   static constexpr int kUnit = 128 + (128 / G) * kTokens <= 256 ? 128 : 64;
@@ -229,41 +231,41 @@ int4_tc_kernel(const __grid_constant__ CUtensorMap x_map, const TcParams p) {
           mbar_wait_bounded(&sh.x_full[i], 1, kAbortWaitNs);
         }
     } else {
-    // One issuing warp per warpgroup: a unit costs some hundred cycles here, which one warp for all
-    // could not keep up with.
-    const int wg = warp - kTmaWarp - 1;
-    constexpr uint32_t kIdesc = idesc_bf16_f32(128, C::kTokens);
-    const uint64_t x_desc = smem_desc_k128(smem_u32(smem + C::kX));
-    const uint32_t d0 = tmem + wg * C::kStride;
-    unsigned n = 0, u = 0;
-    for (int rb = cluster; rb < p.row_blocks; rb += clusters)
-      for (int base = 0; base < nb; base += C::kWg) {
-        const int all = min(C::kWg, nb - base);
-        for (int h = 0; h < C::kHalves; ++h, n += all) {
-          if (wg >= all) continue;
-          const unsigned s = (n + wg) % C::kXStages;
-          wait(&sh.x_full[s], ((n + wg) / C::kXStages) & 1, kErrMmaWait);
-          wait(&sh.a_full[wg][u & 1], (u >> 1) & 1, kErrMmaWait);
-          if (u > 0) wait(&sh.d_free[wg], (u - 1) & 1, kErrMmaWait);
-          tc_fence_after();
-          const uint32_t a0 = d0 + C::kA + (u & 1) * (C::kUnit / 2);
-          const uint64_t b0 = x_desc + ((s * C::kXSlot) >> 4);  // addresses count in 16 bytes
-          if (one && !sh.abort) {
+      // One issuing warp per warpgroup: a unit costs some hundred cycles here, which one warp for all
+      // could not keep up with.
+      const int wg = warp - kTmaWarp - 1;
+      constexpr uint32_t kIdesc = idesc_bf16_f32(128, C::kTokens);
+      const uint64_t x_desc = smem_desc_k128(smem_u32(smem + C::kX));
+      const uint32_t d0 = tmem + wg * C::kStride;
+      unsigned n = 0, u = 0;
+      for (int rb = cluster; rb < p.row_blocks; rb += clusters)
+        for (int base = 0; base < nb; base += C::kWg) {
+          const int all = min(C::kWg, nb - base);
+          for (int h = 0; h < C::kHalves; ++h, n += all) {
+            if (wg >= all) continue;
+            const unsigned s = (n + wg) % C::kXStages;
+            wait(&sh.x_full[s], ((n + wg) / C::kXStages) & 1, kErrMmaWait);
+            wait(&sh.a_full[wg][u & 1], (u >> 1) & 1, kErrMmaWait);
+            if (u > 0) wait(&sh.d_free[wg], (u - 1) & 1, kErrMmaWait);
+            tc_fence_after();
+            const uint32_t a0 = d0 + C::kA + (u & 1) * (C::kUnit / 2);
+            const uint64_t b0 = x_desc + ((s * C::kXSlot) >> 4);  // addresses count in 16 bytes
+            if (one && !sh.abort) {
 #pragma unroll
-            for (int j = 0; j < C::kUnit / 16; ++j)
-              mma_ts(d0 + j / (G / 16) * C::kTokens, a0 + j * 8, b0 + (((j / 4) * C::kAtom + (j % 4) * 32) >> 4), kIdesc,
-                     j % (G / 16) != 0);
-            mma_commit(&sh.d_full[wg]);
-            mma_commit(&sh.x_empty[s]);
+              for (int j = 0; j < C::kUnit / 16; ++j)
+                mma_ts(d0 + j / (G / 16) * C::kTokens, a0 + j * 8, b0 + (((j / 4) * C::kAtom + (j % 4) * 32) >> 4),
+                       kIdesc, j % (G / 16) != 0);
+              mma_commit(&sh.d_full[wg]);
+              mma_commit(&sh.x_empty[s]);
+            }
+            __syncwarp();
+            ++u;
           }
-          __syncwarp();
-          ++u;
         }
+      if (one) {
+        mma_commit(&sh.done[wg]);
+        if (!mbar_wait_bounded(&sh.done[wg], 0, kDefaultWaitLimitNs)) atomicOr(p.status, kErrTeardownWait);
       }
-    if (one) {
-      mma_commit(&sh.done[wg]);
-      if (!mbar_wait_bounded(&sh.done[wg], 0, kDefaultWaitLimitNs)) atomicOr(p.status, kErrTeardownWait);
-    }
     }
   } else {
     const int wg = warp >> 2, quarter = warp & 3, row = quarter * 32 + lane;
@@ -528,8 +530,8 @@ cudaError_t launch_tc(const Int4LinearArgs& a, cudaStream_t stream) {
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
   const int clusters = std::min(sms / p.split, p.row_blocks);
-  return launch_kernel_clustered(kernel, dim3(static_cast<unsigned>(clusters * p.split)), dim3(C::kThreads), C::kSmem, stream,
-                                 true, static_cast<unsigned>(p.split), map, p);
+  return launch_kernel_clustered(kernel, dim3(static_cast<unsigned>(clusters * p.split)), dim3(C::kThreads), C::kSmem,
+                                 stream, true, static_cast<unsigned>(p.split), map, p);
 }
 
 template <int TOKENS>

@@ -1,7 +1,8 @@
 """Small, self-contained launches of single kernels for profiler captures (ncu).
 
 Usage: python -m w8a8_quantized_gemm_b200.profile_cases
-       {gemm,decode,decode1,llm,quant,absmax,smooth,wquant,norm,asym,meanstd,percentile,rowsums,gemm_asym}
+       {gemm,decode,decode1,llm,quant,absmax,smooth,wquant,norm,asym,meanstd,percentile,rowsums,gemm_asym,
+        int4_quant,int4_lin1,int4_lin16,int4_lin64,append,attention}
 
 Each case makes random device inputs of one workload's shape and calls one entry point three
 times (so that a capture can skip the first, cold launch):
@@ -19,6 +20,12 @@ times (so that a capture can skip the first, cold launch):
   percentile  sq_act_abs_percentile (99.99), X bf16 [8192, 8192]
   rowsums sq_weight_row_sums, Wq int8 [28672, 8192]
   gemm_asym  sq_int8_gemm_dequant_ex with asymmetric activations, 2048 x 11008 x 4096
+  int4_quant  sq_quant_weight_int4 (zero points, groups of 64), W bf16 [28672, 8192]
+  int4_lin1, int4_lin16, int4_lin64  sq_int4_linear of 1, 16, 64 tokens, weight 28672 x 8192,
+          groups of 128
+  append  sq_rope_kv_append, 8192 tokens, 64 query and 8 key heads of 128, int8 cache
+  attention  sq_paged_attention, 64 sequences of 8192, 64 query and 8 key heads of 128, int8
+          cache (1.1 GB)
 """
 import sys
 
@@ -120,6 +127,44 @@ def main(mode: str) -> None:
         Y = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
         for _ in range(3):
             sq.sq_int8_gemm_dequant_ex(Xq, Wq, d, sq.SQ_PER_CHANNEL, z, e, sq.SQ_PER_CHANNEL, rs, None, Y)
+    elif mode in ("int4_quant", "int4_lin1", "int4_lin16", "int4_lin64"):
+        N, K = 28672, 8192
+        group = 64 if mode == "int4_quant" else 128
+        W = (torch.randn(N, K, device=dev) * 0.02).to(torch.bfloat16)
+        Wp = torch.empty(sq.sq_int4_weight_bytes(N, K), dtype=torch.uint8, device=dev)
+        e = torch.empty((K // group, N), dtype=torch.bfloat16, device=dev)
+        z = torch.empty((K // group, N), dtype=torch.uint8, device=dev)
+        for _ in range(3 if mode == "int4_quant" else 1):
+            sq.sq_quant_weight_int4(W, None, group, Wp, e, z)
+        if mode != "int4_quant":
+            M = int(mode[8:])
+            X = torch.randn(M, K, device=dev).to(torch.bfloat16)
+            Y = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
+            for _ in range(3):
+                sq.sq_int4_linear(X, Wp, e, z, group, None, Y)
+    elif mode in ("append", "attention"):
+        H, heads, D, P, B, L = 64, 8, 128, 64, 64, 8192
+        pages = (1 if mode == "append" else B) * L // P
+        k = torch.randint(-127, 128, (2, pages, heads, P, D), dtype=torch.int8, device=dev)
+        sc = torch.rand((2, pages, heads, P), device=dev) * 0.02
+        cache = sq.KvCache(k[0], k[1], sc[0], sc[1])
+        if mode == "append":
+            qkv = torch.randn(L, H + 2 * heads, D, device=dev).to(torch.bfloat16)
+            pos = torch.arange(L, dtype=torch.int32, device=dev)
+            angle = pos[:, None] * 10000.0 ** (-torch.arange(D // 2, device=dev) * 2 / D)
+            slots = torch.randperm(L, device=dev).to(torch.int32)
+            out = torch.empty((L, H, D), dtype=torch.bfloat16, device=dev)
+            for _ in range(3):
+                sq.sq_rope_kv_append(qkv[:, :H], qkv[:, H:H + heads], qkv[:, H + heads:], angle.cos(), angle.sin(), pos,
+                                     slots, cache, out)
+        else:
+            q = torch.randn(B, H, D, device=dev).to(torch.bfloat16)
+            table = torch.randperm(pages, device=dev).to(torch.int32).view(B, L // P)
+            lens = torch.full((B,), L, dtype=torch.int32, device=dev)
+            out = torch.empty_like(q)
+            ws = sq.workspace(sq.SQ_OP_PAGED_ATTENTION, B, H, D)
+            for _ in range(3):
+                sq.sq_paged_attention(q, cache, table, lens, D ** -0.5, out, ws=ws)
     else:
         raise SystemExit(f"unknown case {mode!r}")
     sq.sq_sync_status()

@@ -478,7 +478,8 @@ def sq_rope_kv_append(q, k, v, cos, sin, positions, slots, cache: KvCache, q_out
         cp = _dense(cos, torch.float32, (max_pos, half), "cos", dev)
         sp = _dense(sin, torch.float32, (max_pos, half), "sin", dev)
         pp = _dense(positions, torch.int32, (T,), "positions", dev)
-    _check(_lib.sq_rope_kv_append(qp, ldq, kp, ldk, vp, ldv, T, H, cp, sp, max_pos, 2 * half, 1 if interleaved else 0, pp,
+    _check(_lib.sq_rope_kv_append(qp, ldq, kp, ldk, vp, ldv, T, H, cp, sp, max_pos, 2 * half,
+                                  1 if interleaved else 0, pp,
                                   _dense(slots, torch.int32, (T,), "slots", dev), cache.ref, op, _on(stream, dev)))
     return q_out
 
