@@ -153,6 +153,30 @@ def test_linear_nonfinite_tokens_stay_to_themselves(M):
     assert bool(torch.isnan(Y[1]).all()) and not bool(torch.isfinite(Y[M - 1]).any())
 
 
+@pytest.mark.parametrize("M,N,K,group", [(1, 2848, 4128, 128), (2, 2856, 23552, 32), (3, 9480, 1168, 64),
+                                         (4, 9480, 13312, 128), (13, 3016, 27872, 64), (16, 4104, 4112, 128),
+                                         (38, 4664, 3696, 32), (25, 344, 16704, 64), (64, 1032, 8208, 64)])
+def test_linear_large(M, N, K, group):
+    """Many rows, long rows, both: activations that do not fit shared memory at once, clusters that
+    do not all run at once. Every byte is a pair of codes, so the codes are random bytes and their
+    integer values come from the (tested) values call with scales of one."""
+    G = -(-K // group)
+    gen = torch.Generator(device="cuda").manual_seed(M + N)
+    Wp = torch.randint(0, 256, (sq.sq_int4_weight_bytes(N, K),), dtype=torch.uint8, device="cuda", generator=gen)
+    z = torch.randint(0, 16, (G, N), dtype=torch.uint8, device="cuda", generator=gen)
+    e = (torch.rand((G, N), device="cuda", generator=gen) * 0.02 + 0.002).to(torch.bfloat16)
+    X = torch.randn((M, K), device="cuda", generator=gen).to(torch.bfloat16)
+    codes = empty((N, K), torch.bfloat16)
+    sq.sq_dequant_weight_int4(Wp, torch.ones_like(e), z, group, codes)
+    values = codes.double() * e.double().t().repeat_interleave(group, 1)[:, :K]
+    Y = empty((M, N), torch.bfloat16)
+    sq.sq_int4_linear(X, Wp, e, z, group, None, Y)
+    sq.sq_sync_status()
+    y = (X.double() @ values.t()).cpu().numpy()
+    absum = (X.double().abs() @ values.abs().t()).cpu().numpy()
+    _check_linear(Y, y, absum, K)
+
+
 def test_linear_strided_tokens_neighbours_untouched():
     """Tokens read through a wider leading dimension; rows around Y stay as they were."""
     codes, scale, zero = _codes(48, 272, 128, False, 4)

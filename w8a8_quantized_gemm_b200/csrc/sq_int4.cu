@@ -14,6 +14,7 @@
 
 #include <algorithm>
 #include <cfloat>
+#include <cmath>
 
 namespace sq {
 namespace {
@@ -617,7 +618,7 @@ cudaError_t launch_team(const TeamParams& q, int sms, cudaStream_t stream) {
   return launch_kernel(kernel, dim3(static_cast<unsigned>(ctas)), dim3(kTeamWarps * 32), smem, stream, true, q);
 }
 
-// ---- 5 to 16 tokens, or rows too long for the above: bf16 matrix instructions.
+// ---- up to 16 tokens: bf16 matrix instructions.
 // The weight rows are the 16 rows of 16x8x16 instructions, 8 NT tokens their columns. Codes become
 // bf16 exactly (128 + code, minus 128 + zero); a group's fp32 sum is scaled and added to the
 // total. Teams and rings as above; the activations come in chunks of `cp` pairs of column blocks
@@ -858,20 +859,24 @@ cudaError_t launch_wide(const LinearParams& p, int sms, unsigned int* status, cu
   q.Kp = (p.Kb + 1) / 2;
   q.status = status;
   const int64_t Nt = (p.N + 15) / 16;
-  // Cost in units of one pair of blocks at the SM's share of the bandwidth; a warp alone reaches
-  // about a tenth of that. A round of tiles has its start and end, a cluster's joins cost as much again.
+  // The shape of the launch by its estimated time in us, fitted to about 100 measured ones (34 sizes,
+  // 1 to 16 tokens; 9% off in the root mean square): a warp alone takes 0.46 for a pair of blocks, all
+  // warps of an SM together 0.106 a pair, and between the two a smooth maximum; the activations come at
+  // 75 KB a us, a chunk of them costs 0.25 where chunks take turns, a round of tiles 0.77, a cluster
+  // of two 1.3 and of four 4 (of eight more than it saves).
   double least = 1e30;
   size_t smem = 0;
-  for (int split = 1; split <= 8 && split <= q.Kp; split *= 2) {
-    const int64_t clusters = sms / split, tiles = (Nt + clusters - 1) / clusters;
+  for (int split = 1; split <= 4 && split <= q.Kp; split *= 2) {
+    const int64_t clusters = std::min<int64_t>(cluster_slots(sms, split), Nt), tiles = (Nt + clusters - 1) / clusters;
     const int pairs = (q.Kp + split - 1) / split;
     for (int kw = 1; kw <= W && kw <= pairs; ++kw) {
       const int64_t teams = W / kw, rounds = (tiles + teams - 1) / teams;
-      const double slow = 0.6 * W / kw;
-      const double full = static_cast<double>(rounds - 1) * std::max<double>(teams, slow) +
-                          std::max<double>(tiles - (rounds - 1) * teams, slow);
-      const double cost = full * pairs + rounds * (split > 1 ? 60 : 30);
-      if (cost >= least) continue;
+      const double x_kb = 0.5 * static_cast<double>(rounds) * pairs * p.M;
+      const double alone = 0.46 * static_cast<double>(rounds) * ((pairs + kw - 1) / kw);
+      const double together = 0.106 * static_cast<double>(tiles) * pairs;
+      const double base = std::cbrt(alone * alone * alone + together * together * together) + x_kb / 75 +
+                          0.77 * static_cast<double>(rounds) + (split == 4 ? 4.0 : split == 2 ? 1.3 : 0.0);
+      if (base >= least) continue;
       // the largest chunks, up to all columns, that leave three slots for every ring
       const int64_t room = kSmemMax - 1024 - static_cast<int64_t>(W) * p.M * 64;
       for (int ring = 4; ring >= 2; --ring) {
@@ -883,7 +888,9 @@ cudaError_t launch_wide(const LinearParams& p, int sms, unsigned int* status, cu
           all = (left / 2 / p.M - 16) / row / kw * kw;
         }
         if (all < kw || (ring > 2 && buffers == 2 && all * p.M < 64)) continue;
-        least = cost;
+        const double turns = buffers == 2 ? 0.25 * static_cast<double>(rounds) * ((pairs + all - 1) / all) : 0.0;
+        if (base + turns >= least) break;
+        least = base + turns;
         q.split = split;
         q.kw = kw;
         q.ring = ring;
@@ -895,7 +902,7 @@ cudaError_t launch_wide(const LinearParams& p, int sms, unsigned int* status, cu
       }
     }
   }
-  const int64_t clusters = std::min<int64_t>(sms / q.split, Nt);
+  const int64_t clusters = std::min<int64_t>(cluster_slots(sms, q.split), Nt);
   auto kernel = int4_wide_kernel<NT, G, ASYM>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return e;
@@ -908,11 +915,17 @@ cudaError_t launch_linear(const LinearParams& p, unsigned int* status, cudaStrea
   int dev = 0, sms = 148;
   cudaGetDevice(&dev);
   cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  if (p.M <= kTeamTokens) {
+  // Every CTA of the int8 kernel makes bytes of all activations, which takes enough row tiles to pay.
+  // Measured (us, int8 / bf16 kernel) at 0.2, 1, 1.4, 3.5, 4.6 and 12 tiles an SM (448 x 13376, 2472 x
+  // 22560, 3232 x 12112, 8192 x 8192, 11008 x 4096, 28672 x 8192): 1 token 8.1 / 7.0, 19 / 16,
+  // 9.9 / 10.2, 13 / 16, 7.9 / 9.8, 30 / 43; 4 tokens 16 / 7.5, 34 / 17, 16 / 11, 20 / 17, 10 / 11,
+  // 38 / 45.
+  const int64_t Nt = (p.N + 15) / 16;
+  if (p.M <= kTeamTokens && 5 * Nt >= (p.M <= 2 ? 6 : 20) * static_cast<int64_t>(sms)) {
     TeamParams q;
     q.p = p;
     q.Kp = (p.Kb + 1) / 2;
-    const int64_t Nt = (p.N + 15) / 16, ctas = std::min<int64_t>(sms, Nt);
+    const int64_t ctas = std::min<int64_t>(sms, Nt);
     q.kw = team_warps(Nt, sms, q.Kp);
     const int64_t teams = ctas * (kTeamWarps / q.kw);
     q.rounds = static_cast<int>((Nt + teams - 1) / teams);

@@ -513,12 +513,15 @@ cudaError_t launch_tc(const Int4LinearArgs& a, cudaStream_t stream) {
   cudaGetDevice(&dev);
   cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   // Rounds of row blocks over the clusters, in blocks of columns per CTA, and what a round costs
-  // besides: its end, and the exchange of a cluster.
+  // besides: its end, and the exchange of a cluster. Measured, us, clusters of 1 / 2 / 4 / 8:
+  // 64 x 8192 x 8192 37 / 22 / 27 / 52, 24 x 2048 x 14336 52 / 29 / 18 / 22, 25 x 344 x 16704
+  // 65 / 36 / 23 / 15, 64 x 1024 x 1024 9.4 / 7.6 / 7.1 / 9.2.
+  constexpr double ends[4] = {3.0, 5.0, 6.0, 9.0};
   double least = 1e30;
   p.split = 1;
   for (int split = 1; split <= 8 && split <= p.Kb; split *= 2) {
-    const int clusters = sms / split, rounds = (p.row_blocks + clusters - 1) / clusters;
-    const double cost = rounds * ((p.Kb + split - 1) / split + (split > 1 ? 6.0 : 3.0));
+    const int clusters = cluster_slots(sms, split), rounds = (p.row_blocks + clusters - 1) / clusters;
+    const double cost = rounds * ((p.Kb + split - 1) / split + ends[split / 2 - split / 8]);
     if (cost < least) least = cost, p.split = split;
   }
   while ((1 << p.log_split) < p.split) ++p.log_split;
@@ -529,7 +532,7 @@ cudaError_t launch_tc(const Int4LinearArgs& a, cudaStream_t stream) {
   auto kernel = int4_tc_kernel<TOKENS, G, ASYM>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
-  const int clusters = std::min(sms / p.split, p.row_blocks);
+  const int clusters = std::min(cluster_slots(sms, p.split), p.row_blocks);
   return launch_kernel_clustered(kernel, dim3(static_cast<unsigned>(clusters * p.split)), dim3(C::kThreads), C::kSmem,
                                  stream, true, static_cast<unsigned>(p.split), map, p);
 }
