@@ -425,17 +425,19 @@ __global__ void __launch_bounds__(S::WARPS * 32, 1) paged_attention_kernel(const
             for (int j = 0; j < kWords; ++j)
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
-                const int v[4] = {__float2int_rn(bf16_lo(w[j][h].x) * mul), __float2int_rn(bf16_hi(w[j][h].x) * mul),
-                                  __float2int_rn(bf16_lo(w[j][h].y) * mul), __float2int_rn(bf16_hi(w[j][h].y) * mul)};
-                int a[4], b[4];
+                // round to an integer in the low mantissa bits (1.5 * 2^23 added), then bytes with
+                // carries: the three low bytes of v + 0x808080, each less 128, are the signed digits
+                constexpr uint32_t kShift = 0x00808080u - 0x4B400000u;
+                const uint32_t v[4] = {__float_as_uint(__fmaf_rn(bf16_lo(w[j][h].x), mul, 12582912.0f)) + kShift,
+                                       __float_as_uint(__fmaf_rn(bf16_hi(w[j][h].x), mul, 12582912.0f)) + kShift,
+                                       __float_as_uint(__fmaf_rn(bf16_lo(w[j][h].y), mul, 12582912.0f)) + kShift,
+                                       __float_as_uint(__fmaf_rn(bf16_hi(w[j][h].y), mul, 12582912.0f)) + kShift};
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  b[e] = (v[e] - static_cast<int8_t>(v[e])) >> 8;
-                  a[e] = (b[e] - static_cast<int8_t>(b[e])) >> 8;
+                for (int d = 0; d < 3; ++d) {
+                  const uint32_t pick = d == 0 ? 0x0062u : d == 1 ? 0x0051u : 0x0040u;
+                  qf[nt][d == 0 ? 0 : d == 1 ? kParts / 2 : kParts - 1][j][h] =
+                      __byte_perm(__byte_perm(v[0], v[1], pick), __byte_perm(v[2], v[3], pick), 0x5410) ^ 0x80808080u;
                 }
-                qf[nt][0][j][h] = rows::pack4(a[0], a[1], a[2], a[3]);
-                qf[nt][kParts / 2][j][h] = rows::pack4(b[0], b[1], b[2], b[3]);
-                qf[nt][kParts - 1][j][h] = rows::pack4(v[0], v[1], v[2], v[3]);
               }
             const float back =
                 top < 0x7F80u ? p.scale * __uint_as_float(static_cast<uint32_t>(127 - up) << 23) : NAN;
