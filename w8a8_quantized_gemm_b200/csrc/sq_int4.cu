@@ -14,7 +14,6 @@
 
 #include <algorithm>
 #include <cfloat>
-#include <cmath>
 
 namespace sq {
 namespace {
@@ -860,10 +859,10 @@ cudaError_t launch_wide(const LinearParams& p, int sms, unsigned int* status, cu
   q.status = status;
   const int64_t Nt = (p.N + 15) / 16;
   // The shape of the launch by its estimated time in us, fitted to about 100 measured ones (34 sizes,
-  // 1 to 16 tokens; 9% off in the root mean square): a warp alone takes 0.46 for a pair of blocks, all
-  // warps of an SM together 0.106 a pair, and between the two a smooth maximum; the activations come at
-  // 75 KB a us, a chunk of them costs 0.25 where chunks take turns, a round of tiles 0.77, a cluster
-  // of two 1.3 and of four 4 (of eight more than it saves).
+  // 1 to 16 tokens; 9% off in the root mean square): a warp alone takes 0.41 for a pair of blocks, all
+  // warps of an SM together 0.098 a pair, the larger of the two sums and 0.28 of the smaller count;
+  // the activations come at 74 KB a us, a chunk of them costs 0.26 where chunks take turns, a round
+  // of tiles 0.74, a cluster of two 1.3 and of four 4 (of eight more than it saves).
   double least = 1e30;
   size_t smem = 0;
   for (int split = 1; split <= 4 && split <= q.Kp; split *= 2) {
@@ -872,10 +871,10 @@ cudaError_t launch_wide(const LinearParams& p, int sms, unsigned int* status, cu
     for (int kw = 1; kw <= W && kw <= pairs; ++kw) {
       const int64_t teams = W / kw, rounds = (tiles + teams - 1) / teams;
       const double x_kb = 0.5 * static_cast<double>(rounds) * pairs * p.M;
-      const double alone = 0.46 * static_cast<double>(rounds) * ((pairs + kw - 1) / kw);
-      const double together = 0.106 * static_cast<double>(tiles) * pairs;
-      const double base = std::cbrt(alone * alone * alone + together * together * together) + x_kb / 75 +
-                          0.77 * static_cast<double>(rounds) + (split == 4 ? 4.0 : split == 2 ? 1.3 : 0.0);
+      const double alone = 0.41 * static_cast<double>(rounds) * ((pairs + kw - 1) / kw);
+      const double together = 0.098 * static_cast<double>(tiles) * pairs;
+      const double base = std::max(alone, together) + 0.28 * std::min(alone, together) + x_kb / 74 +
+                          0.74 * static_cast<double>(rounds) + (split == 4 ? 4.0 : split == 2 ? 1.3 : 0.0);
       if (base >= least) continue;
       // the largest chunks, up to all columns, that leave three slots for every ring
       const int64_t room = kSmemMax - 1024 - static_cast<int64_t>(W) * p.M * 64;
@@ -888,7 +887,7 @@ cudaError_t launch_wide(const LinearParams& p, int sms, unsigned int* status, cu
           all = (left / 2 / p.M - 16) / row / kw * kw;
         }
         if (all < kw || (ring > 2 && buffers == 2 && all * p.M < 64)) continue;
-        const double turns = buffers == 2 ? 0.25 * static_cast<double>(rounds) * ((pairs + all - 1) / all) : 0.0;
+        const double turns = buffers == 2 ? 0.26 * static_cast<double>(rounds) * ((pairs + all - 1) / all) : 0.0;
         if (base + turns >= least) break;
         least = base + turns;
         q.split = split;
