@@ -436,7 +436,8 @@ typedef struct {
  * stay. Queries are written to q_out, keys and values to slot slots[t] of the cache: as bf16
  * (rounded once), or as int8 from the fp32 values of one head's row:
  *   a = max |y|, scale = a / 127, code = clamp(rne(y * min(127 / a, FLT_MAX)), -128, 127)
- * (IEEE divisions; a == 0 gives codes and scale 0).
+ * (IEEE divisions; a == 0 gives codes and scale 0; a row with a NaN or an infinity gets that as
+ * its scale, and codes without meaning).
  * q: bf16 [T, H, head_dim], k, v: bf16 [T, heads, head_dim]: token strides ldq, ldk, ldv in
  * elements (multiples of 8, at least a token's row), heads and elements dense. q and q_out may
  * both be NULL (H = 0). q_out: bf16 [T, H, head_dim] dense; it may be q itself when ldq is
@@ -473,9 +474,10 @@ SQ_API sq_status sq_rope_kv_append(const void* q_bf16, int64_t ldq, const void* 
  * out: bf16 [B, H, head_dim] dense. lse: fp32 [B, H] or NULL. 1 <= B <= 65535.
  * A page index out of range hides its tokens, a negative length counts as 0 and one past
  * max_pages * page_size as that; each records SQ_ERR_BOUNDS (see sq_sync_status).
- * ws: sq_workspace_size(SQ_OP_PAGED_ATTENTION, B, H, head_dim) bytes, 16-byte aligned,
- * zero-filled before its first use; every completed call leaves its counters at zero again.
- * Calls that share one ws must not overlap on the GPU.
+ * ws: at least sq_workspace_size(SQ_OP_PAGED_ATTENTION, B, H, head_dim) bytes, 16-byte aligned,
+ * zero-filled before its first use; every completed call leaves its counters at zero again, so
+ * one ws of the largest B * H serves calls of any shape one after another. Calls that share one
+ * ws must not overlap on the GPU.
  */
 SQ_API sq_status sq_paged_attention(const void* q_bf16, int64_t ldq, int64_t B, int64_t H, const sq_kv_cache* cache,
                                     const int32_t* block_table, int64_t ld_table, int64_t max_pages,

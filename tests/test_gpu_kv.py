@@ -391,6 +391,45 @@ def test_decode_loop(int8):
         _check_attention(out, lse, ref, D, max(now))
 
 
+def test_one_workspace_for_calls_of_any_shape():
+    """The counters of a large batch lie where an earlier call of another shape, head dimension or
+    cache type left none of its partial sums: one workspace, sized for the largest."""
+    rng = np.random.default_rng(21)
+    ws = sq.workspace(sq.SQ_OP_PAGED_ATTENTION, 300, 64, 64)
+    for B, H, heads, D, n, int8 in [(1, 8, 1, 256, 3000, False), (300, 64, 32, 64, 40, True), (2, 32, 8, 128, 2500, True),
+                                    (300, 8, 2, 96, 70, False), (1, 64, 4, 256, 4000, True), (260, 64, 64, 64, 17, False)]:
+        cache, (k, v) = _filled(rng, 200, heads, 16, D, int8)
+        lens = [max(1, n - 7 * (b % 5)) for b in range(B)]
+        table = rng.integers(0, 200, (B, -(-n // 16))).astype(np.int32)
+        q = _bits(rng, B, H, D)
+        out, lse = _attend(dev_bf16(q), cache, torch.from_numpy(table).cuda(),
+                           torch.tensor(lens, dtype=torch.int32).cuda(), D ** -0.5, ws=ws)
+        sq.sq_sync_status()
+        ref = osv.paged_attention(wl.bf16_bits_to_f32(q).astype(np.float64), k, v, table, lens, D ** -0.5)
+        _check_attention(out, lse, ref, D, n)
+
+
+def test_nonfinite_keys_and_values_show_in_an_int8_cache():
+    """A NaN or an infinity in an appended row is kept as its scale: attention over that token gives
+    NaN for the key head's queries and for no others."""
+    x = torch.randn(3, 2, 64, device="cuda").to(torch.bfloat16)
+    bad_k, bad_v = x.clone(), x.clone()
+    bad_k[1, 0, 5] = float("nan")
+    bad_v[2, 1, 63] = float("inf")
+    cache = _new_cache(1, 2, 16, 64, True)
+    idx = torch.arange(3, dtype=torch.int32, device="cuda")
+    sq.sq_rope_kv_append(None, bad_k, bad_v, None, None, None, idx, cache, None)
+    ks, vs = cache.tensors[2][0, :, :3], cache.tensors[3][0, :, :3]
+    assert bool(torch.isnan(ks[0, 1])) and int(torch.isfinite(ks).sum()) == 5
+    assert bool(torch.isinf(vs[1, 2])) and int(torch.isfinite(vs).sum()) == 5
+    q = torch.randn(1, 4, 64, device="cuda").to(torch.bfloat16)
+    for n, finite in ((1, [True] * 4), (2, [False, False, True, True]), (3, [False] * 4)):
+        out, _ = _attend(q, cache, torch.zeros(1, 1, dtype=torch.int32, device="cuda"),
+                         torch.tensor([n], dtype=torch.int32, device="cuda"), 0.125)
+        assert [bool(torch.isfinite(out[0, h]).all()) for h in range(4)] == finite
+    sq.sq_sync_status()
+
+
 def test_two_streams_with_their_own_workspaces():
     rng = np.random.default_rng(12)
     cache, (k, v) = _filled(rng, 200, 2, 16, 128, True)

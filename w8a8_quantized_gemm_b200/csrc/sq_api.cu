@@ -738,7 +738,7 @@ size_t sq_workspace_size(int op, int64_t M, int64_t N, int64_t K) {
     case SQ_OP_ABS_PERCENTILE:
       return sq::abs_percentile_workspace_bytes();
     case SQ_OP_PAGED_ATTENTION:
-      return (M < 1 || N < 1 || K < 1) ? 0 : sq::paged_attention_workspace_bytes(M, N, K);
+      return (M < 1 || N < 1 || K < 1) ? 0 : sq::paged_attention_workspace_bytes(M, N);
     default:
       return 0;
   }

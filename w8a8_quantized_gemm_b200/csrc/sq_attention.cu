@@ -866,8 +866,6 @@ int cta_count() {
   return std::min(sms, kMaxCtas);
 }
 
-size_t round256(size_t v) { return (v + 255) & ~size_t(255); }
-
 template <typename S>
 cudaError_t launch_shape(AttnParams p, cudaStream_t stream) {
   p.blocks = (p.group + S::kHeads - 1) / S::kHeads;
@@ -880,10 +878,13 @@ cudaError_t launch_shape(AttnParams p, cudaStream_t stream) {
 
 }  // namespace
 
-// Arrival counters (at most one per query head), then two parts per CTA of up to 16 heads.
-size_t paged_attention_workspace_bytes(int64_t B, int64_t H, int64_t D) {
-  return round256(static_cast<size_t>(B) * static_cast<size_t>(H) * 4) +
-         static_cast<size_t>(kMaxCtas) * 2 * 16 * (static_cast<size_t>(D) + 2) * 4;
+// Two parts per CTA of up to 16 heads of up to 256, then the arrival counters (at most one per query
+// head): at the same place whatever the shape, so that calls of different shapes, one after another
+// on one workspace, find the counters at zero.
+constexpr size_t kPartsBytes = static_cast<size_t>(kMaxCtas) * 2 * 16 * (256 + 2) * 4;
+
+size_t paged_attention_workspace_bytes(int64_t B, int64_t H) {
+  return kPartsBytes + static_cast<size_t>(B) * static_cast<size_t>(H) * 4;
 }
 
 cudaError_t launch_paged_attention(const PagedAttentionArgs& a, cudaStream_t stream) {
@@ -902,8 +903,8 @@ cudaError_t launch_paged_attention(const PagedAttentionArgs& a, cudaStream_t str
   p.scale = a.scale * 1.44269504088896341f;
   p.out = a.out;
   p.lse = a.lse;
-  p.counters = static_cast<unsigned*>(a.ws);
-  p.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(a.ws) + round256(static_cast<size_t>(a.B) * a.H * 4));
+  p.parts = static_cast<float*>(a.ws);
+  p.counters = reinterpret_cast<unsigned*>(static_cast<uint8_t*>(a.ws) + kPartsBytes);
   p.status = a.status;
   p.group = static_cast<int>(a.H) / a.cache.heads;
   // 16 query heads at a time where a key head has more than 8: keys and values are read half as

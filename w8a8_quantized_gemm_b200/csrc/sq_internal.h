@@ -257,7 +257,7 @@ struct PagedAttentionArgs {
   void* ws = nullptr;
   unsigned int* status = nullptr;
 };
-size_t paged_attention_workspace_bytes(int64_t B, int64_t H, int64_t D);
+size_t paged_attention_workspace_bytes(int64_t B, int64_t H);
 cudaError_t launch_paged_attention(const PagedAttentionArgs& a, cudaStream_t stream);
 
 }  // namespace sq

@@ -17,6 +17,13 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&r);
 }
 
+// The larger one, or NaN: a row with a NaN gets a scale that says so.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
 // ---------------------------------------------------------------- append
 // 128 threads and at most 72 registers: seven CTAs an SM. Measured (us; 8192 tokens of 64 + 16 heads of
 // 128, int8; 2047 tokens of 32 + 64 heads, bf16): 256 threads 88 / 25, 128 threads 69 / 21, held to 72
@@ -108,8 +115,8 @@ rope_kv_append_kernel(const uint16_t* q, int64_t ldq, const uint16_t* __restrict
     } else {
       float a = 0.0f;
 #pragma unroll
-      for (int j = 0; j < 16; ++j) a = fmaxf(a, fabsf(x[j]));
-      for (int o = lanes / 2; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(quad, a, o));
+      for (int j = 0; j < 16; ++j) a = max_nan(a, fabsf(x[j]));
+      for (int o = lanes / 2; o > 0; o >>= 1) a = max_nan(a, __shfl_xor_sync(quad, a, o));
       const float r = a > 0.0f ? fminf(__fdiv_rn(127.0f, a), FLT_MAX) : 0.0f;
       const int64_t at = (static_cast<int64_t>(head) << c.page_shift) + off;
       int8_t* dst = static_cast<int8_t*>(is_v ? c.v : c.k) + page * c.page_stride + at * D;
@@ -139,8 +146,8 @@ cudaError_t launch_rope_kv_append(const RopeAppendArgs& a, cudaStream_t stream) 
   auto kernel = rope_kv_append_kernel<false, false>;
   if (a.cache.int8) kernel = a.interleaved ? rope_kv_append_kernel<true, true> : rope_kv_append_kernel<true, false>;
   else if (a.interleaved) kernel = rope_kv_append_kernel<false, true>;
-  return launch_kernel(kernel, dim3(static_cast<unsigned>((a.T + tokens - 1) / tokens)), dim3(kAppendThreads), 0, stream,
-                       true, a.q, a.ldq, a.k, a.ldk, a.v, a.ldv, a.T, a.H, a.cos_t, a.sin_t, a.max_pos, a.rot,
+  const dim3 grid(static_cast<unsigned>((a.T + tokens - 1) / tokens));
+  return launch_kernel(kernel, grid, dim3(kAppendThreads), 0, stream, true, a.q, a.ldq, a.k, a.ldk, a.v, a.ldv, a.T, a.H, a.cos_t, a.sin_t, a.max_pos, a.rot,
                        a.positions, a.slots, a.cache, a.q_out, lanes, per, a.status);
 }
 
