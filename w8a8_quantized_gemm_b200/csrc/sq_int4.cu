@@ -350,6 +350,18 @@ __global__ void __launch_bounds__(kTeamWarps * 32, 1) int4_team_kernel(const Tea
   constexpr int kScaleLanes = kGroups * kLanesPerGroup;
   const int e_group = lane / kLanesPerGroup, e_row = lane % kLanesPerGroup * (kScaleBytes / 2);
   const int z_group = lane / 4, z_row = lane % 4 * 4;
+  const int64_t e_step = static_cast<int64_t>(q.kw) * kGroups * p.N;
+  const uint16_t* e_src;  // this lane's scales of pair load_kp, there in pairs before e_end
+  const uint8_t* z_src = nullptr;  // and zero points, before z_end
+  int e_end, z_end;
+  auto locate = [&]() {  // in the tile load_rt from pair load_kp on
+    const int64_t e_n = static_cast<int64_t>(load_rt) * 16 + e_row, z_n = static_cast<int64_t>(load_rt) * 16 + z_row;
+    e_src = p.scale + static_cast<int64_t>(load_kp * kGroups + e_group) * p.N + e_n;
+    if (ASYM) z_src = p.zero + static_cast<int64_t>(load_kp * kGroups + z_group) * p.N + z_n;
+    e_end = e_n < p.N ? (p.groups - e_group + kGroups - 1) / kGroups : 0;
+    z_end = z_n < p.N ? (p.groups - z_group + kGroups - 1) / kGroups : 0;
+  };
+  locate();
   auto fetch = [&](int slot) {
     if (load_rt < Nt) {
       const uint32_t dst = ring32 + slot * kSlot;
@@ -359,21 +371,22 @@ __global__ void __launch_bounds__(kTeamWarps * 32, 1) int4_team_kernel(const Tea
       cp_async<16>(dst + 1024 + lane * 16, load_src + (second ? 1024 : 0), second);
       cp_async<16>(dst + 1536 + lane * 16, load_src + (second ? 1536 : 0), second);
       if (lane < kScaleLanes) {
-        const int gr = load_kp * kGroups + e_group, n = load_rt * 16 + e_row;
-        const bool in = gr < p.groups && n < p.N;
-        cp_async<kScaleBytes>(dst + kScales + lane * kScaleBytes, p.scale + (in ? gr * p.N + n : 0), in);
+        const bool in = load_kp < e_end;
+        cp_async<kScaleBytes>(dst + kScales + lane * kScaleBytes, in ? e_src : p.scale, in);
       }
       if (ASYM && lane < 4 * kGroups) {
-        const int gr = load_kp * kGroups + z_group, n = load_rt * 16 + z_row;
-        const bool in = gr < p.groups && n < p.N;
-        cp_async<4>(dst + kZeros + lane * 4, p.zero + (in ? gr * p.N + n : 0), in);
+        const bool in = load_kp < z_end;
+        cp_async<4>(dst + kZeros + lane * 4, in ? z_src : p.zero, in);
       }
       load_kp += q.kw;
       load_src += 2 * q.kw * kTileBytes;
+      e_src += e_step;
+      if (ASYM) z_src += e_step;
       if (load_kp >= q.Kp) {  // on to the team's next tile
         load_src += tile_jump - static_cast<int64_t>(load_kp - kw) * 2 * kTileBytes;
         load_kp = kw;
         load_rt += step;
+        locate();
       }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
@@ -675,6 +688,18 @@ __global__ void __launch_bounds__(kTeamWarps * 32, 1) int4_wide_kernel(const Wid
   constexpr int kScaleLanes = kGroups * kLanesPerGroup;
   const int e_group = lane / kLanesPerGroup, e_row = lane % kLanesPerGroup * (kScaleBytes / 2);
   const int z_group = lane / 4, z_row = lane % 4 * 4;
+  const int64_t e_step = static_cast<int64_t>(q.kw) * kGroups * p.N;
+  const uint16_t* e_src;  // this lane's scales of pair load_kp, there in pairs before e_end
+  const uint8_t* z_src = nullptr;  // and zero points, before z_end
+  int e_end, z_end;
+  auto locate = [&]() {  // in the tile load_rt from pair load_kp on
+    const int64_t e_n = static_cast<int64_t>(load_rt) * 16 + e_row, z_n = static_cast<int64_t>(load_rt) * 16 + z_row;
+    e_src = p.scale + static_cast<int64_t>(load_kp * kGroups + e_group) * p.N + e_n;
+    if (ASYM) z_src = p.zero + static_cast<int64_t>(load_kp * kGroups + z_group) * p.N + z_n;
+    e_end = e_n < p.N ? (p.groups - e_group + kGroups - 1) / kGroups : 0;
+    z_end = z_n < p.N ? (p.groups - z_group + kGroups - 1) / kGroups : 0;
+  };
+  locate();
   auto fetch = [&](int slot) {
     if (load_rt < Nt) {
       const uint32_t dst = ring32 + slot * kSlot;
@@ -684,21 +709,22 @@ __global__ void __launch_bounds__(kTeamWarps * 32, 1) int4_wide_kernel(const Wid
       cp_async<16>(dst + 1024 + lane * 16, load_src + (second ? 1024 : 0), second);
       cp_async<16>(dst + 1536 + lane * 16, load_src + (second ? 1536 : 0), second);
       if (lane < kScaleLanes) {
-        const int gr = load_kp * kGroups + e_group, n = load_rt * 16 + e_row;
-        const bool in = gr < p.groups && n < p.N;
-        cp_async<kScaleBytes>(dst + kScales + lane * kScaleBytes, p.scale + (in ? gr * p.N + n : 0), in);
+        const bool in = load_kp < e_end;
+        cp_async<kScaleBytes>(dst + kScales + lane * kScaleBytes, in ? e_src : p.scale, in);
       }
       if (ASYM && lane < 4 * kGroups) {
-        const int gr = load_kp * kGroups + z_group, n = load_rt * 16 + z_row;
-        const bool in = gr < p.groups && n < p.N;
-        cp_async<4>(dst + kZeros + lane * 4, p.zero + (in ? gr * p.N + n : 0), in);
+        const bool in = load_kp < z_end;
+        cp_async<4>(dst + kZeros + lane * 4, in ? z_src : p.zero, in);
       }
       load_kp += q.kw;
       load_src += 2 * q.kw * kTileBytes;
+      e_src += e_step;
+      if (ASYM) z_src += e_step;
       if (load_kp >= kp1) {
         load_src += tile_jump - static_cast<int64_t>(load_kp - kp0 - kw) * 2 * kTileBytes;
         load_kp = kp0 + kw;
         load_rt += step;
+        locate();
       }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
