@@ -1010,7 +1010,7 @@ cudaError_t launch_int4_dequant(const uint8_t* Wp, const uint16_t* scale, const 
 }
 
 cudaError_t launch_int4_linear(const Int4LinearArgs& a, cudaStream_t stream) {
-  // Measured (us; these kernels / tcgen05): 8 x 28672 x 8192 44 / 58, 16 x 28672 x 8192 57 / 58,
+  // Measured (us; these kernels / tcgen05): 8 x 28672 x 8192 43 / 58, 16 x 28672 x 8192 55 / 58,
   // 16 x 11008 x 4096 15 / 17, 32 x 28672 x 8192 79 / 63, 64 x 4096 x 4096 45 / 12
   if (a.M > 16) return launch_int4_linear_tc(a, stream);
   LinearParams p{};

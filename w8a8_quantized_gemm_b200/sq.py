@@ -309,20 +309,34 @@ def sq_weight_row_sums(Wq, rowsum, stream=None):
 
 # ---------------------------------------------------------------- 4-bit weights
 # These calls run once per layer and token, so their checks are kept to a few microseconds.
+_cuda_calls = None
+
+
+def _cuda():
+    """torch, and its calls for the current device and stream (the stream's handle, without making
+    a Stream object for it, where torch has that), looked up once."""
+    global _cuda_calls
+    if _cuda_calls is None:
+        torch = _torch()
+        _cuda_calls = (torch, getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device),
+                       getattr(torch._C, "_cuda_getCurrentRawStream", None))
+    return _cuda_calls
+
+
 def _device(t, name):
     """Device index of a CUDA tensor, which must be the current device: the library launches there."""
-    torch = _torch()
+    torch, current, _ = _cuda()
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     dev = t.get_device()
-    if dev != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {t.device}, but the current device is cuda:{torch.cuda.current_device()}")
+    if dev != current():
+        raise ValueError(f"{name} is on {t.device}, but the current device is cuda:{current()}")
     return dev
 
 
 def _on(stream, dev):
-    """The handle of `stream`, or of the current one (without making a Stream object for it)."""
-    raw = getattr(_torch()._C, "_cuda_getCurrentRawStream", None)
+    """The handle of `stream`, or of the current one."""
+    raw = _cuda()[2]
     return raw(dev) if stream is None and raw is not None else _stream(stream)
 
 
@@ -337,20 +351,30 @@ def _dense(t, dtype, shape, name, dev):
     """Data pointer of a contiguous tensor of exactly this type and shape (None passes)."""
     if t is None:
         return None
-    _typed(t, dtype, name, dev)
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if not t.is_contiguous():
+    if t.dtype is not dtype or t.get_device() != dev or t.shape != shape or not t.is_contiguous():
+        _typed(t, dtype, name, dev)
+        if t.shape != shape:
+            raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
         raise ValueError(f"{name} must be contiguous")
     return t.data_ptr()
+
+
+def _rows(t, dtype, name):
+    """(data pointer, rows, columns, row stride) of a 2-D tensor with unit column stride."""
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    stride = t.stride()
+    if len(stride) != 2 or stride[1] != 1:
+        raise ValueError(f"{name} must be 2-D with unit column stride")
+    rows, columns = t.shape
+    return t.data_ptr(), rows, columns, stride[0]
 
 
 def sq_int4_weight_bytes(N: int, K: int) -> int:
     return int(_lib.sq_int4_weight_bytes(int(N), int(K)))
 
 
-def _int4(Wp, w_scale, w_zero, group, N, K, dev):
-    torch = _torch()
+def _int4(torch, Wp, w_scale, w_zero, group, N, K, dev):
     groups = (-(-K // group) if group > 0 else 0, N)
     return (_dense(Wp, torch.uint8, (-(-N // 16) * -(-K // 128) * 1024,), "Wp", dev),
             _dense(w_scale, torch.bfloat16, groups, "w_scale", dev), _dense(w_zero, torch.uint8, groups, "w_zero", dev))
@@ -358,36 +382,34 @@ def _int4(Wp, w_scale, w_zero, group, N, K, dev):
 
 def sq_quant_weight_int4(W, s, group: int, Wp, w_scale, w_zero=None, stream=None):
     """4-bit codes and group scales of W [N, K] (times s); with w_zero, zero points too."""
-    torch = _torch()
+    torch = _cuda()[0]
     dev = _device(W, "W")
-    w = _ptr(W, torch.bfloat16, "W", True)
-    N, K = W.shape
-    p, e, z = _int4(Wp, w_scale, w_zero, group, N, K, dev)
-    _check(_lib.sq_quant_weight_int4(w, N, K, W.stride(0), _dense(s, torch.float32, (K,), "s", dev), group, p, e, z,
+    w, N, K, ldw = _rows(W, torch.bfloat16, "W")
+    p, e, z = _int4(torch, Wp, w_scale, w_zero, group, N, K, dev)
+    _check(_lib.sq_quant_weight_int4(w, N, K, ldw, _dense(s, torch.float32, (K,), "s", dev), group, p, e, z,
                                      _on(stream, dev)))
     return Wp, w_scale, w_zero
 
 
 def sq_dequant_weight_int4(Wp, w_scale, w_zero, group: int, out, stream=None):
     """The bf16 values [N, K] (the shape of `out`) that a 4-bit weight stands for."""
-    torch = _torch()
+    torch = _cuda()[0]
     dev = _device(out, "out")
-    o = _ptr(out, torch.bfloat16, "out")
     N, K = out.shape
-    p, e, z = _int4(Wp, w_scale, w_zero, group, N, K, dev)
+    o = _dense(out, torch.bfloat16, (N, K), "out", dev)
+    p, e, z = _int4(torch, Wp, w_scale, w_zero, group, N, K, dev)
     _check(_lib.sq_dequant_weight_int4(p, e, z, group, N, K, o, _on(stream, dev)))
     return out
 
 
 def sq_int4_linear(X, Wp, w_scale, w_zero, group: int, bias, Y, stream=None):
     """Y [M, N] = X [M, K] times the 4-bit weight, plus bias; M <= 64."""
-    torch = _torch()
+    torch = _cuda()[0]
     dev = _device(X, "X")
-    x = _ptr(X, torch.bfloat16, "X", True)
-    M, K = X.shape
+    x, M, K, ldx = _rows(X, torch.bfloat16, "X")
     N = Y.shape[-1]
-    p, e, z = _int4(Wp, w_scale, w_zero, group, N, K, dev)
-    _check(_lib.sq_int4_linear(x, M, K, X.stride(0), p, e, z, group, _dense(bias, torch.bfloat16, (N,), "bias", dev),
+    p, e, z = _int4(torch, Wp, w_scale, w_zero, group, N, K, dev)
+    _check(_lib.sq_int4_linear(x, M, K, ldx, p, e, z, group, _dense(bias, torch.bfloat16, (N,), "bias", dev),
                                _dense(Y, torch.bfloat16, (M, N), "Y", dev), N, _on(stream, dev)))
     return Y
 
@@ -440,9 +462,10 @@ class KvCache:
         self.ref = C.addressof(self.struct)
 
 
-def _heads(t, heads, dim, name, dev):
+def _heads(t, bf16, heads, dim, name, dev):
     """(data pointer, token stride) of a bf16 [tokens, heads, dim] tensor dense within a token."""
-    _typed(t, _torch().bfloat16, name, dev)
+    if t.dtype is not bf16 or t.get_device() != dev:
+        _typed(t, bf16, name, dev)
     shape, stride = t.shape, t.stride()
     if len(shape) != 3 or shape[1] != heads or shape[2] != dim or stride[2] != 1 or (heads > 1 and stride[1] != dim):
         raise ValueError(f"{name} must be [tokens, {heads}, {dim}], dense within a token")
@@ -453,13 +476,13 @@ def sq_rope_kv_append(q, k, v, cos, sin, positions, slots, cache: KvCache, q_out
                       stream=None):
     """Rotate q and k by position, write q_out, append k and v to the cache's slots. q and q_out
     may be None; cos, sin [max_pos, rot_dim / 2] and positions may be None (no rotation)."""
-    torch = _torch()
+    torch = _cuda()[0]
     dev = _device(k, "k")
     if dev != cache.device:
         raise ValueError(f"cache on cuda:{cache.device}, k on cuda:{dev}")
     heads, D = cache.heads, cache.head_dim
-    kp, ldk = _heads(k, heads, D, "k", dev)
-    vp, ldv = _heads(v, heads, D, "v", dev)
+    kp, ldk = _heads(k, torch.bfloat16, heads, D, "k", dev)
+    vp, ldv = _heads(v, torch.bfloat16, heads, D, "v", dev)
     T = k.shape[0]
     if (q is None) != (q_out is None):
         raise ValueError("q and q_out must be given together")
@@ -468,7 +491,7 @@ def sq_rope_kv_append(q, k, v, cos, sin, positions, slots, cache: KvCache, q_out
     H, qp, ldq, op = 0, None, 0, None
     if q is not None:
         H = q.shape[1]
-        qp, ldq = _heads(q, H, D, "q", dev)
+        qp, ldq = _heads(q, torch.bfloat16, H, D, "q", dev)
         op = _dense(q_out, torch.bfloat16, (T, H, D), "q_out", dev)
     if v.shape[0] != T or (q is not None and q.shape[0] != T):
         raise ValueError("q, k and v must have the same number of tokens")
@@ -487,14 +510,14 @@ def sq_rope_kv_append(q, k, v, cos, sin, positions, slots, cache: KvCache, q_out
 def sq_paged_attention(q, cache: KvCache, block_table, seq_lens, scale: float, out, lse=None, window: int = 0, ws=None,
                        stream=None):
     """out [B, H, D]: attention of one token per sequence over the cache; lse [B, H] fp32 too."""
-    torch = _torch()
+    torch = _cuda()[0]
     dev = _device(q, "q")
     if dev != cache.device:
         raise ValueError(f"cache on cuda:{cache.device}, q on cuda:{dev}")
     if q.dim() != 3:
         raise ValueError("q must be [sequences, heads, head_dim]")
     B, H, D = q.shape
-    qp, ldq = _heads(q, H, cache.head_dim, "q", dev)
+    qp, ldq = _heads(q, torch.bfloat16, H, cache.head_dim, "q", dev)
     _typed(block_table, torch.int32, "block_table", dev)
     shape, stride = block_table.shape, block_table.stride()
     if len(shape) != 2 or shape[0] != B or (shape[1] > 1 and stride[1] != 1):
