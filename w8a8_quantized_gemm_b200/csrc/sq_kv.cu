@@ -144,11 +144,14 @@ cudaError_t launch_rope_kv_append(const RopeAppendArgs& a, cudaStream_t stream) 
   while (per < rows && per < groups) per *= 2;
   const int64_t tokens = groups / per;
   auto kernel = rope_kv_append_kernel<false, false>;
-  if (a.cache.int8) kernel = a.interleaved ? rope_kv_append_kernel<true, true> : rope_kv_append_kernel<true, false>;
-  else if (a.interleaved) kernel = rope_kv_append_kernel<false, true>;
+  if (a.cache.int8)
+    kernel = a.interleaved ? rope_kv_append_kernel<true, true> : rope_kv_append_kernel<true, false>;
+  else if (a.interleaved)
+    kernel = rope_kv_append_kernel<false, true>;
   const dim3 grid(static_cast<unsigned>((a.T + tokens - 1) / tokens));
-  return launch_kernel(kernel, grid, dim3(kAppendThreads), 0, stream, true, a.q, a.ldq, a.k, a.ldk, a.v, a.ldv, a.T, a.H, a.cos_t, a.sin_t, a.max_pos, a.rot,
-                       a.positions, a.slots, a.cache, a.q_out, lanes, per, a.status);
+  return launch_kernel(kernel, grid, dim3(kAppendThreads), 0, stream, true, a.q, a.ldq, a.k, a.ldk, a.v, a.ldv, a.T,
+                       a.H, a.cos_t, a.sin_t, a.max_pos, a.rot, a.positions, a.slots, a.cache, a.q_out, lanes, per,
+                       a.status);
 }
 
 }  // namespace sq
