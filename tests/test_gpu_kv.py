@@ -391,6 +391,26 @@ def test_decode_loop(int8):
         _check_attention(out, lse, ref, D, max(now))
 
 
+@pytest.mark.parametrize("int8", [False, True])
+@pytest.mark.parametrize("B,longest,holes", [(33, 200, False), (1000, 40, True), (2500, 20, True), (5000, 3, False)])
+def test_attention_many_sequences(B, longest, holes, int8):
+    """More sequences than lanes, and than lanes squared, with empty ones among them, long runs of
+    them and at both ends."""
+    rng = np.random.default_rng(B)
+    H, heads, D, P = 2, 1, 64, 8
+    cache, (k, v) = _filled(rng, 100, heads, P, D, int8)
+    lens = rng.integers(0 if holes else 1, longest + 1, B)
+    if holes:
+        lens[:40] = lens[-70:] = lens[B // 2:B // 2 + 100] = 0
+    table = rng.integers(0, 100, (B, -(-longest // P))).astype(np.int32)
+    q = _bits(rng, B, H, D)
+    out, lse = _attend(dev_bf16(q), cache, torch.from_numpy(table).cuda(), torch.from_numpy(lens.astype(np.int32)).cuda(),
+                       D ** -0.5)
+    sq.sq_sync_status()
+    ref = osv.paged_attention(wl.bf16_bits_to_f32(q).astype(np.float64), k, v, table, list(lens), D ** -0.5)
+    _check_attention(out, lse, ref, D, longest)
+
+
 def test_one_workspace_for_calls_of_any_shape():
     """The counters of a large batch lie where an earlier call of another shape, head dimension or
     cache type left none of its partial sums: one workspace, sized for the largest."""

@@ -206,21 +206,18 @@ __device__ __forceinline__ int64_t divide(int64_t a, int64_t b) {
   return a / b;
 }
 
-// Sum over the warp of a 64-bit count.
-__device__ __forceinline__ int64_t warp_sum(int64_t v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
-}
-
-// 32 sequences, one a lane: their ranges, tiles (of all units) and the tiles up to each's end.
+// The tiles (of all units) of `count` sequences a lane from `first` on, and up to the lane's end;
+// the range of the last one.
 template <typename S>
 struct Scan {
   Range r;
   int64_t n, upto;
-  __device__ __forceinline__ Scan(const AttnParams& p, int units, int b0, int lane) : r{} {
-    if (b0 + lane < p.B) r = range_of<S>(p, b0 + lane);
-    n = static_cast<int64_t>(r.last - r.first) * units;
+  __device__ __forceinline__ Scan(const AttnParams& p, int units, int first, int count, int lane) : r{}, n(0) {
+#pragma unroll 4
+    for (int b = first; b < min(first + count, p.B); ++b) {
+      r = range_of<S>(p, b);
+      n += static_cast<int64_t>(r.last - r.first) * units;
+    }
     upto = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -230,34 +227,40 @@ struct Scan {
   }
 };
 
-// The place `at` (< the number of tiles) as a cursor: prefix sums over 32 sequences at a time,
-// the first of which the caller has.
+// The place `at` (< the number of tiles) as a cursor, from a scan of `each` sequences a lane: the
+// lane's, then the sequence among the lane's.
 template <typename S>
-__device__ __forceinline__ Cursor<S> cursor_at(const AttnParams& p, int units, Scan<S> s, int64_t at, int lane) {
+__device__ __forceinline__ Cursor<S> cursor_at(const AttnParams& p, int units, const Scan<S>& scan, int each,
+                                               int64_t at, int lane) {
   Cursor<S> c;
-  int64_t base = 0;
-  for (int b0 = 0;;) {
-    const unsigned past = __ballot_sync(0xffffffffu, at < base + s.upto);
+  int src = __ffs(__ballot_sync(0xffffffffu, at < scan.upto)) - 1;
+  int64_t start = __shfl_sync(0xffffffffu, scan.upto - scan.n, src);
+  Range r = scan.r;
+  c.b = src * each;
+  while (each > 1) {
+    const Scan<S> s(p, units, c.b + lane, 1, lane);
+    const unsigned past = __ballot_sync(0xffffffffu, at < start + s.upto);
     if (past != 0) {
-      const int src = __ffs(past) - 1;
-      const int64_t start = base + __shfl_sync(0xffffffffu, s.upto - s.n, src);
-      c.b = b0 + src;
-      c.r.lo = __shfl_sync(0xffffffffu, s.r.lo, src);
-      c.r.len = __shfl_sync(0xffffffffu, s.r.len, src);
-      c.r.first = __shfl_sync(0xffffffffu, s.r.first, src);
-      c.r.last = __shfl_sync(0xffffffffu, s.r.last, src);
-      const int per = c.r.last - c.r.first;
-      const int unit = static_cast<int>(divide(at - start, per));
-      c.kvh = unit / p.blocks;
-      c.hb = unit % p.blocks;
-      c.unit_pos = start + static_cast<int64_t>(unit) * per;
-      c.tile = c.r.first + static_cast<int>(at - c.unit_pos);
-      return c;
+      src = __ffs(past) - 1;
+      start += __shfl_sync(0xffffffffu, s.upto - s.n, src);
+      r = s.r;
+      c.b += src;
+      break;
     }
-    base += __shfl_sync(0xffffffffu, s.upto, 31);
-    b0 += 32;
-    s = Scan<S>(p, units, b0, lane);
+    start += __shfl_sync(0xffffffffu, s.upto, 31);
+    c.b += 32;
   }
+  c.r.lo = __shfl_sync(0xffffffffu, r.lo, src);
+  c.r.len = __shfl_sync(0xffffffffu, r.len, src);
+  c.r.first = __shfl_sync(0xffffffffu, r.first, src);
+  c.r.last = __shfl_sync(0xffffffffu, r.last, src);
+  const int per = c.r.last - c.r.first;
+  const int unit = static_cast<int>(divide(at - start, per));
+  c.kvh = unit / p.blocks;
+  c.hb = unit % p.blocks;
+  c.unit_pos = start + static_cast<int64_t>(unit) * per;
+  c.tile = c.r.first + static_cast<int>(at - c.unit_pos);
+  return c;
 }
 
 template <typename S>
@@ -283,16 +286,9 @@ __global__ void __launch_bounds__(S::WARPS * 32, 1) paged_attention_kernel(const
   const uint32_t ring32 = smem_u32(ring);
 
   // this CTA's and this warp's piece of the line
-  const Scan<S> scan(p, units, 0, lane);
-  int64_t total = __shfl_sync(0xffffffffu, scan.upto, 31);
-  if (p.B > 32) {
-    int64_t rest = 0;
-    for (int b = lane + 32; b < p.B; b += 32) {
-      const Range r = range_of<S>(p, b);
-      rest += static_cast<int64_t>(r.last - r.first) * units;
-    }
-    total += warp_sum(rest);
-  }
+  const int each = (p.B + 31) / 32;
+  const Scan<S> scan(p, units, lane * each, each, lane);
+  const int64_t total = __shfl_sync(0xffffffffu, scan.upto, 31);
   const int64_t ctas = min(static_cast<int64_t>(gridDim.x), divide(total + W - 1, W));
   const bool works = blockIdx.x < ctas;
   const int64_t cta0 = works ? divide(total * blockIdx.x, ctas) : 0;
@@ -302,7 +298,7 @@ __global__ void __launch_bounds__(S::WARPS * 32, 1) paged_attention_kernel(const
   __syncwarp();
 
   if (p0 < p1) {
-    Cursor<S> load = cursor_at<S>(p, units, scan, p0, lane), cur = load;
+    Cursor<S> load = cursor_at<S>(p, units, scan, each, p0, lane), cur = load;
     const int n = static_cast<int>(p1 - p0);
     const int shift = p.c.page_shift;
     // page table entries win .. win + 63 of sequence win_b, one of each half per lane
