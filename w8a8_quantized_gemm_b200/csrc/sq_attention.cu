@@ -682,9 +682,7 @@ __global__ void __launch_bounds__(S::WARPS * 32, 1) paged_attention_kernel(const
   };
   // elements d .. d + 3 of head hi of a whole unit
   auto write_out = [&](int4 u, int hi, int d, float4 acc, float top, float sum) {
-    const int hl = u.w * S::kHeads + hi;
-    if (hl >= p.group) return;
-    const int64_t h = static_cast<int64_t>(u.y) * p.H + u.z * p.group + hl;
+    const int64_t h = static_cast<int64_t>(u.y) * p.H + u.z * p.group + u.w * S::kHeads + hi;
     const float inv = sum != 0.0f ? 1.0f / sum : 0.0f;
     *reinterpret_cast<uint2*>(p.out + h * D + d) =
         make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
@@ -732,25 +730,32 @@ __global__ void __launch_bounds__(S::WARPS * 32, 1) paged_attention_kernel(const
     if (mine) s_factor[lane][hi] = f, s_top[lane][hi] = top, s_sum[lane][hi] = sum;
   }
   __syncthreads();
+  auto heads_of = [&](int4 u) { return min(S::kHeads, p.group - u.w * S::kHeads); };
   int open[2] = {-1, -1};  // the part that starts the unit left open
+  int turn = warp;         // all units' heads go to the warps in turn: this one's next in the unit
   for (unsigned left = heads_of_groups; left != 0; left &= left - 1) {
     const int k0 = __ffs(left) - 1;
     const int k1 = (left & (left - 1)) != 0 ? __ffs(left & (left - 1)) - 1 : 2 * W;
     const bool begun = s_span[k0][0] < cta0, whole = !begun && s_span[k0][1] <= cta1;
     if (!whole) open[0] = begun ? k0 : open[0], open[1] = begun ? open[1] : k0;
     float* to = p.parts + (static_cast<int64_t>(blockIdx.x) * 2 + (begun ? 0 : 1)) * S::kPart;
-    for (int i = threadIdx.x * 4; i < S::kHeads * D; i += W * 32 * 4) {
-      const int hi = i / D;
-      float4 acc = make_float4(0, 0, 0, 0);
-      for (int j = k0; j < k1; ++j)
-        if ((parts >> j) & 1) add(acc, s_factor[j][hi], *reinterpret_cast<const float4*>(part_of(j) + i));
-      if (whole) {
-        write_out(s_unit[k0], hi, i % D, acc, s_top[k0][hi], s_sum[k0][hi]);
-      } else {
-        *reinterpret_cast<float4*>(to + i) = acc;
-        if (i % D == 0) to[S::kHeads * D + hi] = s_top[k0][hi], to[S::kHeads * (D + 1) + hi] = s_sum[k0][hi];
+    const int4 unit = s_unit[k0];
+    const int heads = heads_of(unit);
+    for (; turn < heads; turn += W) {
+      const float top = s_top[k0][turn], sum = s_sum[k0][turn];
+      for (int d = lane * 4; d < D; d += 128) {
+        float4 acc = make_float4(0, 0, 0, 0);
+        for (int j = k0; j < k1; ++j)
+          if ((parts >> j) & 1)
+            add(acc, s_factor[j][turn], *reinterpret_cast<const float4*>(part_of(j) + turn * D + d));
+        if (whole)
+          write_out(unit, turn, d, acc, top, sum);
+        else
+          *reinterpret_cast<float4*>(to + turn * D + d) = acc;
       }
+      if (!whole && lane == 0) to[S::kHeads * D + turn] = top, to[S::kHeads * (D + 1) + turn] = sum;
     }
+    turn -= heads;
   }
 
   // ---- joining across CTAs: the last one to bring its part adds them all up in order.
@@ -789,19 +794,20 @@ __global__ void __launch_bounds__(S::WARPS * 32, 1) paged_attention_kernel(const
     // part of the k-th CTA: side 1 in the one where the unit starts, side 0 in the others
     const float* parts0 = p.parts + s_from[side] * 2 * S::kPart;
     auto part = [&](int k) { return parts0 + (2 * k + (k == 0 ? 1 : 0)) * S::kPart; };
-    auto load4 = [&](int k, int i) { return __ldcg(reinterpret_cast<const float4*>(part(k) + i)); };
-    // the first parts' states are on the way while the factors are found
-    constexpr int kEarly = 8;
-    float4 early[kEarly];
-    if (first < S::kHeads * D) {
+    // the states come a batch of parts at a time, the first while the factors are found
+    constexpr int kBatch = 16;
+    const int heads = heads_of(unit);
+    float4 state[kBatch];
+    auto load_batch = [&](int k0, int i) {
 #pragma unroll
-      for (int k = 0; k < kEarly; ++k)
-        if (k < count) early[k] = load4(k, first);
-    }
+      for (int k = 0; k < kBatch; ++k)
+        if (k0 + k < count) state[k] = __ldcg(reinterpret_cast<const float4*>(part(k0 + k) + i));
+    };
+    if (first < heads * D) load_batch(0, first);
     // factors [heads][count], where the rings were
     static_assert(S::kSmem >= 2 * S::kHeads * kMaxCtas * 4, "both sides' factors");
     float* factor = reinterpret_cast<float*>(smem) + side * (S::kHeads * kMaxCtas);
-    for (int hi = warp - warp0; hi < S::kHeads; hi += warps) {
+    for (int hi = warp - warp0; hi < heads; hi += warps) {
       auto top_of = [&](int k) { return k < count ? __ldcg(part(k) + S::kHeads * D + hi) : -INFINITY; };
       auto sum_of = [&](int k) { return k < count ? __ldcg(part(k) + S::kHeads * (D + 1) + hi) : 0.0f; };
       const float m = top_of(lane), l = sum_of(lane);
@@ -820,17 +826,15 @@ __global__ void __launch_bounds__(S::WARPS * 32, 1) paged_attention_kernel(const
       if (lane == 0) s_sum[side][hi] = sum, s_top[side][hi] = top;
     }
     __syncthreads();
-    for (int i = first; i < S::kHeads * D; i += step) {
+    for (int i = first; i < heads * D; i += step) {
       const int hi = i / D;
       float4 acc = make_float4(0, 0, 0, 0);
-      int k = 0;
-      if (i == first) {
+      for (int k0 = 0; k0 < count; k0 += kBatch) {
+        if (k0 > 0 || i > first) load_batch(k0, i);
 #pragma unroll
-        for (; k < kEarly; ++k)
-          if (k < count) add(acc, factor[hi * count + k], early[k]);
+        for (int k = 0; k < kBatch; ++k)
+          if (k0 + k < count) add(acc, factor[hi * count + k0 + k], state[k]);
       }
-#pragma unroll 8
-      for (; k < count; ++k) add(acc, factor[hi * count + k], load4(k, i));
       write_out(unit, hi, i % D, acc, s_top[side][hi], s_sum[side][hi]);
     }
   }
