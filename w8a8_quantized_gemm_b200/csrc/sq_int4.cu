@@ -247,9 +247,9 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], 
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+__device__ __forceinline__ float2 ld_cluster_f32x2(uint32_t addr) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
   return v;
 }
 
@@ -854,18 +854,25 @@ __global__ void __launch_bounds__(kTeamWarps * 32, 1) int4_wide_kernel(const Wid
       const int64_t row = (tile0 + clusters * tm) * 16 + r;
       if (row >= p.N) continue;
       float y0 = 0.0f, y1 = 0.0f;
-      for (int c = 0; c < q.split; ++c)
+      const float* at = part + (tm * q.kw * p.M + m) * 16 + r;
+      if (q.split == 1) {
+#pragma unroll 4
         for (int k = 0; k < q.kw; ++k) {
-          const float* at = part + ((tm * q.kw + k) * p.M + m) * 16 + r;
-          if (q.split > 1) {
-            const uint32_t remote = mapa_shared(at, c);
-            y0 += ld_cluster_f32(remote);
-            y1 += ld_cluster_f32(remote + 4);
-          } else {
-            y0 += at[0];
-            y1 += at[1];
+          const float2 v = *reinterpret_cast<const float2*>(at + k * p.M * 16);
+          y0 += v.x;
+          y1 += v.y;
+        }
+      } else {
+        for (int c = 0; c < q.split; ++c) {
+          const uint32_t remote = mapa_shared(at, c);
+#pragma unroll 4
+          for (int k = 0; k < q.kw; ++k) {
+            const float2 v = ld_cluster_f32x2(remote + k * p.M * 64);
+            y0 += v.x;
+            y1 += v.y;
           }
         }
+      }
       if (p.bias != nullptr) {
         const uint32_t b = __ldg(reinterpret_cast<const uint32_t*>(p.bias + row));
         y0 += bf16_lo(b);
