@@ -4,9 +4,9 @@
 //
 // Every key and value is read once for all query heads of its key head: at 4 to 16 flops a
 // byte the call is bound by the bytes of the cache where it is long (64 sequences of up to 8192,
-// 8 key heads of 128, 64 query heads: 131 us, 5.3 TB/s of int8 cache) and by the chain of
-// dependent steps where it is short (one such sequence, 32 query heads: 16.1 us: page table,
-// tile and queries 4, scores and values of two tiles 3, the two joins 5). The work is cut into
+// 8 key heads of 128, 64 query heads: 129 us, 5.4 TB/s of int8 cache) and by the chain of
+// dependent steps where it is short (one such sequence, 32 query heads: 13.3 us: page table,
+// tile and queries 4, scores and values of two tiles 3, the joins 4). The work is cut into
 // tiles of 16 or 32 tokens of one key head; all tiles, in the order (sequence, key head, token),
 // form one line that is dealt out evenly: each CTA (one per SM) gets a contiguous piece of it and
 // each of its warps a contiguous piece of that, whatever the sequences' lengths. A warp works by
