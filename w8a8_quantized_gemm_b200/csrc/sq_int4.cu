@@ -988,7 +988,7 @@ cudaError_t launch_quant_g(const uint16_t* W, int64_t N, int64_t K, int64_t ldw,
   constexpr int smem = kInt4Threads / 32 * kQuantRing * kQuantSlot;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  return launch_kernel(kernel, tile_grid(N, K, 4), dim3(kInt4Threads), smem, stream, false, W, N, K, ldw, s, Wp, scale,
+  return launch_kernel(kernel, tile_grid(N, K, 4), dim3(kInt4Threads), smem, stream, true, W, N, K, ldw, s, Wp, scale,
                        zero);
 }
 
@@ -996,7 +996,7 @@ template <int G>
 cudaError_t launch_dequant_g(const uint8_t* Wp, const uint16_t* scale, const uint8_t* zero, int64_t N, int64_t K,
                              uint16_t* out, cudaStream_t stream) {
   auto kernel = zero != nullptr ? int4_dequant_kernel<G, true> : int4_dequant_kernel<G, false>;
-  return launch_kernel(kernel, tile_grid(N, K, 8), dim3(kInt4Threads), 0, stream, false, Wp, scale, zero, N, K, out);
+  return launch_kernel(kernel, tile_grid(N, K, 8), dim3(kInt4Threads), 0, stream, true, Wp, scale, zero, N, K, out);
 }
 
 }  // namespace
