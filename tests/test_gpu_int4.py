@@ -155,7 +155,9 @@ def test_linear_nonfinite_tokens_stay_to_themselves(M):
 
 @pytest.mark.parametrize("M,N,K,group", [(1, 2848, 4128, 128), (2, 2856, 23552, 32), (3, 9480, 1168, 64),
                                          (4, 9480, 13312, 128), (13, 3016, 27872, 64), (16, 4104, 4112, 128),
-                                         (38, 4664, 3696, 32), (25, 344, 16704, 64), (64, 1032, 8208, 64)])
+                                         (38, 4664, 3696, 32), (25, 344, 16704, 64), (64, 1032, 8208, 64),
+                                         (18, 4824, 4112, 64), (63, 2040, 12304, 128), (33, 3320, 8192, 32),
+                                         (40, 2568, 6160, 128), (64, 29000, 400, 64)])
 def test_linear_large(M, N, K, group):
     """Many rows, long rows, both: activations that do not fit shared memory at once, clusters that
     do not all run at once. Every byte is a pair of codes, so the codes are random bytes and their

@@ -38,7 +38,7 @@ struct TcParams {
   const uint16_t* bias;
   uint16_t* Y;
   int M, K, Kb, groups;
-  int split, log_split;  // CTAs of a cluster
+  int split;  // CTAs of a cluster
   int row_blocks;
   unsigned int* status;
 };
@@ -441,39 +441,35 @@ int4_tc_kernel(const __grid_constant__ CUtensorMap x_map, const TcParams p) {
           atomicOr(p.status, kErrEpilogueWait);
         }
       }
-      // row pairs that this CTA finishes: 64 / split of every token, eight a thread at a time, so that
-      // the loads from the other CTAs are under way together
-      const int log_pairs = 6 - p.log_split, items = p.M << log_pairs;
-      for (int i0 = threadIdx.x; i0 < items; i0 += 8 * C::kWorkers) {
-        float2 y[8];
-        uint32_t at[8];
+      // this CTA's share of the 64 row pairs, a pair per lane and the tokens over the warps; the loads
+      // of a warp's tokens from the other CTAs are under way together
+      constexpr int kWarps = C::kWorkers / 32, kPerWarp = C::kTokens / kWarps;
+      for (int r = 64 * rank / p.split + lane; r < 64 * (rank + 1) / p.split; r += 32) {
+        float2 y[kPerWarp];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int i = min(i0 + j * C::kWorkers, items - 1);
-          const int m = i >> log_pairs, r = ((rank << log_pairs) + (i & ((1 << log_pairs) - 1))) * 2;
-          at[j] = (m * 128 + r) * 4;
-          y[j] = make_float2(0.0f, 0.0f);
-        }
+        for (int j = 0; j < kPerWarp; ++j) y[j] = make_float2(0.0f, 0.0f);
         for (int c = 0; c < p.split; ++c) {
-          const uint32_t from = mapa_shared(part, c);
+          const uint32_t from = mapa_shared(part + warp * 128 + r * 2, c);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float2 v = ld_cluster_f32x2(from + at[j]);
+          for (int j = 0; j < kPerWarp; ++j) {
+            const float2 v = ld_cluster_f32x2(from + j * kWarps * 512);
             y[j].x += v.x;
             y[j].y += v.y;
           }
         }
+        const int64_t n = static_cast<int64_t>(rb) * 128 + r * 2;
+        if (n >= p.N) continue;
+        float2 bias = make_float2(0.0f, 0.0f);
+        if (p.bias != nullptr) {
+          const uint32_t b = __ldg(reinterpret_cast<const uint32_t*>(p.bias + n));
+          bias = make_float2(bf16_lo(b), bf16_hi(b));
+        }
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int m = at[j] >> 9;
-          const int64_t n = static_cast<int64_t>(rb) * 128 + (at[j] & 511) / 4;
-          if (i0 + j * C::kWorkers >= items || n >= p.N) continue;
-          if (p.bias != nullptr) {
-            const uint32_t b = __ldg(reinterpret_cast<const uint32_t*>(p.bias + n));
-            y[j].x += bf16_lo(b);
-            y[j].y += bf16_hi(b);
-          }
-          *reinterpret_cast<__nv_bfloat162*>(p.Y + m * p.N + n) = __floats2bfloat162_rn(y[j].x, y[j].y);
+        for (int j = 0; j < kPerWarp; ++j) {
+          const int m = warp + j * kWarps;
+          if (m < p.M)
+            *reinterpret_cast<__nv_bfloat162*>(p.Y + m * p.N + n) =
+                __floats2bfloat162_rn(y[j].x + bias.x, y[j].y + bias.y);
         }
       }
       if (p.split > 1) {
@@ -514,17 +510,16 @@ cudaError_t launch_tc(const Int4LinearArgs& a, cudaStream_t stream) {
   cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   // Rounds of row blocks over the clusters, in blocks of columns per CTA, and what a round costs
   // besides: its end, and the exchange of a cluster. Measured, us, clusters of 1 / 2 / 4 / 8:
-  // 64 x 8192 x 8192 37 / 22 / 27 / 52, 24 x 2048 x 14336 52 / 29 / 18 / 22, 25 x 344 x 16704
-  // 65 / 36 / 23 / 15, 64 x 1024 x 1024 9.4 / 7.6 / 7.1 / 9.2.
-  constexpr double ends[4] = {3.0, 5.0, 6.0, 9.0};
+  // 64 x 8192 x 8192 37 / 22 / 27 / 52, 24 x 2048 x 14336 52 / 29 / 18 / 22 (of 6 14.5), 25 x 344 x
+  // 16704 65 / 36 / 23 / 15, 64 x 1024 x 1024 9.4 / 7.6 / 7.1 / 9.2; of 2 / 3: 64 x 5120 x 13824
+  // 32 / 24; of 1 / 3: 64 x 28672 x 8192 70 / 74.
   double least = 1e30;
   p.split = 1;
-  for (int split = 1; split <= 8 && split <= p.Kb; split *= 2) {
+  for (int split = 1; split <= 8 && split <= p.Kb; ++split) {
     const int clusters = cluster_slots(sms, split), rounds = (p.row_blocks + clusters - 1) / clusters;
-    const double cost = rounds * ((p.Kb + split - 1) / split + ends[split / 2 - split / 8]);
+    const double cost = rounds * ((p.Kb + split - 1) / split + (split > 1 ? 5.0 + 0.7 * split : 3.0));
     if (cost < least) least = cost, p.split = split;
   }
-  while ((1 << p.log_split) < p.split) ++p.log_split;
   CUtensorMap map{};
   if (!make_bf16_operand_map(&map, a.X, static_cast<uint64_t>(a.K), static_cast<uint64_t>(a.M),
                      static_cast<uint64_t>(a.ldx) * 2, TOKENS))

@@ -71,11 +71,12 @@ cudaError_t launch_kernel(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_
   return launch_kernel_clustered(kernel, grid, block, smem, stream, programmatic, 1u, std::forward<Args>(args)...);
 }
 
-// Clusters of `size` (1, 2, 4 or 8) CTAs that run at once with one CTA per SM: a cluster stays within
-// one of the GPU's groups of SMs, so larger ones leave some SMs out (148 SMs: 74, 33 and 15 clusters
-// of 2, 4 and 8, as the occupancy query gives them; it takes too long to ask on every call).
+// Clusters of `size` (1 to 8) CTAs that run at once with one CTA per SM: a cluster stays within one
+// of the GPU's groups of SMs, so larger ones leave some SMs out (the figures for 148 SMs are the
+// occupancy query's, which takes too long to ask on every call).
 inline int cluster_slots(int sms, int size) {
-  return size <= 2 ? sms / size : size == 4 ? sms * 33 / 148 : sms * 15 / 148;
+  constexpr int slots[8] = {148, 74, 45, 33, 26, 22, 15, 15};
+  return sms * slots[size - 1] / 148;
 }
 
 #ifdef __CUDACC__
