@@ -464,7 +464,9 @@ SQ_API sq_status sq_rope_kv_append(const void* q_bf16, int64_t ldq, const void* 
  * with fp32 scores, softmax statistics and sums, one rounding of out to bf16. For an int8 cache
  * the queries are integers of 23 bits and a power of two (exact down to 2^-14 of a head's
  * largest element, off by at most 2^-23 of it below), so that the scores' sums are exact;
- * a query head with an infinity or NaN gives NaN. Value scales are not negative. A sequence of
+ * a query head with an infinity or NaN gives NaN. Value scales are not negative; lse does not
+ * depend on them (beside one above 2^100, a token may be missing from lse whose share is below
+ * 2^-140 times that scale), and one that is infinite or NaN makes its key head's out NaN. A sequence of
  * length 0 gives out 0 and lse -inf. Cache contents behind a sequence's last token (NaN
  * included) are never used. The work is split over the sequences' lengths and joined in a
  * fixed order: the same inputs give the same bits.

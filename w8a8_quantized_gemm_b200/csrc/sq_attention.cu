@@ -29,9 +29,12 @@
 //   - values become fp16 exactly: (byte ^ 0x80) + 1024 has the byte's bits as its mantissa, one
 //     logic operation, and 1152 less is the code.
 // The probabilities enter as a high and a low 16-bit part, so that the rounding of out to bf16
-// is the only one that counts. For an int8 cache they carry the token's value scale vs: the
-// running maximum is then that of s + log2(vs), which keeps the products within [0, 1], in
-// fp16's range whatever the scales.
+// is the only one that counts. For an int8 cache they carry the token's value scale vs: what is
+// subtracted is then the running maximum of s + log2(vs), less kShift, which keeps the products
+// within [0, 2^kShift], in fp16's range whatever the scales, and the exponentials alone, whose sum
+// is the softmax's, in fp32's: from 2^(kShift - 121) (bf16 values are below 2^128, their scales below
+// 2^121) to 2^(kShift - kFloor) a token, where kFloor stands for the log2 of smaller scales, of zero
+// and of scales that are not finite.
 #include "sq_internal.h"
 #include "sq_ptx.cuh"
 #include "sq_rows.cuh"
@@ -134,6 +137,11 @@ __device__ __forceinline__ float exp2_approx(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
+__device__ __forceinline__ float log2_approx(float x) {
+  float r;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 r = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&r);
@@ -158,8 +166,13 @@ __device__ __forceinline__ void split_bf16(float a, float b, uint32_t& hi, uint3
   hi = pack_bf16(a, b);
   lo = pack_bf16(a - bf16_lo(hi), b - bf16_hi(hi));
 }
-// exp2(a - b) of two running maxima; nothing came before a maximum of -inf.
-__device__ __forceinline__ float shrink(float a, float b) { return a == -INFINITY ? 0.0f : exp2_approx(a - b); }
+// exp2((a - b) / 2) of two running maxima: its square takes a state to the new one. A sum takes it in
+// two steps, since maxima that the scales of values have moved can be further apart than fp32's
+// exponents, and the sum's size makes up for it. Nothing came before a maximum of -inf.
+__device__ __forceinline__ float shrink_half(float a, float b) {
+  return a == -INFINITY ? 0.0f : exp2_approx(0.5f * (a - b));
+}
+constexpr float kShift = 14.0f, kFloor = -90.0f;  // int8 cache: see above
 
 constexpr int kMaxCtas = 160;  // one per SM
 
@@ -532,8 +545,8 @@ __global__ void __launch_bounds__(S::WARPS * 32, 1) paged_attention_kernel(const
           const int row = mt * 16 + h * 8 + g;
           ks[mt][h] = INT8 ? sc[row] : 1.0f;
           vs[mt][h] = INT8 ? sc[kTile + row] : 1.0f;
-          lv[mt][h] = INT8 ? __log2f(fmaxf(vs[mt][h], 7.888609e-31f)) : 0.0f;  // 2^-100: finite for a row of zeros
-          vs[mt][h] *= INT8 ? 16384.0f : 1.0f;
+          lv[mt][h] = INT8 ? fmaxf(log2_approx(vs[mt][h]), kFloor) : 0.0f;
+          if (INT8 && lv[mt][h] == INFINITY) lv[mt][h] = kFloor;
         }
       uint32_t ph[MT][NT][2], pl[MT][NT][2];
 #pragma unroll
@@ -553,13 +566,14 @@ __global__ void __launch_bounds__(S::WARPS * 32, 1) paged_attention_kernel(const
           mn[0] = fmaxf(mn[0], __shfl_xor_sync(0xffffffffu, mn[0], w));
           mn[1] = fmaxf(mn[1], __shfl_xor_sync(0xffffffffu, mn[1], w));
         }
+        if (INT8) mn[0] -= kShift, mn[1] -= kShift;
         const bool grows = mn[0] > m[nt][0] || mn[1] > m[nt][1];
         if (__any_sync(0xffffffffu, grows)) {
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const float top = fmaxf(m[nt][e], mn[e]), f = shrink(m[nt][e], top);
+            const float top = fmaxf(m[nt][e], mn[e]), half = shrink_half(m[nt][e], top), f = half * half;
             m[nt][e] = top;
-            l[nt][e] *= f;
+            l[nt][e] = l[nt][e] * half * half;
 #pragma unroll
             for (int j = 0; j < kSteps; ++j) {
               o[nt][j][e] *= f;
@@ -638,16 +652,15 @@ __global__ void __launch_bounds__(S::WARPS * 32, 1) paged_attention_kernel(const
             for (int w = 4; w < 32; w <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
             const int hi = nt * 8 + 2 * t + e, hl = hb * S::kHeads + hi;  // head in the unit, in its group
             const int h = kvh * p.group + hl;
-            const float unit = INT8 ? 1.0f / 16384 : 1.0f;  // of the probabilities' parts
-            const float inv = sum != 0.0f ? unit / sum : 0.0f;
+            const float inv = sum != 0.0f ? 1.0f / sum : 0.0f;
             uint16_t* out = p.out + (static_cast<int64_t>(cur.b) * p.H + h) * D;
 #pragma unroll
             for (int j = 0; j < kSteps; ++j) {
               const int d0 = 16 * j + (INT8 ? 2 * g : g), d1 = INT8 ? d0 + 1 : d0 + 8;
               const float v0 = o[nt][j][e], v1 = o[nt][j][e + 2];
               if (!whole) {
-                part[hi * D + d0] = v0 * unit;
-                part[hi * D + d1] = v1 * unit;
+                part[hi * D + d0] = v0;
+                part[hi * D + d1] = v1;
               } else if (hl < p.group) {
                 if (INT8) {
                   *reinterpret_cast<uint32_t*>(out + d0) = pack_bf16(v0 * inv, v1 * inv);
@@ -719,8 +732,8 @@ __global__ void __launch_bounds__(S::WARPS * 32, 1) paged_attention_kernel(const
       if (lane - o >= seg0) top = fmaxf(top, v);
     }
     top = __shfl_sync(0xffffffffu, top, seg1);
-    const float f = shrink(m, top);
-    float sum = f * l;
+    const float half = shrink_half(m, top), f = half * half;
+    float sum = l * half * half;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const float v = __shfl_up_sync(0xffffffffu, sum, o);
@@ -817,9 +830,9 @@ __global__ void __launch_bounds__(S::WARPS * 32, 1) paged_attention_kernel(const
       for (int w = 16; w > 0; w >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
       float sum = 0.0f;
       for (int k = lane; k < count; k += 32) {
-        const float f = shrink(k == lane ? m : top_of(k), top);
-        factor[hi * count + k] = f;
-        sum = fmaf(f, k == lane ? l : sum_of(k), sum);
+        const float half = shrink_half(k == lane ? m : top_of(k), top);
+        factor[hi * count + k] = half * half;
+        sum += (k == lane ? l : sum_of(k)) * half * half;
       }
 #pragma unroll
       for (int w = 16; w > 0; w >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
