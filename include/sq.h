@@ -499,7 +499,8 @@ SQ_API const char* sq_last_error(void);
  * of spinning forever, when an index that a paged-cache call read from device memory was out
  * of range (its access was skipped), and, in the debug build libsq_debug.so (same ABI, kernels
  * compiled with device-side bounds guards that skip and record an out-of-range access), when a
- * guard fires. Returns SQ_OK, SQ_ERR_TIMEOUT, SQ_ERR_BOUNDS or SQ_ERR_CUDA. */
+ * guard fires. An index out of range is reported, and cleared, after all else: beside a wait that gave
+ * up this call returns SQ_ERR_TIMEOUT and the next one SQ_ERR_BOUNDS. Returns SQ_OK, SQ_ERR_TIMEOUT, SQ_ERR_BOUNDS or SQ_ERR_CUDA. */
 SQ_API sq_status sq_sync_status(sq_stream_t stream);
 
 /* Library version string and the compute capability it was built for ("sm_100a"). */

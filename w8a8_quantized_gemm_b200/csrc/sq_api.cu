@@ -753,10 +753,11 @@ sq_status sq_sync_status(sq_stream_t stream) {
   e = cudaMemcpyFromSymbol(&word, sq::g_status_word, sizeof word);
   if (e != cudaSuccess) return cuda_fail(e, "sq_sync_status: read status word");
   if (word != 0) {
-    const unsigned int zero = 0;
-    e = cudaMemcpyToSymbol(sq::g_status_word, &zero, sizeof zero);
+    // waits that gave up and guards come before indices, which stay for the next call
+    const unsigned int rest = (word & ~sq::kErrIndex) != 0 ? word & sq::kErrIndex : 0;
+    e = cudaMemcpyToSymbol(sq::g_status_word, &rest, sizeof rest);
     if (e != cudaSuccess) return cuda_fail(e, "sq_sync_status: clear status word");
-    if (word & sq::kErrIndex)
+    if (word == sq::kErrIndex)
       return fail(SQ_ERR_BOUNDS,
                   "a slot, position, page or length read from device memory was out of range (status bits 0x%x)", word);
     if (word & sq::kErrBounds)
