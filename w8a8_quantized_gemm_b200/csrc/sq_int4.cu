@@ -271,7 +271,7 @@ struct LinearParams {
 // word of eight codes masked with 0x0F0F0F0F, and shifted once, is two operands of four. So the
 // activations become integers instead, once: a token, scaled by a power of two to 23 bits, is
 // split into three signed bytes, three columns of the 16x8x32 instructions (elements down to
-// 2^-14 of the token's largest are exact, smaller ones off by 2^-23 of it). Products and a
+// 2^-14 of the token's largest are exact, smaller ones off by at most 2^-22 of it). Products and a
 // group's sums are exact integers, and so is the zero point's part,
 //   sum_k x_k (code - zero) = sum_k x_k code - zero * sum_k x_k,
 // with the group's sums of x taken beforehand. A group's result is scaled and added in fp32.
@@ -312,15 +312,22 @@ __device__ __forceinline__ void mma_u8s8(int (&d)[4], uint32_t a0, uint32_t a1, 
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// Where the rings begin: copies to odd multiples of 16 bytes cost more (2 x 8192 x 28672 35 us, 40 from
+// there).
+template <int G>
+__host__ __device__ constexpr int team_ring_at(int tokens, int col_bytes, int cp, int nt) {
+  return (3 * tokens * col_bytes + cp * (256 / G) * nt * 8 * 4 + 127) / 128 * 128;
+}
+
 // NT: columns / 8; column 3 m + d is byte d (0 the highest) of token m.
 template <int NT, int G, bool ASYM>
 __global__ void __launch_bounds__(kTeamWarps * 32, 1) int4_team_kernel(const TeamParams q) {
   constexpr int kGroups = 256 / G, kSlot = team_slot_bytes<G, ASYM>(), kThreads = kTeamWarps * 32, kCols = NT * 8;
   constexpr int kScales = 2 * kTileBytes, kZeros = kScales + kGroups * 32;
   const LinearParams& p = q.p;
-  extern __shared__ __align__(16) uint8_t smem[];
+  extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint32_t s_top[kTeamWarps];
-  __shared__ float s_mul[kTeamTokens], s_back[kTeamTokens];
+  __shared__ float s_mul[kTeamTokens][2], s_back[kTeamTokens][2];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int teams = kTeamWarps / q.kw, team = warp / q.kw, kw = warp % q.kw;
   const int Nt = static_cast<int>((p.N + 15) / 16), step = gridDim.x * teams;
@@ -336,7 +343,7 @@ __global__ void __launch_bounds__(kTeamWarps * 32, 1) int4_team_kernel(const Tea
 
   // shared memory: columns of bytes | [groups][kCols] sums of a group's bytes | rings | partial sums
   // (with one tile per team, partial sums where the columns were)
-  const int sums_at = 3 * p.M * q.col_bytes, ring_at = sums_at + q.cp * kGroups * kCols * 4;
+  const int sums_at = 3 * p.M * q.col_bytes, ring_at = team_ring_at<G>(p.M, q.col_bytes, q.cp, NT);
   const uint32_t ring32 = smem_u32(smem) + ring_at + warp * q.ring * kSlot;
   int* sums = reinterpret_cast<int*>(smem + sums_at);
   float* part =  // [2][warps][kCols][16]
@@ -415,18 +422,21 @@ __global__ void __launch_bounds__(kTeamWarps * 32, 1) int4_team_kernel(const Tea
   if (threadIdx.x < p.M) {
     uint32_t top = 0;
     for (int w = 0; w < share; ++w) top = max(top, s_top[threadIdx.x * share + w]);
-    // 2^up brings the largest below 2^22; integers cannot carry infinity or NaN, so the token's
-    // results become NaN
-    const int up = min(22 + 126 - static_cast<int>(top >> 7), 120);
-    s_mul[threadIdx.x] = __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
-    s_back[threadIdx.x] = __uint_as_float(top < 0x7F80u ? static_cast<uint32_t>(127 - up) << 23 : 0x7FC00000u);
+    // 2^up brings the largest, which may be subnormal, between 2^21 and 2^22: two factors, since up is
+    // -106 to 155. Integers cannot carry infinity or NaN, so the token's results become NaN
+    const int up = top >= 0x80u ? 22 + 126 - static_cast<int>(top >> 7) : 123 + __clz(static_cast<int>(top));
+    const int up0 = min(up, 120), up1 = up - up0;
+    s_mul[threadIdx.x][0] = __uint_as_float(static_cast<uint32_t>(127 + up0) << 23);
+    s_mul[threadIdx.x][1] = __uint_as_float(static_cast<uint32_t>(127 + up1) << 23);
+    s_back[threadIdx.x][0] = __uint_as_float(top < 0x7F80u ? static_cast<uint32_t>(127 - up0) << 23 : 0x7FC00000u);
+    s_back[threadIdx.x][1] = __uint_as_float(static_cast<uint32_t>(127 - up1) << 23);
   }
   __syncthreads();
   // then 8 elements per thread and step; a warp takes a pair of blocks: 8 words of 32 columns x 4 quad lanes
   auto to_bytes = [&](int first, int pairs) {
     for (int i = warp; i < p.M * pairs; i += kTeamWarps) {
       const int m = i / pairs, kp = i % pairs, word = (first + kp) * 8 + lane / 4;
-      const float mul = s_mul[m];
+      const float mul = s_mul[m][0], mul1 = s_mul[m][1];
       const uint16_t* src = p.X + m * p.ldx + word * 32 + t * 2;
       uint32_t v[8];  // columns 2 t, 2 t + 1 of each 8
 #pragma unroll
@@ -434,8 +444,8 @@ __global__ void __launch_bounds__(kTeamWarps * 32, 1) int4_team_kernel(const Tea
         const uint32_t x = word * 32 + c * 8 < p.K ? __ldg(reinterpret_cast<const uint32_t*>(src + c * 8)) : 0u;
         // round to an integer in the low mantissa bits (1.5 * 2^23 added), then bytes with carries:
         // the three low bytes of v + 0x808080, each less 128, are the signed digits
-        v[2 * c] = __float_as_uint(__fmaf_rn(bf16_lo(x), mul, 12582912.0f)) + (0x00808080u - 0x4B400000u);
-        v[2 * c + 1] = __float_as_uint(__fmaf_rn(bf16_hi(x), mul, 12582912.0f)) + (0x00808080u - 0x4B400000u);
+        v[2 * c] = __float_as_uint(__fmaf_rn(bf16_lo(x) * mul1, mul, 12582912.0f)) + (0x00808080u - 0x4B400000u);
+        v[2 * c + 1] = __float_as_uint(__fmaf_rn(bf16_hi(x) * mul1, mul, 12582912.0f)) + (0x00808080u - 0x4B400000u);
       }
 #pragma unroll
       for (int d = 0; d < 3; ++d) {
@@ -558,8 +568,8 @@ __global__ void __launch_bounds__(kTeamWarps * 32, 1) int4_team_kernel(const Tea
         y0 += fmaf(fmaf(v0.x, 256.0f, v1.x), 256.0f, v2.x);
         y1 += fmaf(fmaf(v0.y, 256.0f, v1.y), 256.0f, v2.y);
       }
-      y0 *= s_back[m];
-      y1 *= s_back[m];
+      y0 = y0 * s_back[m][0] * s_back[m][1];
+      y1 = y1 * s_back[m][0] * s_back[m][1];
       if (p.bias != nullptr) {
         const uint32_t b = __ldg(reinterpret_cast<const uint32_t*>(p.bias + n));
         y0 += bf16_lo(b);
@@ -576,8 +586,7 @@ __global__ void __launch_bounds__(kTeamWarps * 32, 1) int4_team_kernel(const Tea
 template <int G, bool ASYM>
 int64_t team_smem(const TeamParams& q, int nt) {
   const int64_t cols = nt * 8, sums = kTeamWarps * cols * 64;
-  const int64_t rest = 3 * q.p.M * q.col_bytes + static_cast<int64_t>(q.cp) * (256 / G) * cols * 4 +
-                       kTeamWarps * q.ring * team_slot_bytes<G, ASYM>();
+  const int64_t rest = team_ring_at<G>(q.p.M, q.col_bytes, q.cp, nt) + kTeamWarps * q.ring * team_slot_bytes<G, ASYM>();
   return q.rounds == 1 ? std::max(rest, sums) : rest + 2 * sums;
 }
 
