@@ -463,7 +463,8 @@ SQ_API sq_status sq_rope_kv_append(const void* q_bf16, int64_t ldq, const void* 
  *   lse[b,h] = log sum_t exp( scale * (q[b,h] . k_t) )
  * with fp32 scores, softmax statistics and sums, one rounding of out to bf16. For an int8 cache
  * the queries are integers of 23 bits and a power of two (exact down to 2^-14 of a head's
- * largest element, off by at most 2^-23 of it below), so that the scores' sums are exact;
+ * largest element, off by at most 2^-22 of it below, where scale times that element is at least
+ * 2^-104), so that the scores' sums are exact;
  * a query head with an infinity or NaN gives NaN. Value scales are not negative; lse does not
  * depend on them (beside one above 2^100, a token may be missing from lse whose share is below
  * 2^-140 times that scale), and one that is infinite or NaN makes its key head's out NaN. A sequence of

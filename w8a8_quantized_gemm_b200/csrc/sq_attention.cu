@@ -25,7 +25,7 @@
 // instructions than all the rest, so
 //   - scores use the 16x8x32 int8 instructions: a query, scaled by a power of two to 23 bits,
 //     is split into three signed bytes and the three exact products are put together again
-//     (elements down to 2^-14 of the head's largest are exact, smaller ones off by 2^-23 of it);
+//     (elements down to 2^-14 of the head's largest are exact, smaller ones off by at most 2^-22 of it);
 //   - values become fp16 exactly: (byte ^ 0x80) + 1024 has the byte's bits as its mantissa, one
 //     logic operation, and 1152 less is the code.
 // The probabilities enter as a high and a low 16-bit part, so that the rounding of out to bf16
@@ -426,21 +426,23 @@ __global__ void __launch_bounds__(S::WARPS * 32, 1) paged_attention_kernel(const
             top = max(top >> 16, top & 0xFFFFu);
             top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
             top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            // 2^up brings the largest below 2^22; integers cannot carry infinity or NaN, so the
-            // head's scores become NaN
-            const int up = min(22 + 126 - static_cast<int>(top >> 7), 120);
-            const float mul = __uint_as_float(static_cast<uint32_t>(up + 127) << 23);
+            // 2^up brings the largest, which may be subnormal, between 2^21 and 2^22: two factors, since up
+            // is -106 to 155. Integers cannot carry infinity or NaN, so the head's scores become NaN
+            const int up = top >= 0x80u ? 22 + 126 - static_cast<int>(top >> 7) : 123 + __clz(static_cast<int>(top));
+            const int up0 = min(up, 120), up1 = up - up0;
+            const float mul = __uint_as_float(static_cast<uint32_t>(127 + up0) << 23);
+            const float mul1 = __uint_as_float(static_cast<uint32_t>(127 + up1) << 23);
 #pragma unroll
             for (int j = 0; j < kWords; ++j)
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
                 // round to an integer in the low mantissa bits (1.5 * 2^23 added), then bytes with
                 // carries: the three low bytes of v + 0x808080, each less 128, are the signed digits
-                constexpr uint32_t kShift = 0x00808080u - 0x4B400000u;
-                const uint32_t v[4] = {__float_as_uint(__fmaf_rn(bf16_lo(w[j][h].x), mul, 12582912.0f)) + kShift,
-                                       __float_as_uint(__fmaf_rn(bf16_hi(w[j][h].x), mul, 12582912.0f)) + kShift,
-                                       __float_as_uint(__fmaf_rn(bf16_lo(w[j][h].y), mul, 12582912.0f)) + kShift,
-                                       __float_as_uint(__fmaf_rn(bf16_hi(w[j][h].y), mul, 12582912.0f)) + kShift};
+                constexpr uint32_t kBytes = 0x00808080u - 0x4B400000u;
+                const float x[4] = {bf16_lo(w[j][h].x), bf16_hi(w[j][h].x), bf16_lo(w[j][h].y), bf16_hi(w[j][h].y)};
+                uint32_t v[4];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) v[c] = __float_as_uint(__fmaf_rn(x[c] * mul1, mul, 12582912.0f)) + kBytes;
 #pragma unroll
                 for (int d = 0; d < 3; ++d) {
                   const uint32_t pick = d == 0 ? 0x0062u : d == 1 ? 0x0051u : 0x0040u;
@@ -449,9 +451,10 @@ __global__ void __launch_bounds__(S::WARPS * 32, 1) paged_attention_kernel(const
                 }
               }
             const float back =
-                top < 0x7F80u ? p.scale * __uint_as_float(static_cast<uint32_t>(127 - up) << 23) : NAN;
-            factor[nt][0] = __shfl_sync(0xffffffffu, back, 8 * t);
-            factor[nt][1] = __shfl_sync(0xffffffffu, back, 8 * t + 4);
+                top < 0x7F80u ? p.scale * __uint_as_float(static_cast<uint32_t>(127 - up0) << 23) : NAN;
+            const float factor_g = back * __uint_as_float(static_cast<uint32_t>(127 - up1) << 23);
+            factor[nt][0] = __shfl_sync(0xffffffffu, factor_g, 8 * t);
+            factor[nt][1] = __shfl_sync(0xffffffffu, factor_g, 8 * t + 4);
           } else {
 #pragma unroll
             for (int j = 0; j < kWords; ++j)
