@@ -391,7 +391,8 @@ SQ_API sq_status sq_dequant_weight_int4(const uint8_t* Wp, const void* w_scale_b
  * order that depends on the shapes only: the same inputs give the same bits). Up to 4 tokens
  * may be taken as integers of 23 bits and a power of two instead, with exact group sums:
  * elements down to 2^-14 of their token's largest are exact, smaller ones off by at most 2^-22
- * of it, and a token with an infinity or NaN gives NaN. With more tokens those give what the
+ * of it, a token with an infinity or NaN gives NaN, and scales (of which the group sums are
+ * multiples) may be up to 2^100. With more tokens those give what the
  * formula does. Other tokens' results do not depend on them.
  * X: bf16 [M, K], ldx, 1 <= M <= 64 (more tokens: sq_dequant_weight_int4 or the int8 GEMM).
  * For a weight quantized with smoothing factors s, X must already be divided by s (folded

@@ -79,3 +79,15 @@ def test_elements_far_below_the_largest(M):
     Y = _run(dev_bf16(X), (Wp, e, z), group, None, N)
     sq.sq_sync_status()
     _check(Y, X, values, None)
+
+
+@pytest.mark.parametrize("M", [1, 2, 4])
+@pytest.mark.parametrize("scale,token", [(2.0 ** 99, 2.0 ** -60), (2.0 ** 60, 2.0 ** 40), (2.0 ** -120, 2.0 ** -9), (2.0 ** -132, 2.0 ** 30)])
+def test_scales_far_from_one(M, scale, token):
+    """Scales up to 2^100 and down to bf16's smallest, tokens that bring the results back into range."""
+    N, K, group = _rows(M), 1040, 64
+    weight, values = _weight(N, K, group, True, M, scale, 1.9 * scale)
+    X = wl.f32_to_bf16_bits((np.random.default_rng(M).normal(0, 1, (M, K)) * token).astype(np.float32))
+    Y = _run(dev_bf16(X), weight, group, None, N)
+    sq.sq_sync_status()
+    _check(Y, X, values, None)

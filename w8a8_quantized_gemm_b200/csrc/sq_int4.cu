@@ -428,7 +428,8 @@ __global__ void __launch_bounds__(kTeamWarps * 32, 1) int4_team_kernel(const Tea
     const int up0 = min(up, 120), up1 = up - up0;
     s_mul[threadIdx.x][0] = __uint_as_float(static_cast<uint32_t>(127 + up0) << 23);
     s_mul[threadIdx.x][1] = __uint_as_float(static_cast<uint32_t>(127 + up1) << 23);
-    s_back[threadIdx.x][0] = __uint_as_float(top < 0x7F80u ? static_cast<uint32_t>(127 - up0) << 23 : 0x7FC00000u);
+    // (of sums in units of the highest digit)
+    s_back[threadIdx.x][0] = __uint_as_float(top < 0x7F80u ? static_cast<uint32_t>(143 - up0) << 23 : 0x7FC00000u);
     s_back[threadIdx.x][1] = __uint_as_float(static_cast<uint32_t>(127 - up1) << 23);
   }
   __syncthreads();
@@ -565,8 +566,8 @@ __global__ void __launch_bounds__(kTeamWarps * 32, 1) int4_team_kernel(const Tea
         const float* c = all + (k * kCols + 3 * m) * 16 + r;
         const float2 v0 = *reinterpret_cast<const float2*>(c), v1 = *reinterpret_cast<const float2*>(c + 16);
         const float2 v2 = *reinterpret_cast<const float2*>(c + 32);
-        y0 += fmaf(fmaf(v0.x, 256.0f, v1.x), 256.0f, v2.x);
-        y1 += fmaf(fmaf(v0.y, 256.0f, v1.y), 256.0f, v2.y);
+        y0 += fmaf(fmaf(v2.x, 0x1p-8f, v1.x), 0x1p-8f, v0.x);
+        y1 += fmaf(fmaf(v2.y, 0x1p-8f, v1.y), 0x1p-8f, v0.y);
       }
       y0 = y0 * s_back[m][0] * s_back[m][1];
       y1 = y1 * s_back[m][0] * s_back[m][1];
