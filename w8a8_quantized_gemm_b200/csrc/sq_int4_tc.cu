@@ -69,11 +69,13 @@ struct Cfg {
 };
 
 template <int BYTES>
-__device__ __forceinline__ void cp_async(uint32_t dst, const void* src) {
+__device__ __forceinline__ void cp_async(uint32_t dst, const void* src, bool valid = true) {
   if constexpr (BYTES == 16)
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
   else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(BYTES) : "memory");
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(BYTES),
+                 "r"(valid ? BYTES : 0)
+                 : "memory");
 }
 __device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
                                        uint32_t accumulate) {
@@ -275,8 +277,8 @@ int4_tc_kernel(const __grid_constant__ CUtensorMap x_map, const TcParams p) {
     const int64_t Nt = (p.N + 15) / 16;
     constexpr int kPer = C::kPer;  // groups of a block
     // ---- this warp's blocks: wg, wg + kWg, ... of each row block, codes and factors several ahead.
-    // Rows past N take a valid row's bytes and groups past K the last group's: neither is ever used
-    // (the tokens are zero there).
+    // Rows past N take a valid row's bytes and groups past K the last group's zero points: neither is
+    // ever used (the tokens are zero there). Scales past K are zero, whatever the last group's is.
     int load_rb = wg < nb ? cluster : p.row_blocks, load_b = wg;
     const int64_t tile_bytes = static_cast<int64_t>(p.Kb) * kTileBytes;
     const uint8_t *src = nullptr, *z_src = nullptr;  // 16 bytes `lane` of this warp's first tile in the next block
@@ -305,7 +307,8 @@ int4_tc_kernel(const __grid_constant__ CUtensorMap x_map, const TcParams p) {
         cp_async<16>(dst + 24 * kCodeRow, src + second + 512);
         const int gr = (b0 + load_b) * kPer;
         if (lane < kPer * kELanes)
-          cp_async<kE>(at + C::kScales + lane * kE, e_src + min(gr + e_group, p.groups - 1) * p.N);
+          cp_async<kE>(at + C::kScales + lane * kE, e_src + min(gr + e_group, p.groups - 1) * p.N,
+                       gr + e_group < p.groups);
         if (ASYM && lane < kPer * 8)
           cp_async<4>(at + C::kZeros + lane * 4, z_src + min(gr + z_group, p.groups - 1) * p.N);
         src += C::kWg * kTileBytes;
