@@ -371,6 +371,8 @@ SQ_API size_t sq_int4_weight_bytes(int64_t N, int64_t K);
  *   r = min(1 / e, FLT_MAX) (0 if e == 0),  code = clamp(rne(w' * r) + z, 0, 15)
  * (fp32, IEEE divisions, round half to even). The codes are taken against the rounded scale,
  * so rounding it to bf16 costs no accuracy of its own beyond a grid 2^-9 wider or narrower.
+ * A group with a NaN (in W, s or their product) gets NaN as its scale, one with an infinity (or
+ * whose hi - lo is one) infinity: no value of it is finite, its codes and zero point have no meaning.
  * W: bf16 [N, K], ldw. s: fp32 [K] or NULL. Wp, w_scale, w_zero (or NULL): written whole.
  */
 SQ_API sq_status sq_quant_weight_int4(const void* W_bf16, int64_t N, int64_t K, int64_t ldw, const float* s,

@@ -35,6 +35,17 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
       __hmul2_rn(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
   return *reinterpret_cast<const uint32_t*>(&r);
 }
+// The larger and the smaller one, or NaN.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
 // bf16 pair of 128 + z: 0x4300 is 128, whose mantissa counts in ones.
 __device__ __forceinline__ uint32_t zero_pair(uint32_t z) { return 0x43004300u | z | (z << 16); }
 
@@ -129,21 +140,21 @@ int4_quant_kernel(const uint16_t* __restrict__ W, int64_t N, int64_t K, int64_t 
           v[4 * a + i] = rows::f2_mul(rows::f2_pack(bf16_lo(w[i]), bf16_hi(w[i])), sv[4 * a + i]);
           float x, y;
           rows::f2_unpack(v[4 * a + i], x, y);
-          hi[a] = ASYM ? fmaxf(hi[a], fmaxf(x, y)) : fmaxf(hi[a], fmaxf(fabsf(x), fabsf(y)));
-          if (ASYM) lo[a] = fminf(lo[a], fminf(x, y));
+          hi[a] = ASYM ? max_nan(hi[a], max_nan(x, y)) : max_nan(hi[a], max_nan(fabsf(x), fabsf(y)));
+          if (ASYM) lo[a] = min_nan(lo[a], min_nan(x, y));
         }
       }
 #pragma unroll
       for (int a = 0; a < 4; a += kSpan) {
 #pragma unroll
         for (int i = 1; i < kSpan; ++i) {
-          hi[a] = fmaxf(hi[a], hi[a + i]);
-          lo[a] = fminf(lo[a], lo[a + i]);
+          hi[a] = max_nan(hi[a], hi[a + i]);
+          lo[a] = min_nan(lo[a], lo[a + i]);
         }
 #pragma unroll
         for (int o = 1; o < 4; o <<= 1) {
-          hi[a] = fmaxf(hi[a], __shfl_xor_sync(0xffffffffu, hi[a], o));
-          if (ASYM) lo[a] = fminf(lo[a], __shfl_xor_sync(0xffffffffu, lo[a], o));
+          hi[a] = max_nan(hi[a], __shfl_xor_sync(0xffffffffu, hi[a], o));
+          if (ASYM) lo[a] = min_nan(lo[a], __shfl_xor_sync(0xffffffffu, lo[a], o));
         }
 #pragma unroll
         for (int i = 1; i < kSpan; ++i) hi[a + i] = hi[a], lo[a + i] = lo[a];
