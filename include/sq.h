@@ -523,6 +523,12 @@ SQ_API uint64_t sq_kernel_launch_count(void);
  * use; the output of the armed call is undefined. */
 SQ_API void sq_debug_arm_fault(int fault, uint64_t wait_limit_ns);
 
+/* Test hook of the bounds guards (libsq_debug.so; SQ_ERR_UNSUPPORTED otherwise). From now on the current
+ * device's guards of the 4-bit and paged-cache kernels take every buffer for `margin` (>= 0) elements
+ * shorter than it is, so that they skip and record accesses near its end: 0 restores them.
+ * Synchronises the device. Not for production use. */
+SQ_API sq_status sq_debug_guard_margin(int64_t margin);
+
 /* Test hook (no counterpart on the pages): the launch plan that sq_int8_gemm_dequant
  * (outliers = 0) or the GEMM of llmint8_decomposed_linear (outliers = 1) uses for an
  * M x N x K product, computed on the host without touching a device. plan (caller-owned,

@@ -16,6 +16,10 @@ namespace sq {
 // Per-device error word set by kernels whose bounded waits give up.
 __device__ unsigned int g_status_word;
 
+#ifdef SQ_DEBUG_GUARDS
+__device__ long long g_guard_margin;  // what guard conditions take buffers shorter by
+#endif
+
 // Looked up on every launch (a host-side query on the current device): no address is kept
 // across calls, so none outlives a device reset and concurrent host threads share no state.
 unsigned int* device_status_word() {
@@ -775,6 +779,20 @@ uint64_t sq_kernel_launch_count(void) { return sq::g_launches.load(); }
 void sq_debug_arm_fault(int fault, uint64_t wait_limit_ns) {
   g_arm_fault = fault;
   g_arm_limit_ns = wait_limit_ns == 0 ? sq::kDefaultWaitLimitNs : wait_limit_ns;
+}
+
+sq_status sq_debug_guard_margin(int64_t margin) {
+  const char* fn = "sq_debug_guard_margin";
+#ifdef SQ_DEBUG_GUARDS
+  if (margin < 0) return fail(SQ_ERR_INVALID, "%s: margin must not be negative", fn);
+  cudaError_t e = cudaDeviceSynchronize();
+  if (e != cudaSuccess) return cuda_fail(e, fn);
+  const long long value = margin;
+  e = cudaMemcpyToSymbol(sq::g_guard_margin, &value, sizeof value);
+  return e == cudaSuccess ? SQ_OK : cuda_fail(e, fn);
+#else
+  return fail(SQ_ERR_UNSUPPORTED, "%s(%lld): built without guards", fn, static_cast<long long>(margin));
+#endif
 }
 
 sq_status sq_debug_gemm_plan(int64_t M, int64_t N, int64_t K, int outliers, int64_t* plan) {

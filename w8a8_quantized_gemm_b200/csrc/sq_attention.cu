@@ -316,7 +316,9 @@ __global__ void __launch_bounds__(S::WARPS * 32, 1) paged_attention_kernel(const
     const int shift = p.c.page_shift;
     // page table entries win .. win + 63 of sequence win_b, one of each half per lane
     int win = 0, win_b = -1, pages0 = 0, pages1 = 0;
-    auto entry = [&](int b, int i) { return i < p.max_pages ? __ldg(p.table + b * p.ld_table + i) : -1; };
+    auto entry = [&](int b, int i) {
+      return i < p.max_pages && SQ_GUARD(b < p.B && i >= 0) ? __ldg(p.table + b * p.ld_table + i) : -1;
+    };
     const bool paged = (1 << shift) >= kTile;  // a tile lies in one page, its rows one after another
     constexpr int kChunks = S::kRowBytes / 16, kCopies = kTile * kChunks / 32;
     // place of copy i of this lane: row (32 i + lane) / kChunks
@@ -348,17 +350,22 @@ __global__ void __launch_bounds__(S::WARPS * 32, 1) paged_attention_kernel(const
         const int64_t off = (p.c.page_stride * one + row * D) * (INT8 ? 1 : 2) + lane * 16;
         k += off;
         v += off;
+        const int64_t bytes = p.c.elements() * (INT8 ? 1 : 2);
 #pragma unroll
-        for (int i = 0; i < kCopies; ++i) cp_async16(dst + in_stage(i), k + i * 512, true);
+        for (int i = 0; i < kCopies; ++i)
+          cp_async16(dst + in_stage(i), k + i * 512, SQ_GUARD(within(k + i * 512, 16, p.c.k, bytes)));
 #pragma unroll
-        for (int i = 0; i < kCopies; ++i) cp_async16(dst + S::kHalf + in_stage(i), v + i * 512, true);
+        for (int i = 0; i < kCopies; ++i)
+          cp_async16(dst + S::kHalf + in_stage(i), v + i * 512, SQ_GUARD(within(v + i * 512, 16, p.c.v, bytes)));
         if (INT8) {
           const int64_t at = p.c.scale_page_stride * one + row;
           if (kTile == 32) {
-            cp_async4(dst + 2 * S::kHalf + lane * 4, p.c.k_scale + at + lane, true);
-            cp_async4(dst + 2 * S::kHalf + 128 + lane * 4, p.c.v_scale + at + lane, true);
+            const bool ok = SQ_GUARD(within(p.c.k_scale + at, 32, p.c.k_scale, p.c.scales()));
+            cp_async4(dst + 2 * S::kHalf + lane * 4, p.c.k_scale + at + lane, ok);
+            cp_async4(dst + 2 * S::kHalf + 128 + lane * 4, p.c.v_scale + at + lane, ok);
           } else {
-            cp_async4(dst + 2 * S::kHalf + lane * 4, (lane < 16 ? p.c.k_scale : p.c.v_scale) + at + (lane & 15), true);
+            cp_async4(dst + 2 * S::kHalf + lane * 4, (lane < 16 ? p.c.k_scale : p.c.v_scale) + at + (lane & 15),
+                      SQ_GUARD(within(p.c.k_scale + at, 16, p.c.k_scale, p.c.scales())));
           }
         }
       } else {
@@ -376,16 +383,18 @@ __global__ void __launch_bounds__(S::WARPS * 32, 1) paged_attention_kernel(const
         for (int i = 0; i < kCopies; ++i) {
           const int r = (i * 32 + lane) / kChunks, ch = (i * 32 + lane) % kChunks;
           const int64_t o = __shfl_sync(0xffffffffu, off, r) + ch * 16;
-          const bool ok = (mask >> r) & 1;
+          const bool ok = ((mask >> r) & 1) && SQ_GUARD(within(k + o, 16, k, p.c.elements() * (INT8 ? 1 : 2)));
           cp_async16(dst + in_stage(i), k + o, ok);
           cp_async16(dst + S::kHalf + in_stage(i), v + o, ok);
         }
         if (INT8) {
           const int64_t sat = valid ? page * p.c.scale_page_stride + row : 0;
           if (kTile == 32 || lane < 16)
-            cp_async4(dst + 2 * S::kHalf + (lane & (kTile - 1)) * 4, p.c.k_scale + sat, valid);
+            cp_async4(dst + 2 * S::kHalf + (lane & (kTile - 1)) * 4, p.c.k_scale + sat,
+                      valid && SQ_GUARD(within(p.c.k_scale + sat, 1, p.c.k_scale, p.c.scales())));
           if (kTile == 32 || lane >= 16)
-            cp_async4(dst + 2 * S::kHalf + (kTile + (lane & (kTile - 1))) * 4, p.c.v_scale + sat, valid);
+            cp_async4(dst + 2 * S::kHalf + (kTile + (lane & (kTile - 1))) * 4, p.c.v_scale + sat,
+                      valid && SQ_GUARD(within(p.c.k_scale + sat, 1, p.c.k_scale, p.c.scales())));
         }
       }
       if (lane == 0) *reinterpret_cast<unsigned*>(ring + stage * S::kStage + S::kStage - 16) = mask;
@@ -662,9 +671,8 @@ __global__ void __launch_bounds__(S::WARPS * 32, 1) paged_attention_kernel(const
               const int d0 = 16 * j + (INT8 ? 2 * g : g), d1 = INT8 ? d0 + 1 : d0 + 8;
               const float v0 = o[nt][j][e], v1 = o[nt][j][e + 2];
               if (!whole) {
-                part[hi * D + d0] = v0;
-                part[hi * D + d1] = v1;
-              } else if (hl < p.group) {
+                if (SQ_GUARD(hi < S::kHeads && d1 < D)) part[hi * D + d0] = v0, part[hi * D + d1] = v1;
+              } else if (hl < p.group && SQ_GUARD(d1 < D && within(out, D, p.out, static_cast<int64_t>(p.B) * p.H * D))) {
                 if (INT8) {
                   *reinterpret_cast<uint32_t*>(out + d0) = pack_bf16(v0 * inv, v1 * inv);
                 } else {
@@ -677,7 +685,7 @@ __global__ void __launch_bounds__(S::WARPS * 32, 1) paged_attention_kernel(const
               if (!whole) {
                 part[S::kHeads * D + hi] = m[nt][e];
                 part[S::kHeads * (D + 1) + hi] = sum;
-              } else if (hl < p.group && p.lse != nullptr) {
+              } else if (hl < p.group && p.lse != nullptr && SQ_GUARD(cur.b < p.B && h < p.H)) {
                 p.lse[static_cast<int64_t>(cur.b) * p.H + h] =
                     sum != 0.0f ? (m[nt][e] + log2f(sum)) * 0.693147180559945309f : -INFINITY;
               }
@@ -700,6 +708,7 @@ __global__ void __launch_bounds__(S::WARPS * 32, 1) paged_attention_kernel(const
   auto write_out = [&](int4 u, int hi, int d, float4 acc, float top, float sum) {
     const int64_t h = static_cast<int64_t>(u.y) * p.H + u.z * p.group + u.w * S::kHeads + hi;
     const float inv = sum != 0.0f ? 1.0f / sum : 0.0f;
+    if (!SQ_GUARD(h >= 0 && h < static_cast<int64_t>(p.B) * p.H && d + 4 <= D)) return;
     *reinterpret_cast<uint2*>(p.out + h * D + d) =
         make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
     if (d == 0 && p.lse != nullptr) p.lse[h] = sum != 0.0f ? (top + log2f(sum)) * 0.693147180559945309f : -INFINITY;
@@ -766,7 +775,7 @@ __global__ void __launch_bounds__(S::WARPS * 32, 1) paged_attention_kernel(const
             add(acc, s_factor[j][turn], *reinterpret_cast<const float4*>(part_of(j) + turn * D + d));
         if (whole)
           write_out(unit, turn, d, acc, top, sum);
-        else
+        else if (SQ_GUARD(within(to + turn * D + d, 4, p.parts, static_cast<int64_t>(kMaxCtas) * 2 * S::kPart)))
           *reinterpret_cast<float4*>(to + turn * D + d) = acc;
       }
       if (!whole && lane == 0) to[S::kHeads * D + turn] = top, to[S::kHeads * (D + 1) + turn] = sum;
@@ -785,7 +794,8 @@ __global__ void __launch_bounds__(S::WARPS * 32, 1) paged_attention_kernel(const
         const int64_t c0 = divide((s_span[at][0] + 1) * ctas - 1, total);
         const int count = static_cast<int>(divide(s_span[at][1] * ctas - 1, total) - c0) + 1;
         unsigned* counter = p.counters + s_unit[at].x;
-        last = atomicAdd(counter, 1u) == static_cast<unsigned>(count - 1);
+        if (SQ_GUARD(c0 >= 0 && c0 + count <= ctas && within(counter, 1, p.counters, static_cast<int64_t>(p.B) * p.H)))
+          last = atomicAdd(counter, 1u) == static_cast<unsigned>(count - 1);
         if (last) *counter = 0;  // as the next call needs it
         s_from[warp] = c0;
         s_count[warp] = count;

@@ -169,7 +169,7 @@ int4_quant_kernel(const uint16_t* __restrict__ W, int64_t N, int64_t K, int64_t 
       if (ASYM) my_z = static_cast<int>(fminf(fmaxf(rintf(__fmul_rn(-low, my_r)), 0.0f), 15.0f));
       if (t % kSpan == 0 && t * 32 < cols && n < N) {
         const int64_t gr = kb * (128 / G) + t / kSpan;
-        if (SQ_GUARD(gr < (K + G - 1) / G)) {
+        if (SQ_GUARD(within(scale + gr * N + n, 1, scale, (K + G - 1) / G * N))) {
           scale[gr * N + n] = __bfloat16_as_ushort(e);
           if (ASYM) zero[gr * N + n] = static_cast<uint8_t>(my_z);
         }
@@ -192,8 +192,9 @@ int4_quant_kernel(const uint16_t* __restrict__ W, int64_t N, int64_t K, int64_t 
           word[a] = word[a] * 16 + code;
         }
       }
-      __stcs(reinterpret_cast<uint4*>(Wp + (rt * Kb + kb) * kTileBytes + (h * 32 + lane) * 16),
-             make_uint4(word[0], word[1], word[2], word[3]));
+      uint8_t* to = Wp + (rt * Kb + kb) * kTileBytes + (h * 32 + lane) * 16;
+      if (SQ_GUARD(within(to, 16, Wp, Nt * Kb * kTileBytes)))
+        __stcs(reinterpret_cast<uint4*>(to), make_uint4(word[0], word[1], word[2], word[3]));
     }
   }
   asm volatile("cp.async.wait_group 0;" ::: "memory");
@@ -244,7 +245,8 @@ int4_dequant_kernel(const uint8_t* __restrict__ Wp, const uint16_t* __restrict__
           w[u] = __shfl_sync(0xffffffffu, word[a], (lane & ~3) | u) >> (4 * t);
           w[u] = mul_bf16x2(sub_bf16x2((w[u] & 0x000F000Fu) | 0x43004300u, zp), e2);
         }
-        if (n < N && k < K) __stcs(reinterpret_cast<uint4*>(out + n * K + k), make_uint4(w[0], w[1], w[2], w[3]));
+        if (n < N && k < K && SQ_GUARD(within(out + n * K + k, 8, out, N * K)))
+          __stcs(reinterpret_cast<uint4*>(out + n * K + k), make_uint4(w[0], w[1], w[2], w[3]));
       }
     }
   }
@@ -333,10 +335,11 @@ __host__ __device__ constexpr int team_ring_at(int tokens, int col_bytes, int cp
 // NT: columns / 8; column 3 m + d is byte d (0 the highest) of token m.
 template <int NT, int G, bool ASYM>
 __global__ void __launch_bounds__(kTeamWarps * 32, 1) int4_team_kernel(const TeamParams q) {
-  constexpr int kGroups = 256 / G, kSlot = team_slot_bytes<G, ASYM>(), kThreads = kTeamWarps * 32, kCols = NT * 8;
+  constexpr int kGroups = 256 / G, kSlot = team_slot_bytes<G, ASYM>(), kCols = NT * 8;
   constexpr int kScales = 2 * kTileBytes, kZeros = kScales + kGroups * 32;
   const LinearParams& p = q.p;
-  extern __shared__ __align__(128) uint8_t smem[];
+  extern __shared__ __align__(128) uint8_t aligned_smem[];
+  uint8_t* smem = aligned_smem;
   __shared__ uint32_t s_top[kTeamWarps];
   __shared__ float s_mul[kTeamTokens][2], s_back[kTeamTokens][2];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -385,16 +388,18 @@ __global__ void __launch_bounds__(kTeamWarps * 32, 1) int4_team_kernel(const Tea
     if (load_rt < Nt) {
       const uint32_t dst = ring32 + slot * kSlot;
       const bool second = 2 * load_kp + 1 < p.Kb;
-      cp_async<16>(dst + lane * 16, load_src, true);
-      cp_async<16>(dst + 512 + lane * 16, load_src + 512, true);
-      cp_async<16>(dst + 1024 + lane * 16, load_src + (second ? 1024 : 0), second);
-      cp_async<16>(dst + 1536 + lane * 16, load_src + (second ? 1536 : 0), second);
+      const bool codes = SQ_GUARD(
+          within(load_src, second ? 1552 : 528, p.Wp, static_cast<int64_t>(Nt) * p.Kb * kTileBytes));
+      cp_async<16>(dst + lane * 16, load_src, codes);
+      cp_async<16>(dst + 512 + lane * 16, load_src + 512, codes);
+      cp_async<16>(dst + 1024 + lane * 16, load_src + (second ? 1024 : 0), second && codes);
+      cp_async<16>(dst + 1536 + lane * 16, load_src + (second ? 1536 : 0), second && codes);
       if (lane < kScaleLanes) {
-        const bool in = load_kp < e_end;
+        const bool in = load_kp < e_end && SQ_GUARD(within(e_src, kScaleBytes / 2, p.scale, p.groups * p.N));
         cp_async<kScaleBytes>(dst + kScales + lane * kScaleBytes, in ? e_src : p.scale, in);
       }
       if (ASYM && lane < 4 * kGroups) {
-        const bool in = load_kp < z_end;
+        const bool in = load_kp < z_end && SQ_GUARD(within(z_src, 4, p.zero, p.groups * p.N));
         cp_async<4>(dst + kZeros + lane * 4, in ? z_src : p.zero, in);
       }
       load_kp += q.kw;
@@ -587,7 +592,8 @@ __global__ void __launch_bounds__(kTeamWarps * 32, 1) int4_team_kernel(const Tea
         y0 += bf16_lo(b);
         y1 += bf16_hi(b);
       }
-      *reinterpret_cast<__nv_bfloat162*>(p.Y + m * p.N + n) = __floats2bfloat162_rn(y0, y1);
+      if (SQ_GUARD(within(p.Y + m * p.N + n, 2, p.Y, p.M * p.N)))
+        *reinterpret_cast<__nv_bfloat162*>(p.Y + m * p.N + n) = __floats2bfloat162_rn(y0, y1);
     }
     side ^= q.rounds > 1;
   }
@@ -728,16 +734,18 @@ __global__ void __launch_bounds__(kTeamWarps * 32, 1) int4_wide_kernel(const Wid
     if (load_rt < Nt) {
       const uint32_t dst = ring32 + slot * kSlot;
       const bool second = 2 * load_kp + 1 < p.Kb;
-      cp_async<16>(dst + lane * 16, load_src, true);
-      cp_async<16>(dst + 512 + lane * 16, load_src + 512, true);
-      cp_async<16>(dst + 1024 + lane * 16, load_src + (second ? 1024 : 0), second);
-      cp_async<16>(dst + 1536 + lane * 16, load_src + (second ? 1536 : 0), second);
+      const bool codes = SQ_GUARD(
+          within(load_src, second ? 1552 : 528, p.Wp, static_cast<int64_t>(Nt) * p.Kb * kTileBytes));
+      cp_async<16>(dst + lane * 16, load_src, codes);
+      cp_async<16>(dst + 512 + lane * 16, load_src + 512, codes);
+      cp_async<16>(dst + 1024 + lane * 16, load_src + (second ? 1024 : 0), second && codes);
+      cp_async<16>(dst + 1536 + lane * 16, load_src + (second ? 1536 : 0), second && codes);
       if (lane < kScaleLanes) {
-        const bool in = load_kp < e_end;
+        const bool in = load_kp < e_end && SQ_GUARD(within(e_src, kScaleBytes / 2, p.scale, p.groups * p.N));
         cp_async<kScaleBytes>(dst + kScales + lane * kScaleBytes, in ? e_src : p.scale, in);
       }
       if (ASYM && lane < 4 * kGroups) {
-        const bool in = load_kp < z_end;
+        const bool in = load_kp < z_end && SQ_GUARD(within(z_src, 4, p.zero, p.groups * p.N));
         cp_async<4>(dst + kZeros + lane * 4, in ? z_src : p.zero, in);
       }
       load_kp += q.kw;
@@ -760,7 +768,8 @@ __global__ void __launch_bounds__(kTeamWarps * 32, 1) int4_wide_kernel(const Wid
     for (int m = warp; m < p.M; m += W)
       for (int i = lane; i < cols; i += 32) {
         const bool in = k0 + i * 8 < p.K;
-        cp_async<16>(dst + m * x_row + i * 16, p.X + m * p.ldx + (in ? k0 + i * 8 : 0), in);
+        cp_async<16>(dst + m * x_row + i * 16, p.X + m * p.ldx + (in ? k0 + i * 8 : 0),
+                     in && SQ_GUARD(k0 >= 0 && k0 + i * 8 + 8 <= p.K));
       }
     asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(smem_u32(&s_there[buffer])) : "memory");
   };
@@ -899,7 +908,8 @@ __global__ void __launch_bounds__(kTeamWarps * 32, 1) int4_wide_kernel(const Wid
         y0 += bf16_lo(b);
         y1 += bf16_hi(b);
       }
-      *reinterpret_cast<__nv_bfloat162*>(p.Y + m * p.N + row) = __floats2bfloat162_rn(y0, y1);
+      if (SQ_GUARD(within(p.Y + m * p.N + row, 2, p.Y, p.M * p.N)))
+        *reinterpret_cast<__nv_bfloat162*>(p.Y + m * p.N + row) = __floats2bfloat162_rn(y0, y1);
     }
     if (q.split > 1) cluster_sync();  // the sums are read: they may be overwritten, or the CTA may end
     rt += step;

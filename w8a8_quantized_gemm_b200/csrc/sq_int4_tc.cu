@@ -301,15 +301,19 @@ int4_tc_kernel(const __grid_constant__ CUtensorMap x_map, const TcParams p) {
       if (load_rb < p.row_blocks) {
         const uint32_t at = ring + slot * C::kCodeSlot;
         const uint32_t dst = at + lane / 4 * kCodeRow + lane % 4 * 16;  // row lane / 4, then 8 on
-        cp_async<16>(dst, src);
-        cp_async<16>(dst + 8 * kCodeRow, src + 512);
-        cp_async<16>(dst + 16 * kCodeRow, src + second);
-        cp_async<16>(dst + 24 * kCodeRow, src + second + 512);
+        if (SQ_GUARD(within(src, second + 528, p.Wp, Nt * tile_bytes))) {
+          cp_async<16>(dst, src);
+          cp_async<16>(dst + 8 * kCodeRow, src + 512);
+          cp_async<16>(dst + 16 * kCodeRow, src + second);
+          cp_async<16>(dst + 24 * kCodeRow, src + second + 512);
+        }
         const int gr = (b0 + load_b) * kPer;
-        if (lane < kPer * kELanes)
+        if (lane < kPer * kELanes &&
+            SQ_GUARD(within(e_src + min(gr + e_group, p.groups - 1) * p.N, kE / 2, p.scale, p.groups * p.N)))
           cp_async<kE>(at + C::kScales + lane * kE, e_src + min(gr + e_group, p.groups - 1) * p.N,
                        gr + e_group < p.groups);
-        if (ASYM && lane < kPer * 8)
+        if (ASYM && lane < kPer * 8 &&
+            SQ_GUARD(within(z_src + min(gr + z_group, p.groups - 1) * p.N, 4, p.zero, p.groups * p.N)))
           cp_async<4>(at + C::kZeros + lane * 4, z_src + min(gr + z_group, p.groups - 1) * p.N);
         src += C::kWg * kTileBytes;
         load_b += C::kWg;
@@ -470,7 +474,7 @@ int4_tc_kernel(const __grid_constant__ CUtensorMap x_map, const TcParams p) {
 #pragma unroll
         for (int j = 0; j < kPerWarp; ++j) {
           const int m = warp + j * kWarps;
-          if (m < p.M)
+          if (m < p.M && SQ_GUARD(within(p.Y + m * p.N + n, 2, p.Y, p.M * p.N)))
             *reinterpret_cast<__nv_bfloat162*>(p.Y + m * p.N + n) =
                 __floats2bfloat162_rn(y[j].x + bias.x, y[j].y + bias.y);
         }

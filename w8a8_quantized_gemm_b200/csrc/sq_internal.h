@@ -86,6 +86,7 @@ inline int cluster_slots(int sms, int size) {
 // constant true and costs nothing.
 #ifdef SQ_DEBUG_GUARDS
 extern __device__ unsigned int g_status_word;
+extern __device__ long long g_guard_margin;  // elements, 0 but in tests of the guards
 __device__ __forceinline__ bool guard_ok(bool c) {
   if (!c) atomicOr(&g_status_word, kErrBounds);
   return c;
@@ -94,6 +95,16 @@ __device__ __forceinline__ bool guard_ok(bool c) {
 #else
 #define SQ_GUARD(c) true
 #endif
+
+// Whether p[0 .. n) lies in the `total` elements from `base` on (guard conditions).
+template <typename T>
+__device__ __forceinline__ bool within(const T* p, int64_t n, const void* base, int64_t total) {
+  const T* first = static_cast<const T*>(base);
+#ifdef SQ_DEBUG_GUARDS
+  total -= g_guard_margin;
+#endif
+  return p >= first && p + n <= first + total;
+}
 
 __device__ __forceinline__ void griddep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void griddep_launch_dependents() {
@@ -229,6 +240,15 @@ struct KvView {  // a checked sq_kv_cache, as the kernels take it
   int64_t num_pages = 0, page_stride = 0, scale_page_stride = 0;
   int heads = 0, head_dim = 0, page_shift = 0;
   bool int8 = false;
+#ifdef __CUDACC__
+  // elements of k (v), and scales, from the first page's first to the last page's last (guard conditions)
+  __device__ __forceinline__ int64_t elements() const {
+    return (num_pages - 1) * page_stride + (static_cast<int64_t>(heads) << page_shift) * head_dim;
+  }
+  __device__ __forceinline__ int64_t scales() const {
+    return (num_pages - 1) * scale_page_stride + (static_cast<int64_t>(heads) << page_shift);
+  }
+#endif
 };
 struct RopeAppendArgs {
   const uint16_t *q = nullptr, *k = nullptr, *v = nullptr;

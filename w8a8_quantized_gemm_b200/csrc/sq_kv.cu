@@ -78,7 +78,7 @@ rope_kv_append_kernel(const uint16_t* q, int64_t ldq, const uint16_t* __restrict
   float cs[8], sn[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) cs[j] = 1.0f, sn[j] = 0.0f;
-  if (turn) {
+  if (turn && SQ_GUARD(within(cos_t + pos * (rot / 2) + 8 * i, 8, cos_t, max_pos * (rot / 2)))) {
     const float4* cp = reinterpret_cast<const float4*>(cos_t + pos * (rot / 2) + 8 * i);
     const float4* sp = reinterpret_cast<const float4*>(sin_t + pos * (rot / 2) + 8 * i);
     const float4 c0 = __ldg(cp), c1 = __ldg(cp + 1), s0 = __ldg(sp), s1 = __ldg(sp + 1);
@@ -106,7 +106,7 @@ rope_kv_append_kernel(const uint16_t* q, int64_t ldq, const uint16_t* __restrict
       uint16_t* dst = is_q ? q_out + (tok * H + head) * D
                            : static_cast<uint16_t*>(is_v ? c.v : c.k) + page * c.page_stride +
                                  (static_cast<int64_t>(head) << c.page_shift) * D + static_cast<int64_t>(off) * D;
-      if (on) {
+      if (on && SQ_GUARD(p1 + 8 <= D && within(dst, D, is_q ? q_out : is_v ? c.v : c.k, is_q ? T * H * D : c.elements()))) {
         *reinterpret_cast<uint4*>(dst + p0) = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]),
                                                          pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
         *reinterpret_cast<uint4*>(dst + p1) = make_uint4(pack_bf16(x[8], x[9]), pack_bf16(x[10], x[11]),
@@ -120,7 +120,7 @@ rope_kv_append_kernel(const uint16_t* q, int64_t ldq, const uint16_t* __restrict
       const float r = a > 0.0f ? fminf(__fdiv_rn(127.0f, a), FLT_MAX) : 0.0f;
       const int64_t at = (static_cast<int64_t>(head) << c.page_shift) + off;
       int8_t* dst = static_cast<int8_t*>(is_v ? c.v : c.k) + page * c.page_stride + at * D;
-      if (on) {
+      if (on && SQ_GUARD(p1 + 8 <= D && within(dst, D, is_v ? c.v : c.k, c.elements()))) {
         int e[16];
 #pragma unroll
         for (int j = 0; j < 16; ++j) e[j] = __float2int_rn(fminf(fmaxf(__fmul_rn(x[j], r), -128.0f), 127.0f));
@@ -129,7 +129,8 @@ rope_kv_append_kernel(const uint16_t* q, int64_t ldq, const uint16_t* __restrict
         *reinterpret_cast<uint2*>(dst + p1) =
             make_uint2(sq::rows::pack4(e[8], e[9], e[10], e[11]), sq::rows::pack4(e[12], e[13], e[14], e[15]));
       }
-      if (i == 0) (is_v ? c.v_scale : c.k_scale)[page * c.scale_page_stride + at] = __fdiv_rn(a, 127.0f);
+      float* to = (is_v ? c.v_scale : c.k_scale) + page * c.scale_page_stride + at;
+      if (i == 0 && SQ_GUARD(within(to, 1, is_v ? c.v_scale : c.k_scale, c.scales()))) *to = __fdiv_rn(a, 127.0f);
     }
   }
 }

@@ -62,6 +62,7 @@ _SIGS = {
     "sq_sync_status": ([_p], _i32),
     "sq_version": ([], C.c_char_p),
     "sq_debug_arm_fault": ([_i32, C.c_uint64], None),
+    "sq_debug_guard_margin": ([_i64], _i32),
     "sq_debug_gemm_plan": ([_i64, _i64, _i64, _i32, _p], _i32),
     "sq_kernel_launch_count": ([], C.c_uint64),
 }
@@ -545,6 +546,10 @@ def sq_sync_status(stream=None):
 
 def sq_kernel_launch_count() -> int:
     return int(_lib.sq_kernel_launch_count())
+
+
+def sq_debug_guard_margin(margin: int):
+    _check(_lib.sq_debug_guard_margin(int(margin)))
 
 
 def sq_debug_arm_fault(fault: int, wait_limit_ns: int = 0):
