@@ -464,7 +464,10 @@ SQ_API sq_status sq_rope_kv_append(const void* q_bf16, int64_t ldq, const void* 
  *   out[b,h] = sum_t p_t v_t,  p = softmax_t( scale * (q[b,h] . k_t) ),
  *   over max(0, seq_lens[b] - window) <= t < seq_lens[b]   (window == 0: the whole sequence)
  *   lse[b,h] = log sum_t exp( scale * (q[b,h] . k_t) )
- * with fp32 scores, softmax statistics and sums, one rounding of out to bf16. For an int8 cache
+ * with fp32 scores, softmax statistics and sums, one rounding of out to bf16. In the product with v a
+ * probability is the sum of two bf16 numbers (off by at most 2^-17 of itself; bf16 cache), or,
+ * times its value scale, of two fp16 numbers (off by 2^-22 of itself, and by 2^-38 of the largest
+ * such product of its head; int8 cache). For an int8 cache
  * the queries are integers of 23 bits and a power of two (exact down to 2^-14 of a head's
  * largest element, off by at most 2^-22 of it below, where scale times that element is at least
  * 2^-104), so that the scores' sums are exact;

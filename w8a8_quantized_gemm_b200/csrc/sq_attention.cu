@@ -3,8 +3,11 @@
 // "SmoothQuant量化实战" §5.2 (KV-cache INT8 with per-token, per-head scales).
 //
 // Every key and value is read once for all query heads of its key head: at 4 to 16 flops a
-// byte the call is bound by the bytes of the cache where it is long (64 sequences of up to 8192,
-// 8 key heads of 128, 64 query heads: 129 us, 5.4 TB/s of int8 cache) and by the chain of
+// byte the call is bound by the bytes of the cache, behind the latency of two warps' instructions a
+// scheduler, where it is long (64 sequences of up to 8192, 8 key heads of 128, 64 query heads: 126
+// us, 5.5 TB/s of int8 cache, for some milliseconds at 1965 MHz; 147 us, 4.7 TB/s, for seconds,
+// which the power limit brings to 1700 MHz; inputs that change from call to call take the same, and
+// full lengths 5.7 TB/s of 1109 MB at 1965 MHz) and by the chain of
 // dependent steps where it is short (one such sequence, 32 query heads: 13.3 us: page table,
 // tile and queries 4, scores and values of two tiles 3, the joins 4). The work is cut into
 // tiles of 16 or 32 tokens of one key head; all tiles, in the order (sequence, key head, token),
@@ -28,8 +31,9 @@
 //     (elements down to 2^-14 of the head's largest are exact, smaller ones off by at most 2^-22 of it);
 //   - values become fp16 exactly: (byte ^ 0x80) + 1024 has the byte's bits as its mantissa, one
 //     logic operation, and 1152 less is the code.
-// The probabilities enter as a high and a low 16-bit part, so that the rounding of out to bf16
-// is the only one that counts. For an int8 cache they carry the token's value scale vs: what is
+// The probabilities enter as a high and a low 16-bit part (two bf16 numbers carry 16 bits, two fp16
+// numbers 22), so that the rounding of out to bf16 is the only one that counts; their sum is of
+// the whole ones. For an int8 cache they carry the token's value scale vs: what is
 // subtracted is then the running maximum of s + log2(vs), less kShift, which keeps the products
 // within [0, 2^kShift], in fp16's range whatever the scales, and the exponentials alone, whose sum
 // is the softmax's, in fp32's: from 2^(kShift - 121) (bf16 values are below 2^128, their scales below

@@ -74,7 +74,7 @@ __device__ __forceinline__ void cp_async(uint32_t dst, const void* src, bool val
 // element): products are packed pairs, a code's rounding is an addition of 1.5 * 2^23 (the
 // product is below 23 in magnitude, even where a subnormal scale is half a step off), and its
 // zero point and clamp one packed 16-bit operation per pair. 28672 x 8192 with zero points, groups
-// of 64: 126 us, 4.8 TB/s; 4096 x 4096, groups of 128: 11 us.
+// of 64: 123 us, 4.9 TB/s; 4096 x 4096, groups of 128: 11 us.
 constexpr int kQuantRing = 3, kQuantRow = 256 + 16, kQuantSlot = 16 * kQuantRow;
 
 template <int G, bool ASYM>
@@ -296,7 +296,7 @@ struct LinearParams {
 // teams of the grid in turn); within a tile the warps take pairs of 128-column blocks in turn.
 // Every lane brings its own fragments into its warp's ring with asynchronous copies, across tiles
 // and with nothing to wait for but the copies. The team meets once a tile to add its warps' sums
-// up in order. One token: 28672 x 8192 27 us (4.5 TB/s), 8192 x 28672 32 us, 4096 x 4096 5.2 us (launch,
+// up in order. One token: 28672 x 8192 27 us (4.5 TB/s), 8192 x 8192 10.4 us, 4096 x 4096 4.9 us (launch,
 // first bytes and join).
 constexpr int kTeamWarps = 16;  // of a CTA, one CTA per SM
 constexpr int kTeamTokens = 4;
@@ -631,8 +631,8 @@ bool team_fits(TeamParams* q, int nt) {
 // its team's warps need for it, about a tenth of the SM's bandwidth each; teams with more than
 // one tile wait for their slowest warp at each. Among equals the larger team, which is done sooner
 // with a small weight. Measured, us, one token, teams of 2 / 4 / 8 / 16 warps: 4096 x 4096
-// 5.3 / 5.0 / 5.1 / 5.7 (8 taken), 11008 x 4096 7.7 / 8.4 / 8.6 / 10.4 (3 taken, 7.8),
-// 28672 x 8192 28.3 / 27.6 / 27.9 / 33.6 (1 taken, 29.5: 6% off the best).
+// 5.3 / 4.8 / 4.9 / 5.6 (8 taken), 11008 x 4096 7.1 / 7.5 / 7.8 / 9.6 (3 taken, 6.9),
+// 28672 x 8192 27.0 / 26.7 / 26.2 / 31.7 (1 taken, 26.9: 3% off the best).
 int team_warps(int64_t Nt, int sms, int Kp) {
   const int64_t tiles = (Nt + sms - 1) / sms;  // of an SM
   int best = 1;
@@ -664,9 +664,10 @@ cudaError_t launch_team(const TeamParams& q, int sms, cudaStream_t stream) {
 // total. Teams and rings as above; the activations come in chunks of `cp` pairs of column blocks
 // for all teams of a CTA, one chunk ahead, and where there are too few row tiles for that the
 // CTAs of a cluster share the columns and add their sums up, in order, through distributed
-// shared memory. Bound by the unpacking: 16 x 28672 x 8192 55 us (2.3 TB/s), half of the integer
-// pipe and 0.55 instructions a cycle with 12 or 13 of the 16 warps at work; 8 x 28672 x 8192 43,
-// 5 x 11008 x 4096 12.2.
+// shared memory. 16 x 28672 x 8192 55 us (2.3 TB/s), 8 x 28672 x 8192 43.5, 5 x 11008 x 4096 12.2:
+// no unit is full (integer pipe 51%, 0.55 instructions a cycle); bound by waiting, most of it at the
+// block barrier of each chunk, with 12 or 13 of the 16 warps at work where an SM has as many tiles,
+// and then for instructions before.
 struct WideParams {
   LinearParams p;
   int split;    // CTAs of a cluster
@@ -983,9 +984,9 @@ cudaError_t launch_linear(const LinearParams& p, unsigned int* status, cudaStrea
   cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   // Every CTA of the int8 kernel makes bytes of all activations, which takes enough row tiles to pay.
   // Measured (us, int8 / bf16 kernel) at 0.2, 1, 1.4, 3.5, 4.6 and 12 tiles an SM (448 x 13376, 2472 x
-  // 22560, 3232 x 12112, 8192 x 8192, 11008 x 4096, 28672 x 8192): 1 token 8.1 / 7.0, 19 / 16,
-  // 9.9 / 10.2, 13 / 16, 7.9 / 9.8, 30 / 43; 4 tokens 16 / 7.5, 34 / 17, 16 / 11, 20 / 17, 10 / 11,
-  // 38 / 45.
+  // 22560, 3232 x 12112, 8192 x 8192, 11008 x 4096, 28672 x 8192): 1 token 7.9 / 7.1, 16 / 15,
+  // 9.3 / 10.4, 10.4 / 14.6, 7.6 / 10.0, 26 / 41; 4 tokens 16 / 7.6, 32 / 16, 17 / 12, 18 / 16, 10.7 / 11.5,
+  // 35 / 43.
   const int64_t Nt = (p.N + 15) / 16;
   if (p.M <= kTeamTokens && 5 * Nt >= (p.M <= 2 ? 6 : 20) * static_cast<int64_t>(sms)) {
     TeamParams q;

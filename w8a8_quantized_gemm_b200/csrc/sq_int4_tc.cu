@@ -2,9 +2,11 @@
 //   Y[m,n] = sum_k X[m,k] * (code[n,k] - zero[g,n]) * scale[g,n] + bias[n]
 //
 // The weight rows are the 128 rows of the instructions, the tokens (up to 64) their columns, so
-// that every code is made a bf16 number once for all tokens. That bounds the call (half of the
-// time a block takes; 64 x 28672 x 8192 68 us, 64 x 8192 x 8192 23.1, of which 4 are the row
-// block's end: the bytes alone would take 19 and 6, the products 19 and 5). Warpgroups take the
+// that every code is made a bf16 number once for all tokens. 64 x 28672 x 8192 69 us, 64 x 8192 x
+// 8192 22.6, of which 4 are the row block's end (the bytes alone would take 20 and 6, the products
+// 19 and 5): no unit is full (integer pipe 46%, tensor pipe 24%, half of the issue slots). Bound by
+// latency: two warps a scheduler each convert, store, wait for the products, read back and add in
+// turn, half of a block's time in the conversion. Warpgroups take the
 // 128-column blocks of a row block in turn. A thread
 // owns a weight row: its 64 bytes of codes (contiguous in the tiled layout) come by asynchronous
 // copies several blocks ahead, become code - zero exactly (128 + code, minus 128 + zero) in the
