@@ -187,3 +187,21 @@ def test_on_a_side_stream_and_in_a_graph():
     graph.replay()
     sq.sq_sync_status()
     _check(Yg, host_bits(X), values, None)
+
+
+@pytest.mark.parametrize("M", [1, 4])
+@pytest.mark.parametrize("place", [0, -1])
+def test_nonfinite_scales_stay_in_their_rows(M, place):
+    N, K, group = _rows(M, 8), 144, 32
+    rng = np.random.default_rng(M)
+    scale = oracle.float_to_bf16(rng.uniform(0.002, 0.02, (5, N)).astype(np.float32))
+    zero, codes = rng.integers(0, 16, (5, N), dtype=np.uint8), rng.integers(0, 16, (N, K), dtype=np.uint8)
+    scale[place, [3, N - 1]], scale[place, 20] = 0x7F80, 0x7FC0  # infinity, NaN
+    X = wl.f32_to_bf16_bits(rng.normal(0, 1, (M, K)).astype(np.float32))
+    weight = (torch.from_numpy(osv.int4_pack(codes)).cuda(), dev_bf16(scale), torch.from_numpy(zero).cuda())
+    Y = _run(dev_bf16(X), weight, group, None, N)
+    sq.sq_sync_status()
+    assert not bool(torch.isfinite(Y[:, [3, 20, N - 1]]).any())
+    rest = np.setdiff1d(np.arange(N), [3, 20, N - 1])
+    values = osv.int4_values(codes[rest], scale[:, rest], zero[:, rest], group)
+    _check(Y[:, torch.from_numpy(rest).cuda()].contiguous(), X, values, None)
